@@ -20,13 +20,15 @@ from ._lib import (FP8Q_ERR_ALIGN, FP8Q_ERR_ARCH, FP8Q_ERR_ARG, FP8Q_ERR_LAUNCH,
                    FP8Q_ERR_NOT_POW2, FP8Q_ERR_RANGE, FP8Q_ERR_SHAPE, FP8Q_ERR_TIMEOUT, FP8Q_OK, FP8Q_SCALE_E8M0, FP8Q_SCALE_F32,
                    Fp8qError)
 
+import contextlib
 import ctypes
 
 __all__ = ["quant_weight_block", "rmsnorm_quant_token", "add_rmsnorm_quant", "gemm_w8a8_block",
            "gemm_w8a8_block_splitk", "gemm_splitk_workspace_bytes", "splitk_workspace",
            "quant_rowwise", "gemm_w8a8_rowwise", "silu_mul_quant", "inverse_rope_quant",
            "gemm_w8a8_block_diag", "gemm_w8a8_mx", "qkv_scales", "kv_cache_write", "WeightBatch",
-           "selftest_timeout", "attention_decode", "attention_decode_workspace_bytes",
+           "paged_batch_tables", "tree_mask", "attention_tree", "attention_tree_workspace_bytes",
+           "kv_cache_accept", "selftest_timeout", "attention_decode", "attention_decode_workspace_bytes",
            "grouped_gemm_w8a8_block", "check_device_error", "Fp8qError", "FP8Q_SCALE_F32",
            "FP8Q_SCALE_E8M0", "scale_format"]
 
@@ -211,6 +213,168 @@ def attention_decode(q_codes: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
         block_size, max_seq_len, float(sm_scale), _ptr(o), _ld(o), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream))
     _lib.check(st, "fp8q_attention_decode")
+    return o
+
+
+def _expect(device, **tensors):
+    """Checks of the speculative-decoding calls: each value is (tensor, dtype, shape), a shape entry
+    of None standing for any size; contiguous CUDA tensors, all on `device`."""
+    for name, (t, dtype, shape) in tensors.items():
+        if t.device != device or t.dtype != dtype or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}")
+        if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+            raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+
+
+@contextlib.contextmanager
+def _launch(device, stream):
+    """Makes the tensors' device and the launch stream current, so that what is allocated inside
+    belongs to that stream; yields the stream's handle."""
+    if device.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, not {device}")
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    with torch.cuda.stream(stream):
+        yield stream.cuda_stream
+
+
+def paged_batch_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
+                       free_blocks: torch.Tensor, free_count: torch.Tensor, block_size: int,
+                       max_tokens: int, out=None, stream=None):
+    """Block tables and slot maps from request lengths (fp8q_paged_batch_tables): int32 [B] cached
+    and added positions, block_table int32 [B, max_blocks] (extended in place), the stack of free
+    block ids int32 [num_free] and its height int32 [1] -> (cu_tokens int32 [B + 1], seq_lens
+    int32 [B], slots int64 [max_tokens], positions int64 [max_tokens], free_left int32 [1]).
+    `out`: those five, to be written."""
+    dev, B = ctx_lens.device, ctx_lens.shape[0]
+    i32, i64 = torch.int32, torch.int64
+    _expect(dev, ctx_lens=(ctx_lens, i32, (B,)), new_lens=(new_lens, i32, (B,)),
+            block_table=(block_table, i32, (B, None)), free_blocks=(free_blocks, i32, (None,)),
+            free_count=(free_count, i32, (1,)))
+    with _launch(dev, stream) as st:
+        if out is None:
+            out = (torch.empty(B + 1, dtype=i32, device=dev), torch.empty(B, dtype=i32, device=dev),
+                   torch.empty(max_tokens, dtype=i64, device=dev),
+                   torch.empty(max_tokens, dtype=i64, device=dev),
+                   torch.empty(1, dtype=i32, device=dev))
+        else:
+            _expect(dev, cu_tokens=(out[0], i32, (B + 1,)), seq_lens=(out[1], i32, (B,)),
+                    slots=(out[2], i64, (max_tokens,)), positions=(out[3], i64, (max_tokens,)),
+                    free_left=(out[4], i32, (1,)))
+        cu, lens, slots, positions, left = out
+        rc = _lib.lib().fp8q_paged_batch_tables(
+            _ptr(ctx_lens), _ptr(new_lens), B, int(block_size), _ptr(block_table),
+            block_table.shape[1], _ptr(free_blocks), free_blocks.shape[0], _ptr(free_count),
+            _ptr(left), int(max_tokens), _ptr(cu), _ptr(lens), _ptr(slots), _ptr(positions), st)
+    _lib.check(rc, "fp8q_paged_batch_tables")
+    return cu, lens, slots, positions, left
+
+
+def tree_mask(parents: torch.Tensor, cu_nodes: torch.Tensor, max_nodes: int, ctx_lens=None,
+              out_mask=None, out_positions=None, stream=None):
+    """Ancestor masks of drafted trees (fp8q_tree_mask): parents int32 [total] (index within the
+    sequence, -1 for a child of the context), offsets int32 [B + 1], at most max_nodes nodes per
+    sequence -> (mask int64 [total, ceil(max_nodes / 64)], positions int64 [total] = ctx + depth)."""
+    dev, total, B = parents.device, parents.shape[0], cu_nodes.shape[0] - 1
+    words = (int(max_nodes) + 63) // 64
+    _expect(dev, parents=(parents, torch.int32, (total,)),
+            cu_nodes=(cu_nodes, torch.int32, (B + 1,)))
+    if ctx_lens is not None:
+        _expect(dev, ctx_lens=(ctx_lens, torch.int32, (B,)))
+    with _launch(dev, stream) as st:
+        mask = (torch.empty((total, words), dtype=torch.int64, device=dev) if out_mask is None
+                else out_mask)
+        pos = (torch.empty(total, dtype=torch.int64, device=dev) if out_positions is None
+               else out_positions)
+        if (mask.dtype != torch.int64 or mask.device != dev or mask.shape[0] != total
+                or mask.shape[1] < words):
+            raise ValueError(f"out_mask must be int64 [{total}, >= {words}] on {dev}")
+        _expect(dev, out_positions=(pos, torch.int64, (total,)))
+        rc = _lib.lib().fp8q_tree_mask(_ptr(parents), _ptr(cu_nodes), _ptr(ctx_lens), B, total,
+                                       int(max_nodes), _ptr(mask), _ld(mask), _ptr(pos), st)
+    _lib.check(rc, "fp8q_tree_mask")
+    return mask, pos
+
+
+def attention_tree_workspace_bytes(B: int, Hq: int, Hkv: int, D: int, max_nodes: int,
+                                   max_seq_len: int) -> int:
+    b = ctypes.c_int64(0)
+    st = _lib.lib().fp8q_attention_tree_workspace_bytes(B, Hq, Hkv, D, max_nodes, max_seq_len,
+                                                        ctypes.byref(b))
+    _lib.check(st, "fp8q_attention_tree_workspace_bytes")
+    return b.value
+
+
+def attention_tree(q_codes: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   scale3: torch.Tensor, block_table: torch.Tensor, ctx_lens: torch.Tensor,
+                   cu_nodes: torch.Tensor, mask, Hq: int, Hkv: int, block_size: int,
+                   max_nodes: int, max_seq_len: int, sm_scale=None, workspace=None, out=None,
+                   stream=None):
+    """Attention of drafted trees over the FP8 KV cache (fp8q_attention_tree): q_codes uint8
+    [total, Hq*D], caches uint8 [slots, Hkv*D], scale3 fp32 [3], block_table int32 [B, max blocks],
+    ctx_lens int32 [B], cu_nodes int32 [B + 1], mask int64 [total, words] (from tree_mask; None: each
+    node sees all nodes before it) -> bf16 [total, Hq*D].  sm_scale defaults to 1/sqrt(D)."""
+    dev, total, B = q_codes.device, q_codes.shape[0], ctx_lens.shape[0]
+    D = k_cache.shape[-1] // Hkv
+    slots = k_cache.shape[0]
+    _expect(dev, k_cache=(k_cache, torch.uint8, (slots, Hkv * D)),
+            v_cache=(v_cache, torch.uint8, (slots, Hkv * D)), scale3=(scale3, torch.float32, (3,)),
+            block_table=(block_table, torch.int32, (B, None)),
+            ctx_lens=(ctx_lens, torch.int32, (B,)), cu_nodes=(cu_nodes, torch.int32, (B + 1,)))
+    if q_codes.dtype != torch.uint8 or q_codes.shape[1] != Hq * D:
+        raise ValueError(f"q_codes must be uint8 [total, {Hq * D}]")
+    words = (int(max_nodes) + 63) // 64
+    if mask is not None and (mask.dtype != torch.int64 or mask.device != dev
+                             or mask.shape[0] != total or mask.shape[1] < words):
+        raise ValueError(f"mask must be int64 [{total}, >= {words}] on {dev}")
+    if sm_scale is None:
+        sm_scale = 1.0 / float(np.sqrt(D))
+    with _launch(dev, stream) as st:
+        if workspace is None:
+            n = attention_tree_workspace_bytes(B, Hq, Hkv, D, max_nodes, max_seq_len)
+            workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+        o = torch.empty((total, Hq * D), dtype=torch.bfloat16, device=dev) if out is None else out
+        if o.dtype != torch.bfloat16 or o.device != dev or tuple(o.shape) != (total, Hq * D):
+            raise ValueError(f"out must be bf16 [{total}, {Hq * D}] on {dev}")
+        rc = _lib.lib().fp8q_attention_tree(
+            _ptr(q_codes), _ld(q_codes), _ptr(k_cache), _ptr(v_cache), slots, _ptr(scale3),
+            _ptr(block_table), block_table.shape[1], _ptr(ctx_lens), _ptr(cu_nodes), _ptr(mask),
+            _ld(mask) if mask is not None else 0, B, total, Hq, Hkv, D, int(block_size),
+            int(max_nodes), int(max_seq_len), float(sm_scale), _ptr(o), _ld(o), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), st)
+    _lib.check(rc, "fp8q_attention_tree")
+    return o
+
+
+def kv_cache_accept(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                    ctx_lens: torch.Tensor, cu_nodes: torch.Tensor, path: torch.Tensor,
+                    path_lens: torch.Tensor, block_size: int, out_lens=None, stream=None):
+    """Moves the cache rows of accepted nodes up behind the context (fp8q_kv_cache_accept): caches
+    uint8 [slots, Hkv*D] or [layers, slots, Hkv*D] (in place), path int32 [B, max_path] node indices
+    in ascending order, path_lens int32 [B] -> new context lengths int32 [B]."""
+    dev, B = ctx_lens.device, ctx_lens.shape[0]
+    i32 = torch.int32
+    if k_cache.dim() not in (2, 3):
+        raise ValueError("k_cache must be [slots, Hkv*D] or [layers, slots, Hkv*D]")
+    layers = k_cache.shape[0] if k_cache.dim() == 3 else 1
+    slots, row = k_cache.shape[-2:]
+    shape = tuple(k_cache.shape)
+    _expect(dev, k_cache=(k_cache, torch.uint8, shape), v_cache=(v_cache, torch.uint8, shape),
+            block_table=(block_table, i32, (B, None)), ctx_lens=(ctx_lens, i32, (B,)),
+            cu_nodes=(cu_nodes, i32, (B + 1,)), path=(path, i32, (B, None)),
+            path_lens=(path_lens, i32, (B,)))
+    with _launch(dev, stream) as st:
+        o = torch.empty(B, dtype=i32, device=dev) if out_lens is None else out_lens
+        _expect(dev, out_lens=(o, i32, (B,)))
+        rc = _lib.lib().fp8q_kv_cache_accept(
+            _ptr(k_cache), _ptr(v_cache), slots, layers, slots * row, row, _ptr(block_table),
+            block_table.shape[1], int(block_size), _ptr(ctx_lens), _ptr(cu_nodes), _ptr(path),
+            path.shape[1], _ptr(path_lens), B, _ptr(o), st)
+    _lib.check(rc, "fp8q_kv_cache_accept")
     return o
 
 

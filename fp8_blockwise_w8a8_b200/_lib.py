@@ -63,6 +63,15 @@ SIGNATURES = {
     "fp8q_attention_decode": (_I, [_P, _I64, _P, _P, _I64, _P, _P, _I64, _P, _I64, _I64, _I64,
                                    _I64, _I64, _I64, ctypes.c_float, _P, _I64, _P, _I64, _P]),
     "fp8q_attention_decode_workspace_bytes": (_I, [_I64, _I64, _I64, _I64, _I64, _P]),
+    "fp8q_paged_batch_tables": (_I, [_P, _P, _I64, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _P,
+                                     _P, _P, _P, _P]),
+    "fp8q_tree_mask": (_I, [_P, _P, _P, _I64, _I64, _I64, _P, _I64, _P, _P]),
+    "fp8q_attention_tree": (_I, [_P, _I64, _P, _P, _I64, _P, _P, _I64, _P, _P, _P, _I64, _I64,
+                                 _I64, _I64, _I64, _I64, _I64, _I64, _I64, ctypes.c_float, _P,
+                                 _I64, _P, _I64, _P]),
+    "fp8q_attention_tree_workspace_bytes": (_I, [_I64, _I64, _I64, _I64, _I64, _I64, _P]),
+    "fp8q_kv_cache_accept": (_I, [_P, _P, _I64, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _P,
+                                  _I64, _P, _I64, _P, _P]),
     "fp8q_abi_version": (_I, []),
 }
 

@@ -13,6 +13,8 @@
 #include "ptx.cuh"
 #include "quant_kernels.cuh"
 #include "attn_kernels.cuh"
+#include "spec_kernels.cuh"
+#include "tree_attn_kernels.cuh"
 
 namespace {
 
@@ -31,6 +33,12 @@ struct DeviceState {
 // fp32 partials (192 tile-splits of 128 x 256).
 constexpr int64_t kStaticScratchBytes = int64_t{24} << 20;
 __device__ __align__(256) uint8_t g_splitk_static_scratch[kStaticScratchBytes];
+
+// Shared memory of the table builder at its largest batch, and of the ancestor-mask kernel.
+constexpr int kTablesMaxSmem = 2 * 4 * (fp8q::kTablesMaxB + 1);
+constexpr int tree_mask_smem(int max_nodes) {
+  return max_nodes * ((max_nodes + 63) / 64) * 8 + max_nodes * 4;
+}
 
 std::mutex g_mu;
 DeviceState g_dev[kMaxDevices];
@@ -111,7 +119,12 @@ int device_state(DeviceState **out) {
         cudaFuncSetAttribute(fp8q::k_rmsnorm_quant_token<true, false, true, false,
                                                          fp8q::kScaleE8M0>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
-            cudaSuccess)
+            cudaSuccess ||
+        cudaFuncSetAttribute(fp8q::k_paged_tables, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kTablesMaxSmem) != cudaSuccess ||
+        cudaFuncSetAttribute(fp8q::k_tree_mask<1024>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             tree_mask_smem(fp8q::kTreeMaxNodes)) != cudaSuccess)
       return FP8Q_ERR_LAUNCH;
     st.attrs_set = true;
   }
@@ -161,6 +174,17 @@ int make_bf16_out_map(CUtensorMap *map, void *base, int64_t rows, int64_t cols, 
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+bool aligned_to(const void *p, uintptr_t bytes) {
+  return reinterpret_cast<uintptr_t>(p) % bytes == 0;
+}
+
+// Whether two byte ranges share a byte.
+bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a_bytes > 0 && b_bytes > 0 && x < y + static_cast<uintptr_t>(b_bytes) &&
+         y < x + static_cast<uintptr_t>(a_bytes);
+}
 
 int launch_status() {
   return cudaGetLastError() == cudaSuccess ? FP8Q_OK : FP8Q_ERR_LAUNCH;
@@ -346,6 +370,23 @@ int attn_chunk(int64_t B, int64_t Hkv, int64_t max_seq_len) {
   return static_cast<int>(c);
 }
 
+int tree_attn_shape_status(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t block_size,
+                           int64_t max_nodes, int64_t max_seq_len) {
+  if (B < 0 || B > 65535 || Hq <= 0 || Hkv <= 0 || Hkv > 65535 || Hq % Hkv ||
+      (D != 64 && D != 128) || Hq * D > (1 << 24) || Hq / Hkv > 128 || block_size <= 0 ||
+      block_size > INT32_MAX || max_nodes < 0 || max_nodes > fp8q::kTreeMaxNodes ||
+      max_seq_len < 0 || max_seq_len > INT32_MAX - 128)
+    return FP8Q_ERR_SHAPE;
+  return FP8Q_OK;
+}
+
+int64_t tree_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
+                                  int64_t max_nodes, int64_t max_seq_len) {
+  if (B == 0 || max_nodes == 0 || max_seq_len == 0) return 0;
+  return 16;
+}
+
+
 int attn_shape_status(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t block_size,
                       int64_t max_seq_len) {
   // B and Hkv are grid dimensions (z, y)
@@ -367,7 +408,7 @@ int64_t attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t max_seq
 
 extern "C" {
 
-int fp8q_abi_version(void) { return (1 << 16) | 6; }
+int fp8q_abi_version(void) { return (1 << 16) | 7; }
 
 const char *fp8q_status_string(int status) {
   switch (status) {
@@ -959,6 +1000,211 @@ int fp8q_attention_decode(const void *q_e4m3, int64_t ldq, const void *k_cache,
   else if (G == 2) fp8q::k_attn_decode_combine<2><<<gc, fp8q::kAttnThreads, 0, stream>>>(a);
   else if (G == 4) fp8q::k_attn_decode_combine<4><<<gc, fp8q::kAttnThreads, 0, stream>>>(a);
   else fp8q::k_attn_decode_combine<8><<<gc, fp8q::kAttnThreads, 0, stream>>>(a);
+  return launch_status();
+}
+
+int fp8q_paged_batch_tables(const int32_t *ctx_lens, const int32_t *new_lens, int64_t B,
+                            int64_t block_size, int32_t *block_table, int64_t max_blocks,
+                            const int32_t *free_blocks, int64_t num_free,
+                            const int32_t *free_count, int32_t *free_left, int64_t max_tokens,
+                            int32_t *cu_tokens, int32_t *seq_lens, int64_t *slots,
+                            int64_t *positions, cudaStream_t stream) {
+  if (B < 0 || B > fp8q::kTablesMaxB || block_size <= 0 || block_size > INT32_MAX ||
+      max_blocks < 0 || max_blocks > INT32_MAX / block_size || num_free < 0 ||
+      num_free > INT32_MAX || max_tokens < 0 || max_tokens > INT32_MAX)
+    return FP8Q_ERR_SHAPE;
+  if (!free_count || !free_left || !cu_tokens || (num_free > 0 && !free_blocks) ||
+      (B > 0 && (!ctx_lens || !new_lens || !seq_lens || (max_blocks > 0 && !block_table))) ||
+      (max_tokens > 0 && (!slots || !positions)))
+    return FP8Q_ERR_NULL;
+  if (!aligned_to(ctx_lens, 4) || !aligned_to(new_lens, 4) || !aligned_to(block_table, 4) ||
+      !aligned_to(free_blocks, 4) || !aligned_to(free_count, 4) || !aligned_to(free_left, 4) ||
+      !aligned_to(cu_tokens, 4) || !aligned_to(seq_lens, 4) || !aligned_to(slots, 8) ||
+      !aligned_to(positions, 8))
+    return FP8Q_ERR_ALIGN;
+  // every CTA reads the inputs while the first one writes the results
+  const void *in[] = {ctx_lens, new_lens, free_count};
+  const int64_t in_bytes[] = {4 * B, 4 * B, 4};
+  const void *res[] = {free_left, cu_tokens, seq_lens};
+  const int64_t res_bytes[] = {4, 4 * (B + 1), 4 * B};
+  for (int i = 0; i < 3; ++i)
+    for (int j = 0; j < 3; ++j)
+      if (overlap(in[i], in_bytes[i], res[j], res_bytes[j])) return FP8Q_ERR_ARG;
+  DeviceState *st = nullptr;
+  const int rc = device_state(&st);
+  if (rc != FP8Q_OK) return rc;
+  fp8q::TablesArgs a;
+  a.ctx_lens = ctx_lens;
+  a.new_lens = new_lens;
+  a.B = static_cast<int>(B);
+  a.block_size = static_cast<uint32_t>(block_size);
+  a.block_table = block_table;
+  a.max_blocks = max_blocks;
+  a.capacity = max_blocks * block_size;
+  a.free_blocks = free_blocks;
+  a.num_free = num_free;
+  a.free_count = free_count;
+  a.free_left = free_left;
+  a.max_tokens = max_tokens;
+  a.cu = cu_tokens;
+  a.seq_lens = seq_lens;
+  a.slots = slots;
+  a.positions = positions;
+  const int64_t need = (max_tokens + fp8q::kTablesThreads - 1) / fp8q::kTablesThreads;
+  const int64_t cap = 2 * static_cast<int64_t>(st->sms);
+  const int grid = static_cast<int>(need < 1 ? 1 : (need < cap ? need : cap));
+  fp8q::k_paged_tables<<<grid, fp8q::kTablesThreads, 8 * (B + 1), stream>>>(a);
+  return launch_status();
+}
+
+int fp8q_tree_mask(const int32_t *parents, const int32_t *cu_nodes, const int32_t *ctx_lens,
+                   int64_t B, int64_t total, int64_t max_nodes, int64_t *mask, int64_t ldm,
+                   int64_t *positions, cudaStream_t stream) {
+  if (B < 0 || B > INT32_MAX || total < 0 || total > INT32_MAX || max_nodes < 0 ||
+      max_nodes > fp8q::kTreeMaxNodes)
+    return FP8Q_ERR_SHAPE;
+  const int64_t words = (max_nodes + 63) / 64;
+  if (ldm < words) return FP8Q_ERR_SHAPE;
+  if (B == 0 || total == 0 || max_nodes == 0) return FP8Q_OK;
+  if (!parents || !cu_nodes || !mask) return FP8Q_ERR_NULL;
+  if (!aligned_to(parents, 4) || !aligned_to(cu_nodes, 4) || !aligned_to(ctx_lens, 4) ||
+      !aligned_to(mask, 8) || !aligned_to(positions, 8))
+    return FP8Q_ERR_ALIGN;
+  DeviceState *st = nullptr;
+  const int rc = device_state(&st);
+  if (rc != FP8Q_OK) return rc;
+  fp8q::TreeMaskArgs a;
+  a.parents = parents;
+  a.cu = cu_nodes;
+  a.ctx_lens = ctx_lens;
+  a.total = total;
+  a.max_nodes = static_cast<int>(max_nodes);
+  a.words = static_cast<int>(words);
+  a.mask = mask;
+  a.ldm = ldm;
+  a.positions = positions;
+  const int smem = tree_mask_smem(a.max_nodes);
+  const unsigned grid = static_cast<unsigned>(B);
+  if (max_nodes <= 256)
+    fp8q::k_tree_mask<128><<<grid, 128, smem, stream>>>(a);
+  else
+    fp8q::k_tree_mask<1024><<<grid, 1024, smem, stream>>>(a);
+  return launch_status();
+}
+
+int fp8q_attention_tree_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
+                                        int64_t max_nodes, int64_t max_seq_len, int64_t *bytes) {
+  if (!bytes) return FP8Q_ERR_NULL;
+  *bytes = 0;
+  const int rc = tree_attn_shape_status(B, Hq, Hkv, D, 1, max_nodes, max_seq_len);
+  if (rc != FP8Q_OK) return rc;
+  *bytes = tree_attn_workspace_bytes(B, Hq, Hkv, D, max_nodes, max_seq_len);
+  return FP8Q_OK;
+}
+
+int fp8q_attention_tree(const void *q_e4m3, int64_t ldq, const void *k_cache, const void *v_cache,
+                        int64_t num_slots, const float *scale3, const int32_t *block_table,
+                        int64_t max_blocks, const int32_t *ctx_lens, const int32_t *cu_nodes,
+                        const int64_t *tree_mask, int64_t ldm, int64_t B, int64_t total,
+                        int64_t Hq, int64_t Hkv, int64_t D, int64_t block_size,
+                        int64_t max_nodes, int64_t max_seq_len, float sm_scale, void *out_bf16,
+                        int64_t ldo, void *workspace, int64_t workspace_bytes,
+                        cudaStream_t stream) {
+  int rc = tree_attn_shape_status(B, Hq, Hkv, D, block_size, max_nodes, max_seq_len);
+  if (rc != FP8Q_OK) return rc;
+  if (num_slots < 0 || num_slots > INT32_MAX || max_blocks < 0 || max_blocks > INT32_MAX ||
+      max_blocks * block_size < max_seq_len || total < 0 || total > INT32_MAX ||
+      ldq < Hq * D || ldo < Hq * D || (tree_mask && ldm < (max_nodes + 63) / 64))
+    return FP8Q_ERR_SHAPE;
+  if (B == 0 || total == 0 || max_nodes == 0) return FP8Q_OK;
+  if (!q_e4m3 || !k_cache || !v_cache || !scale3 || !block_table || !ctx_lens || !cu_nodes ||
+      !out_bf16 || !workspace)
+    return FP8Q_ERR_NULL;
+  if (!aligned16(q_e4m3) || ldq % 16 || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned16(workspace) || !aligned16(out_bf16) || ldo % 8 || !aligned_to(scale3, 4) ||
+      !aligned_to(block_table, 4) || !aligned_to(ctx_lens, 4) || !aligned_to(cu_nodes, 4) ||
+      !aligned_to(tree_mask, 8))
+    return FP8Q_ERR_ALIGN;
+  if (workspace_bytes < tree_attn_workspace_bytes(B, Hq, Hkv, D, max_nodes, max_seq_len))
+    return FP8Q_ERR_SHAPE;
+  DeviceState *st = nullptr;
+  if ((rc = device_state(&st)) != FP8Q_OK) return rc;
+  fp8q::TreeAttnArgs a;
+  a.q = static_cast<const uint8_t *>(q_e4m3);
+  a.ldq = ldq;
+  a.k_cache = static_cast<const uint8_t *>(k_cache);
+  a.v_cache = static_cast<const uint8_t *>(v_cache);
+  a.num_blocks = num_slots / block_size;
+  a.scale3 = scale3;
+  a.block_table = block_table;
+  a.max_blocks = max_blocks;
+  a.ctx_lens = ctx_lens;
+  a.cu = cu_nodes;
+  a.mask = tree_mask;
+  a.ldm = ldm;
+  a.total = total;
+  a.B = static_cast<int>(B);
+  a.Hq = static_cast<int>(Hq);
+  a.Hkv = static_cast<int>(Hkv);
+  a.block_size = static_cast<int>(block_size);
+  a.max_nodes = static_cast<int>(max_nodes);
+  a.max_seq_len = static_cast<int>(max_seq_len);
+  a.sm_scale = sm_scale;
+  a.ws = static_cast<float *>(workspace);
+  a.out = static_cast<uint16_t *>(out_bf16);
+  a.ldo = ldo;
+  const dim3 grid(static_cast<unsigned>((max_nodes + 3) / 4), static_cast<unsigned>(Hq),
+                  static_cast<unsigned>(B));
+  if (D == 128) fp8q::k_tree_attn<128><<<grid, 128, 0, stream>>>(a);
+  else fp8q::k_tree_attn<64><<<grid, 128, 0, stream>>>(a);
+  return launch_status();
+}
+
+int fp8q_kv_cache_accept(void *k_cache, void *v_cache, int64_t num_slots, int64_t layers,
+                         int64_t layer_stride, int64_t row_bytes, const int32_t *block_table,
+                         int64_t max_blocks, int64_t block_size, const int32_t *ctx_lens,
+                         const int32_t *cu_nodes, const int32_t *path, int64_t max_path,
+                         const int32_t *path_lens, int64_t B, int32_t *new_lens,
+                         cudaStream_t stream) {
+  if (B < 0 || B > INT32_MAX || num_slots < 0 || num_slots > INT32_MAX || layers < 0 ||
+      layers > 65535 || row_bytes <= 0 || row_bytes % 16 || row_bytes > (1 << 24) ||
+      layer_stride < 0 || (layers > 1 && layer_stride < num_slots * row_bytes) ||
+      block_size <= 0 || block_size > INT32_MAX || max_blocks < 0 ||
+      max_blocks > INT32_MAX / block_size || max_path < 0 || max_path > fp8q::kTreeMaxNodes)
+    return FP8Q_ERR_SHAPE;
+  if (B == 0 || layers == 0) return FP8Q_OK;
+  if (!ctx_lens || !cu_nodes || !path_lens || !new_lens || (max_path > 0 && !path) ||
+      (num_slots > 0 && (!k_cache || !v_cache)) || (max_blocks > 0 && !block_table))
+    return FP8Q_ERR_NULL;
+  if (!aligned16(k_cache) || !aligned16(v_cache) || layer_stride % 16 ||
+      !aligned_to(block_table, 4) || !aligned_to(ctx_lens, 4) || !aligned_to(cu_nodes, 4) ||
+      !aligned_to(path, 4) || !aligned_to(path_lens, 4) || !aligned_to(new_lens, 4))
+    return FP8Q_ERR_ALIGN;
+  // the CTAs of the other layers read what the first layer's would overwrite
+  const void *in[] = {ctx_lens, cu_nodes, path, path_lens, block_table};
+  const int64_t in_bytes[] = {4 * B, 4 * (B + 1), 4 * B * max_path, 4 * B, 4 * B * max_blocks};
+  for (int i = 0; i < 5; ++i)
+    if (overlap(in[i], in_bytes[i], new_lens, 4 * B)) return FP8Q_ERR_ARG;
+  DeviceState *st = nullptr;
+  const int rc = device_state(&st);
+  if (rc != FP8Q_OK) return rc;
+  fp8q::AcceptArgs a;
+  a.k_cache = static_cast<uint8_t *>(k_cache);
+  a.v_cache = static_cast<uint8_t *>(v_cache);
+  a.layer_stride = layer_stride;
+  a.num_blocks = num_slots / block_size;
+  a.block_table = block_table;
+  a.max_blocks = max_blocks;
+  a.block_size = static_cast<uint32_t>(block_size);
+  a.ctx_lens = ctx_lens;
+  a.cu = cu_nodes;
+  a.path = path;
+  a.max_path = max_path;
+  a.path_lens = path_lens;
+  a.chunks = static_cast<int>(row_bytes / 16);
+  a.new_lens = new_lens;
+  const dim3 grid(static_cast<unsigned>(B), static_cast<unsigned>(layers));
+  fp8q::k_kv_accept<<<grid, fp8q::kAcceptThreads, 16 * max_path, stream>>>(a);
   return launch_status();
 }
 

@@ -326,6 +326,123 @@ int fp8q_attention_decode(const void *q_e4m3, int64_t ldq, const void *k_cache,
 int fp8q_attention_decode_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
                                           int64_t max_seq_len, int64_t *bytes);
 
+/* ------------------------------------------------------------------------------------------------
+ * A speculative-decoding step over the paged FP8 KV cache.  Every sequence b has ctx_lens[b]
+ * committed positions in the cache and adds drafted tokens ("nodes") behind them:
+ *   fp8q_paged_batch_tables  gives each node its cache slot (and its request the blocks it lacks)
+ *   fp8q_tree_mask           gives each node its position and the bits of its ancestors
+ *   fp8q_kv_cache_write      writes the nodes' K and V at those slots
+ *   fp8q_attention_tree      attention of every node over the context and its ancestors
+ *   fp8q_kv_cache_accept     moves the accepted nodes' rows up behind the context
+ * All lengths, offsets and tables are DEVICE memory, so that a step can be captured in a CUDA graph
+ * and replayed with other lengths.  The pages define no such step; it is built on the cache of
+ * FP8-RL abstract, item (ii).
+ * --------------------------------------------------------------------------------------------- */
+
+/* Block tables and slot maps from request lengths.  Request b holds ctx_lens[b] positions in
+ * ceil(ctx / block_size) blocks and adds new_lens[b] tokens at positions ctx .. ctx + new - 1, packed
+ * request after request as tokens 0 .. T - 1:
+ *   block_table  [B][max_blocks] int32, read and written: entries ceil(ctx / block_size) ..
+ *                ceil((ctx + new) / block_size) - 1 of row b are popped from the free stack, lower
+ *                requests and lower entries first; all other entries are left as they were
+ *   free_blocks  [num_free] int32, read: a stack of free block ids, its top entry
+ *                free_blocks[free_count - 1]
+ *   free_count   [1] int32, read; free_left [1] int32, written: entries left on the stack.  The
+ *                caller copies it back (or swaps the two) before the next step
+ *   cu_tokens    [B + 1] int32, written: first token of each request, cu_tokens[B] = T
+ *   seq_lens     [B] int32, written: ctx + new
+ *   slots        [max_tokens] int64, written: block_table[b][p / block_size] * block_size +
+ *                p % block_size of the token's position p; -1 behind the last token (a slot that
+ *                fp8q_kv_cache_write skips)
+ *   positions    [max_tokens] int64, written: p; 0 behind the last token
+ * Recorded as FP8Q_ERR_RANGE: a negative length, or ctx + new above max_blocks * block_size (the
+ * length is clamped); T above max_tokens (the last requests' tokens are cut off, in all outputs);
+ * free_count outside [0, num_free] (clamped); fewer free blocks than needed (the entries that get
+ * none become -1, and so do their tokens' slots, as where block_table holds a negative id).
+ * B <= 16384, max_blocks * block_size and max_tokens <= 2^31 - 1 (FP8Q_ERR_SHAPE).  free_left,
+ * cu_tokens and seq_lens must not overlap ctx_lens, new_lens or free_count (FP8Q_ERR_ARG), nor any
+ * other array another (undefined results).  int32 arrays 4-byte, int64 arrays 8-byte aligned.
+ * One launch; B = 0 is a batch without requests (T = 0). */
+int fp8q_paged_batch_tables(const int32_t *ctx_lens, const int32_t *new_lens, int64_t B,
+                            int64_t block_size, int32_t *block_table, int64_t max_blocks,
+                            const int32_t *free_blocks, int64_t num_free,
+                            const int32_t *free_count, int32_t *free_left, int64_t max_tokens,
+                            int32_t *cu_tokens, int32_t *seq_lens, int64_t *slots,
+                            int64_t *positions, cudaStream_t stream);
+
+/* Ancestor masks of drafted trees.  The nodes of sequence b are rows cu_nodes[b] ..
+ * cu_nodes[b + 1] - 1; node i's parent is parents[row] in [0, i), or -1 for a child of the context.
+ *   mask       [total][ldm] int64, written: word w of node i holds bit j - 64 w for each j in
+ *              [64 w, 64 w + 64) that is i or an ancestor of i; ceil(max_nodes / 64) words per row
+ *   ctx_lens   [B] int32 or NULL (zeros); positions [total] int64 or NULL, written: ctx_lens[b]
+ *              plus the node's depth (0 for a child of the context), its rotary position
+ *   max_nodes  a HOST bound on the nodes of a sequence, <= 1024
+ * Recorded as FP8Q_ERR_RANGE: a parent outside [-1, i) (taken as -1); offsets that decrease or
+ * leave [0, total], a sequence of more than max_nodes nodes (the rest of its rows are not written).
+ * Rows behind the last sequence are left as they were.  B, total <= 2^31 - 1. */
+int fp8q_tree_mask(const int32_t *parents, const int32_t *cu_nodes, const int32_t *ctx_lens,
+                   int64_t B, int64_t total, int64_t max_nodes, int64_t *mask, int64_t ldm,
+                   int64_t *positions, cudaStream_t stream);
+
+/* Attention of drafted trees over the FP8 KV cache.  Node i of sequence b (row cu_nodes[b] + i) sees
+ * the positions 0 .. ctx_lens[b] - 1 and, among the nodes j <= i (cached at position ctx + j), those
+ * whose bit j of its mask row is set; bits above i are ignored; a NULL mask stands for all j <= i (a
+ * chain: also a piece of a prompt).  With the cached rows found through block_table as in
+ * fp8q_attention_decode, kv head g = h / (Hq / Hkv) and (s_q, s_k, s_v) = scale3:
+ *   z_j = sm_scale * s_q * s_k * sum_d dec(q[row][h D + d]) * dec(k_cache[slot_j][g D + d])
+ *   out[row][h D + d] = bf16( s_v * sum_j softmax(z)_j * dec(v_cache[slot_j][g D + d]) )
+ * over the positions seen; a node that sees none gets 0.  What is not seen does not count, whatever
+ * it holds (NaN codes, rows that were never written).
+ *   q_e4m3       [total][ldq] uint8 codes (Hq heads of D; from fp8q_kv_cache_write)
+ *   tree_mask    [total][ldm] int64 or NULL (from fp8q_tree_mask), ldm >= ceil(max_nodes / 64)
+ *   max_nodes, max_seq_len
+ *                HOST bounds on a sequence's nodes (<= 1024) and on ctx + nodes
+ *                (<= max_blocks * block_size)
+ *   out_bf16     [total][ldo] bf16, written; rows behind the last sequence are left as they were
+ *   workspace    DEVICE memory of fp8q_attention_tree_workspace_bytes(...) bytes, 16-byte aligned,
+ *                caller-owned; it needs no initialisation.  Two calls that share one must be
+ *                ordered (same stream, or synchronized), replays of captured graphs among them
+ * D is 64 or 128, Hq a multiple of Hkv with Hq / Hkv <= 128, num_slots <= 2^31 - 1, B <= 65535; q and
+ * out 16-byte aligned with ldq % 16 == 0, ldo % 8 == 0.  Results within
+ * |out - ref| <= ulp_bf16(|ref|)/2 + absref * (2^-11 + 2 (D + 2) 2^-24 zabs + (L + 16) 2^-23)
+ * of the fp64 reference, as fp8q_attention_decode (absref, zabs over the positions seen, L their
+ * number).  Recorded as FP8Q_ERR_RANGE: offsets as in fp8q_tree_mask; a context that is negative or
+ * makes ctx + nodes exceed max_seq_len (clamped); a block id outside [0, num_slots / block_size)
+ * (its positions are not seen). */
+int fp8q_attention_tree(const void *q_e4m3, int64_t ldq, const void *k_cache, const void *v_cache,
+                        int64_t num_slots, const float *scale3, const int32_t *block_table,
+                        int64_t max_blocks, const int32_t *ctx_lens, const int32_t *cu_nodes,
+                        const int64_t *tree_mask, int64_t ldm, int64_t B, int64_t total,
+                        int64_t Hq, int64_t Hkv, int64_t D, int64_t block_size,
+                        int64_t max_nodes, int64_t max_seq_len, float sm_scale, void *out_bf16,
+                        int64_t ldo, void *workspace, int64_t workspace_bytes,
+                        cudaStream_t stream);
+
+/* Workspace bytes of fp8q_attention_tree for these sizes, written to *bytes (HOST pointer);
+ * depends on the sizes only. */
+int fp8q_attention_tree_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
+                                        int64_t max_nodes, int64_t max_seq_len, int64_t *bytes);
+
+/* Accepted rows to consecutive positions.  path[b] lists the accepted nodes of sequence b, strictly
+ * ascending (a node's ancestors come before it); for k < path_lens[b] the cache rows of position
+ * ctx + path[b][k] are copied to position ctx + k, in K and V of every layer, as if in the order of
+ * k; new_lens[b] = ctx_lens[b] + path_lens[b] is the committed context of the next step.
+ *   k_cache, v_cache  [layers] caches of [num_slots][row_bytes] uint8, layer_stride BYTES apart, read
+ *                     and written (row_bytes = Hkv * D, a multiple of 16); 16-byte aligned
+ *   path              [B][max_path] int32, max_path <= 1024; entries from path_lens[b] on are not read
+ *   cu_nodes          [B + 1] int32: sequence b has cu_nodes[b + 1] - cu_nodes[b] nodes
+ * A sequence whose path is not strictly ascending within its nodes, is longer than its nodes or
+ * max_path, leaves the table (max_blocks * block_size positions) or meets a block id outside
+ * [0, num_slots / block_size) records FP8Q_ERR_RANGE: none of its rows moves and its new length is
+ * ctx_lens[b].  Slots of different (sequence, position) pairs that are moved must differ.  new_lens
+ * must not overlap the other int32 arrays (FP8Q_ERR_ARG). */
+int fp8q_kv_cache_accept(void *k_cache, void *v_cache, int64_t num_slots, int64_t layers,
+                         int64_t layer_stride, int64_t row_bytes, const int32_t *block_table,
+                         int64_t max_blocks, int64_t block_size, const int32_t *ctx_lens,
+                         const int32_t *cu_nodes, const int32_t *path, int64_t max_path,
+                         const int32_t *path_lens, int64_t B, int32_t *new_lens,
+                         cudaStream_t stream);
+
 /* Grouped W8A8 GEMM for MoE experts (a6): for each expert e the rows
  * [group_offsets[e], group_offsets[e+1]) of aq/sa/out are multiplied by expert e's weight.
  *   wq             [E][N][ldw] uint8 codes (expert stride N * ldw)

@@ -1,0 +1,411 @@
+"""GPU parity of the attention of drafted trees over the FP8 KV cache (fp8q_attention_tree) against the
+float64 oracle: head layouts with 1 to 40 query heads per kv head, head sizes 64 and 128, ragged
+drafts from no node to 1024, contexts from none to long, block sizes 1 to 128, arbitrary masks (rows
+that see nothing among them), NaN codes in places that are not seen, scores that grow along the
+positions, strided and padded rows, caches beyond 2^31 bytes, inputs out of range, captured and
+replayed calls, and a whole speculative step.
+
+The gate is the one of the decode attention, from the kernel's arithmetic: a score is a sum of D exact
+products in fp32 then one scale, |dz| <= (D + 2) 2^-24 zabs, which moves a weight by at most 2 |dz|
+relatively; a weight enters the value sum as fp16 (at most 2^-11 relatively); value sums, softmax sums,
+merges and exp2 add at most (L + 16) 2^-23 of absref; the bf16 rounding half an ulp.  Weights far below
+the largest one are fp16 subnormals: the largest weight is held between 2^7 and 2^15, a subnormal is
+off by at most 2^-25, so each position adds at most 2^-32 of the largest value in magnitude:
+    |out - ref| <= ulp_bf16(|ref|) / 2 + L 2^-32 vmax
+                   + absref * (2^-11 + 2 (D + 2) 2^-24 zabs + (L + 16) 2^-23).
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import fp8_blockwise_w8a8_b200 as fq
+from oracle import speculative as spec
+
+from helpers import host_bf16_f64
+
+pytestmark = pytest.mark.gpu
+RANGE = 9
+
+
+def i32(a):
+    return torch.from_numpy(np.ascontiguousarray(a, np.int32)).cuda()
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def _codes(shape, rng, std=40.0):
+    """E4M3 codes of N(0, std) values, as the cache holds them under a per-tensor scale."""
+    x = torch.from_numpy(rng.standard_normal(shape, dtype=np.float32) * np.float32(std))
+    return x.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+
+
+def _case(Hq, Hkv, D, nodes, ctx, bs, seed, kind="tree", spare=3):
+    """Random codes, a shuffled block table and trees; kind "random" gives arbitrary masks."""
+    rng = np.random.default_rng(seed)
+    need = [-(-(c + n) // bs) for c, n in zip(ctx, nodes)]
+    width = max(1, max(need))
+    blocks = sum(need) + spare
+    perm = rng.permutation(blocks)
+    table = np.full((len(nodes), width), -1, np.int32)
+    at = 0
+    for b, k in enumerate(need):
+        table[b, :k] = perm[at:at + k]
+        at += k
+    sees = []
+    for n in nodes:
+        if kind == "random":
+            sees.append(rng.random((n, n)) < 0.4)
+        elif kind == "chain":
+            sees.append(np.tril(np.ones((n, n), bool)))
+        else:
+            sees.append(spec.tree_sees([rng.integers(max(-1, i - 5), i) for i in range(n)]))
+    return dict(Hq=Hq, Hkv=Hkv, D=D, bs=bs, ctx=np.array(ctx), nodes=list(nodes), table=table,
+                sees=sees, q=[_codes((n, Hq * D), rng) for n in nodes],
+                k=_codes((blocks * bs, Hkv * D), rng), v=_codes((blocks * bs, Hkv * D), rng),
+                s3=np.array([0.011, 0.012, 0.007], np.float32),
+                max_nodes=max(1, max(nodes)), max_len=max(1, max(c + n for c, n in zip(ctx, nodes))))
+
+
+def _args(d, mask=True):
+    words = -(-d["max_nodes"] // 64)
+    bits = np.concatenate([spec.pack_bits(s, words) for s in d["sees"]])
+    return [dev(np.concatenate(d["q"])), dev(d["k"]), dev(d["v"]), dev(d["s3"]), i32(d["table"]),
+            i32(d["ctx"]), i32(np.concatenate([[0], np.cumsum(d["nodes"])])),
+            dev(bits) if mask else None, d["Hq"], d["Hkv"], d["bs"], d["max_nodes"], d["max_len"]]
+
+
+def _oracle(d, sm_scale=None):
+    return spec.attention(d["q"], d["k"], d["v"], d["s3"], d["table"], d["ctx"], d["sees"], d["Hq"],
+                          d["Hkv"], d["bs"], sm_scale)
+
+
+def _check(o, d, sm_scale=None, seqs=None):
+    D = d["D"]
+    got = host_bf16_f64(o)
+    ref, absref, zabs, count = _oracle(d, sm_scale)
+    cu = np.concatenate([[0], np.cumsum(d["nodes"])])
+    vmax = float(d["s3"][2]) * 448.0
+    for b in range(len(ref)) if seqs is None else seqs:
+        L = count[b].astype(np.float64)[:, None]
+        z = np.repeat(zabs[b], D, axis=1)
+        bound = (oracle.bf16_ulp(np.abs(ref[b])) / 2 + L * 2.0 ** -32 * vmax
+                 + absref[b] * (2.0 ** -11 + 2 * (D + 2) * 2.0 ** -24 * z + (L + 16) * 2.0 ** -23))
+        err = np.abs(got[cu[b]:cu[b + 1]] - ref[b])
+        bad = ~(err <= bound)
+        assert not bad.any(), (f"sequence {b}: {bad.sum()} of {bad.size} outside the bound, first at "
+                               f"{np.argwhere(bad)[0]}; largest excess {np.nanmax(err - bound):.3e}")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (4, 4), (6, 2), (5, 1), (8, 2), (16, 2), (40, 1)])
+def test_head_layouts_and_ragged_lengths(Hq, Hkv, D):
+    d = _case(Hq, Hkv, D, [1, 3, 0, 17, 33, 64, 65, 2, 7], [0, 1, 40, 63, 64, 65, 127, 300, 0], 16,
+              seed=Hq + Hkv + D)
+    o = fq.attention_tree(*_args(d))
+    assert fq.check_device_error() == 0
+    _check(o, d)
+
+
+@pytest.mark.parametrize("bs", [1, 7, 64, 128])
+def test_block_sizes(bs):
+    d = _case(8, 2, 128, [5, 1, 12], [130, 77, 3], bs, seed=30 + bs)
+    o = fq.attention_tree(*_args(d))
+    assert fq.check_device_error() == 0
+    _check(o, d)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_arbitrary_masks_and_rows_that_see_nothing(D):
+    d = _case(8, 4, D, [70, 1, 9, 20], [0, 0, 0, 5], 16, seed=50, kind="random")
+    d["sees"][0][3] = False
+    d["sees"][0][69] = False
+    d["sees"][1][0] = False
+    o = fq.attention_tree(*_args(d))
+    assert fq.check_device_error() == 0
+    _check(o, d)
+    got = host_bf16_f64(o)
+    assert not got[[3, 69, 70]].any()
+
+
+def test_bits_above_the_diagonal_are_ignored():
+    d = _case(4, 2, 64, [40, 6], [10, 70], 16, seed=51)
+    a = _args(d)
+    o = fq.attention_tree(*a)
+    for s in d["sees"]:
+        s |= ~np.tril(np.ones_like(s))
+    b = _args(d)
+    assert not torch.equal(a[7], b[7])
+    assert torch.equal(fq.attention_tree(*b), o)
+
+
+@pytest.mark.parametrize("Hq,Hkv,n", [(2, 2, 1024), (8, 1, 300), (16, 2, 129)])
+def test_no_mask_is_a_chain(Hq, Hkv, n):
+    d = _case(Hq, Hkv, 128, [n, 2], [100, 64], 16, seed=52 + n, kind="chain")
+    o = fq.attention_tree(*_args(d, mask=False))
+    assert fq.check_device_error() == 0
+    _check(o, d)
+    assert torch.equal(o, fq.attention_tree(*_args(d)))
+
+
+def test_long_contexts():
+    d = _case(8, 2, 128, [33, 4, 1], [20011, 9000, 130], 16, seed=53)
+    o = fq.attention_tree(*_args(d))
+    assert fq.check_device_error() == 0
+    _check(o, d)
+
+
+def test_many_short_sequences():
+    rng = np.random.default_rng(54)
+    d = _case(4, 2, 64, rng.integers(0, 4, 700).tolist(), rng.integers(0, 30, 700).tolist(), 8, 54)
+    o = fq.attention_tree(*_args(d))
+    assert fq.check_device_error() == 0
+    _check(o, d)
+
+
+@pytest.mark.parametrize("sm_scale", [0.0, -0.09, 0.5])
+def test_softmax_scales(sm_scale):
+    d = _case(8, 2, 128, [12, 40], [200, 333], 16, seed=55)
+    o = fq.attention_tree(*_args(d), sm_scale=sm_scale)
+    assert fq.check_device_error() == 0
+    _check(o, d, sm_scale)
+
+
+@pytest.mark.parametrize("nodes", [3, 20, 40])
+@pytest.mark.parametrize("down", [False, True])
+def test_scores_that_grow_along_the_positions(nodes, down):
+    """Keys whose size grows (or falls) with the position, queries of one sign: the running maximum
+    moves in every tile by up to hundreds of log2 units."""
+    d = _case(4, 2, 128, [nodes], [900], 16, seed=56)
+    rng = np.random.default_rng(57)
+    L = 900 + nodes
+    ramp = np.linspace(0.02, 60.0, L)[:, None] * rng.uniform(0.5, 1.5, (L, 2 * 128))
+    slots = d["table"][0][np.arange(L) // 16] * 16 + np.arange(L) % 16
+    enc = lambda x: (torch.from_numpy(x.astype(np.float32)).to(torch.float8_e4m3fn)
+                     .view(torch.uint8).numpy())
+    d["k"][slots] = enc(ramp[::-1].copy() if down else ramp)
+    d["q"][0] = enc(rng.uniform(20, 60, (nodes, 4 * 128)))
+    o = fq.attention_tree(*_args(d))
+    assert fq.check_device_error() == 0
+    _check(o, d)
+
+
+@pytest.mark.parametrize("Hq,Hkv,n", [(4, 2, 6), (4, 1, 12), (8, 1, 30)])
+def test_nan_codes_that_are_not_seen(Hq, Hkv, n):
+    """NaN in every slot no sequence holds and in K and V of nodes that only some rows see: the other
+    rows stay exact; a row that sees a NaN value is NaN in that value's dims only, one that sees a NaN
+    key is NaN throughout."""
+    D = 128
+    d = _case(Hq, Hkv, D, [n, 5], [150, 0], 16, seed=58, kind="star")
+    d["sees"] = [np.eye(n, dtype=bool), np.eye(5, dtype=bool)]
+    slot = lambda b, p: d["table"][b, p // 16] * 16 + p % 16
+    held = {slot(0, p) for p in range(150 + n)} | {slot(1, p) for p in range(5)}
+    for s in set(range(len(d["k"]))) - held:
+        d["k"][s] = d["v"][s] = 0x7F
+    clean = dict(d, k=d["k"].copy(), v=d["v"].copy())
+    d["v"][slot(0, 150 + 2), 7] = 0xFF                  # node 2: one dim of kv head 0
+    d["k"][slot(0, 150 + 4), 3] = 0x7F                  # node 4: key of kv head 0
+    o = fq.attention_tree(*_args(d))
+    assert fq.check_device_error() == 0
+    got = host_bf16_f64(o).reshape(n + 5, Hq, D)
+    G = Hq // Hkv
+    bad = np.zeros((n + 5, Hq, D), bool)
+    bad[2, :G, 7] = True
+    bad[4, :G] = True
+    np.testing.assert_array_equal(np.isnan(got), bad)
+    ref = fq.attention_tree(*_args(clean))
+    _check(ref, clean)
+    same = host_bf16_f64(ref).reshape(n + 5, Hq, D)
+    np.testing.assert_array_equal(got[~bad], same[~bad])
+
+
+def test_strided_and_padded_rows():
+    """Leading dimensions wider than the rows, and a capacity beyond the last sequence: what lies
+    outside the rows is neither read nor written."""
+    d = _case(4, 2, 64, [3, 70, 1], [20, 100, 64], 16, seed=59)
+    a = _args(d)
+    total, W = sum(d["nodes"]), 4 * 64
+    q = torch.full((total + 9, W + 48), 0x7F, dtype=torch.uint8, device="cuda")
+    q[:total, :W] = a[0]
+    mask = torch.full((total + 9, 5), -1, dtype=torch.int64, device="cuda")
+    mask[:total, :a[7].shape[1]] = a[7]
+    out = torch.full((total + 9, W + 8), 3.0, dtype=torch.bfloat16, device="cuda")
+    a[0], a[7] = q[:, :W], mask
+    fq.attention_tree(*a, out=out[:, :W])
+    assert fq.check_device_error() == 0
+    _check(out[:total, :W].contiguous(), d)
+    assert (out[total:] == 3.0).all() and (out[:, W:] == 3.0).all()
+
+
+def test_cache_beyond_two_gigabytes():
+    Hkv, D, bs = 16, 128, 64
+    slots = (5 << 30) // (2 * Hkv * D)                  # 2.5 GiB each for K and V
+    rng = np.random.default_rng(60)
+    blocks = slots // bs
+    nodes, ctx = [3, 2], [200, 100]
+    table = np.array([[blocks - 1, 0, blocks - 2, blocks // 2], [blocks - 3, blocks - 4, 5, 6]])
+    small = _case(16, Hkv, D, nodes, ctx, bs, seed=60)
+    k = torch.zeros((slots, Hkv * D), dtype=torch.uint8, device="cuda")
+    v = torch.zeros_like(k)
+    for b in range(2):
+        for i in range(-(-(ctx[b] + nodes[b]) // bs)):
+            at, to = small["table"][b, i] * bs, int(table[b, i]) * bs
+            k[to:to + bs] = dev(small["k"][at:at + bs])
+            v[to:to + bs] = dev(small["v"][at:at + bs])
+    a = _args(small)
+    a[1], a[2], a[4] = k, v, i32(table)
+    o = fq.attention_tree(*a)
+    assert fq.check_device_error() == 0
+    _check(o, small)
+
+
+def test_inputs_out_of_range():
+    """A bad block id hides its positions, a context beyond the bound and too many nodes are clamped,
+    offsets outside the rows too: recorded, the other sequences as ever."""
+    d = _case(8, 2, 128, [4, 5, 6], [100, 90, 80], 16, seed=61)
+    d["table"][1, 2] = 10 ** 6
+    o = fq.attention_tree(*_args(d))
+    assert fq.check_device_error() == RANGE and fq.check_device_error() == 0
+    _check(o, d)                                        # the oracle leaves the block out as well
+    d["table"][1, 2] = -1
+    o = fq.attention_tree(*_args(d))
+    assert fq.check_device_error() == RANGE
+    _check(o, d)
+    d = _case(8, 2, 128, [4, 5, 6], [100, 90, 80], 16, seed=62)
+    for where, value in ((5, [100, 10 ** 6, 80]), (5, [100, -5, 80]), (6, [0, 4, 4, 99]),
+                         (6, [0, 4, 2, 15])):
+        a = _args(d)
+        a[where] = i32(value)
+        o = fq.attention_tree(*a)
+        assert fq.check_device_error() == RANGE
+        _check(o, d, seqs=[0])
+    a = _args(d)
+    a[11] = 4                                           # max_nodes below the other sequences' counts
+    out = torch.full((15, 8 * 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    fq.attention_tree(*a, out=out)
+    assert fq.check_device_error() == RANGE
+    _check(out, d, seqs=[0])
+    assert (out[8] == 3.0).all() and (out[13:] == 3.0).all()
+
+
+def test_same_call_same_bits():
+    d = _case(32, 8, 128, [16, 3, 9, 11], [3000, 700, 5000, 64], 16, seed=63)
+    a = _args(d)
+    o = fq.attention_tree(*a)
+    ws = torch.full((fq.attention_tree_workspace_bytes(4, 32, 8, 128, 16, d["max_len"]) + 16,), 255,
+                    dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        assert torch.equal(fq.attention_tree(*a, workspace=ws), o)
+
+
+def test_captured_and_replayed_with_other_lengths():
+    """One graph, replayed with the lengths, tables, masks and codes of another batch; a second graph
+    over the same workspace in between."""
+    d1 = _case(8, 2, 128, [4, 9, 2, 7], [500, 30, 0, 64], 16, seed=64)
+    d2 = _case(8, 2, 128, [1, 9, 12, 0], [20, 400, 90, 3], 16, seed=65)
+    for d in (d1, d2):                                  # one capacity for both
+        d["max_nodes"], d["max_len"] = 12, 600
+    a1, a2 = _args(d1), _args(d2)
+    width = -(-600 // 16)
+    fixed = [torch.zeros((22, 8 * 128), dtype=torch.uint8, device="cuda"),
+             torch.zeros((max(len(d1["k"]), len(d2["k"])), 256), dtype=torch.uint8, device="cuda"),
+             torch.zeros((max(len(d1["k"]), len(d2["k"])), 256), dtype=torch.uint8, device="cuda"),
+             a1[3], i32(np.full((4, width), -1)), i32(np.zeros(4)), i32(np.zeros(5)),
+             torch.zeros((22, 1), dtype=torch.int64, device="cuda"), *a1[8:]]
+    out = torch.zeros((22, 8 * 128), dtype=torch.bfloat16, device="cuda")
+    other = torch.zeros_like(out)
+    ws = torch.empty(max(16, fq.attention_tree_workspace_bytes(4, 8, 2, 128, 12, 600)),
+                     dtype=torch.uint8, device="cuda")
+    fq.attention_tree(*fixed, workspace=ws, out=out)
+    graphs = []
+    for o in (out, other):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            fq.attention_tree(*fixed, workspace=ws, out=o)
+        graphs.append(g)
+    for d, a in ((d1, a1), (d2, a2), (d1, a1)):
+        for i in (0, 1, 2, 7):
+            fixed[i][:a[i].shape[0]] = a[i]
+        fixed[4][:, :a[4].shape[1]] = a[4]
+        fixed[5].copy_(a[5])
+        fixed[6].copy_(a[6])
+        for g in graphs:
+            g.replay()
+        _check(out[:sum(d["nodes"])], d)
+        assert torch.equal(out[:sum(d["nodes"])], other[:sum(d["nodes"])])
+    assert fq.check_device_error() == 0
+
+
+def test_on_another_stream():
+    d = _case(8, 2, 128, [4, 9], [500, 30], 16, seed=66)
+    a = _args(d)
+    o = fq.attention_tree(*a)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    outs = [fq.attention_tree(*a, stream=s) for _ in range(20)]
+    torch.cuda.current_stream().wait_stream(s)
+    for x in outs:
+        assert torch.equal(x, o)
+
+
+def test_speculative_step_end_to_end():
+    """Tables, positions, cache write, tree attention, acceptance, and the next step's decode over the
+    moved rows, each from the device results of the one before, against the oracle."""
+    Hq, Hkv, D, bs, B = 8, 2, 128, 16, 3
+    rng = np.random.default_rng(67)
+    ctx, nodes = np.array([37, 0, 90]), [6, 3, 8]
+    trees = [[-1, 0, 0, 1, 2, 2], [-1, 0, 1], [-1, -1, 0, 1, 2, 3, 4, 4]]
+    paths = [[0, 2, 5], [0], [1, 3, 5]]
+    table = np.full((B, 8), -1, np.int32)
+    table[0, :3], table[2, :6] = [4, 9, 1], [0, 7, 2, 11, 3, 5]
+    free = np.array([14, 8, 13, 6, 10, 12], np.int32)
+    slots_n, s3 = 16 * bs, np.array([0.02, 0.03, 0.01], np.float32)
+    k, v = _codes((slots_n, Hkv * D), rng), _codes((slots_n, Hkv * D), rng)
+    dk, dv, dbt, dctx, ds3 = dev(k), dev(v), i32(table), i32(ctx), dev(s3)
+    cu, lens, slots, _, left = fq.paged_batch_tables(dctx, i32(nodes), dbt, i32(free), i32([6]), bs,
+                                                     20)
+    total = sum(nodes)
+    mask, pos = fq.tree_mask(i32(np.concatenate(trees + [[0, 0, 0]])), cu, 8, ctx_lens=dctx)
+    qkv = torch.from_numpy(rng.standard_normal((20, (Hq + 2 * Hkv) * D), dtype=np.float32)) \
+        .to(torch.bfloat16).cuda()
+    q = fq.kv_cache_write(qkv, Hq, Hkv, D, slots, ds3, dk, dv)
+    o = fq.attention_tree(q, dk, dv, ds3, dbt, dctx, cu, mask, Hq, Hkv, bs, 8, 128)
+    path = np.full((B, 4), -1, np.int32)
+    for b, p in enumerate(paths):
+        path[b, :len(p)] = p
+    plen = np.array([len(p) for p in paths])
+    hk, hv = dk.cpu().numpy().copy(), dv.cpu().numpy().copy()
+    new_ctx = fq.kv_cache_accept(dk, dv, dbt, dctx, cu, i32(path), i32(plen), bs)
+    assert fq.check_device_error() == 0
+
+    wt, wcu, _, wslots, _, wleft = spec.batch_tables(ctx, nodes, table, bs, free, 6, 20)
+    np.testing.assert_array_equal(dbt.cpu().numpy(), wt)
+    np.testing.assert_array_equal(slots.cpu().numpy(), wslots)
+    assert left.item() == wleft
+    bits = qkv.cpu().view(torch.int16).numpy().view(np.uint16)
+    wq = oracle.kv_cache_write(bits, Hq, Hkv, D, wslots, s3, k, v)
+    np.testing.assert_array_equal(hk, k)
+    np.testing.assert_array_equal(hv, v)
+    np.testing.assert_array_equal(q.cpu().numpy(), wq)
+    sees = [spec.tree_sees(t) for t in trees]
+    depth = np.concatenate([s.sum(1) - 1 + c for s, c in zip(sees, ctx)])
+    np.testing.assert_array_equal(pos.cpu().numpy()[:total], depth)
+    d = dict(Hq=Hq, Hkv=Hkv, D=D, bs=bs, ctx=ctx, nodes=nodes, table=wt, sees=sees, k=k, v=v, s3=s3,
+             q=[wq[wcu[b]:wcu[b + 1]] for b in range(B)])
+    _check(o[:total], d)
+    (wk, wv), wctx = spec.accept([k, v], wt, ctx, path, plen, bs)
+    np.testing.assert_array_equal(dk.cpu().numpy(), wk)
+    np.testing.assert_array_equal(dv.cpu().numpy(), wv)
+    np.testing.assert_array_equal(new_ctx.cpu().numpy(), wctx)
+    # the accepted path is now an ordinary context: one decode step sees the same rows as the path's
+    # last node did, in the order of the path
+    last = torch.stack([q[wcu[b] + paths[b][-1]] for b in range(B)])
+    step = fq.attention_decode(last, dk, dv, ds3, dbt, new_ctx, Hq, Hkv, bs, 128)
+    one = dict(d, ctx=wctx - 1, nodes=[1] * B, sees=[np.ones((1, 1), bool)] * B, k=wk, v=wv,
+               q=[last[b:b + 1].cpu().numpy() for b in range(B)])
+    _check(step, one)
+    np.testing.assert_allclose(host_bf16_f64(step),
+                               host_bf16_f64(o)[[wcu[b] + paths[b][-1] for b in range(B)]],
+                               rtol=2.0 ** -6, atol=2.0 ** -8)

@@ -1,0 +1,273 @@
+"""GPU parity of the integer operators of a speculative-decoding step (block tables and slot maps,
+ancestor masks, the move of accepted rows) against the oracle, equal to the last bit: batches from one
+request to more than a CTA's threads, block sizes 1, 5, 16 and 64, empty requests and trees, padded
+capacities, chains of 1024 nodes, overlapping moves, and inputs that break a rule (recorded, clamped,
+nothing outside the buffers)."""
+import numpy as np
+import pytest
+import torch
+
+import fp8_blockwise_w8a8_b200 as fq
+from oracle import speculative as spec
+
+pytestmark = pytest.mark.gpu
+RANGE = 9
+
+
+def i32(a):
+    return torch.from_numpy(np.ascontiguousarray(a, np.int32)).cuda()
+
+
+def host(t):
+    return t.cpu().numpy()
+
+
+# --- block tables and slot maps ------------------------------------------------------------------
+
+def _tables_case(B, bs, ctx_hi, new_hi, seed, spare=7):
+    rng = np.random.default_rng(seed)
+    ctx, new = rng.integers(0, ctx_hi + 1, B), rng.integers(0, new_hi + 1, B)
+    have, want = -(-ctx // bs), -(-(ctx + new) // bs)
+    perm = rng.permutation(int(want.sum()) + spare).astype(np.int32)
+    table = np.full((B, max(1, int(want.max(initial=0))) + 1), -1, np.int32)
+    at = 0
+    for b in range(B):
+        table[b, :have[b]] = perm[at:at + have[b]]
+        at += have[b]
+    return ctx, new, table, perm[at:]
+
+
+def _check_tables(ctx, new, table, bs, free, count, max_tokens):
+    want = spec.batch_tables(ctx, new, table, bs, free, count, max_tokens)
+    bt = i32(table)
+    cu, lens, slots, pos, left = fq.paged_batch_tables(i32(ctx), i32(new), bt, i32(free),
+                                                       i32([count]), bs, max_tokens)
+    for got, ref in zip((bt, cu, lens, slots, pos, left), want):
+        np.testing.assert_array_equal(host(got), ref)
+
+
+@pytest.mark.parametrize("B,bs,ctx_hi,new_hi", [
+    (1, 16, 0, 1), (1, 5, 40, 3000), (7, 1, 9, 4), (64, 16, 4096, 1), (513, 16, 100, 9),
+    (1500, 64, 500, 40), (3, 16, 20, 20000)])
+def test_tables(B, bs, ctx_hi, new_hi):
+    ctx, new, table, free = _tables_case(B, bs, ctx_hi, new_hi, B + bs)
+    total = int(new.sum())
+    _check_tables(ctx, new, table, bs, free, len(free), total + 77)
+    _check_tables(ctx, new, table, bs, free, len(free) - 3, total)
+    assert fq.check_device_error() == 0
+
+
+def test_tables_largest_batch():
+    ctx, new, table, free = _tables_case(16384, 16, 30, 3, 1)
+    _check_tables(ctx, new, table, 16, free, len(free), int(new.sum()) + 1)
+    assert fq.check_device_error() == 0
+
+
+def test_tables_no_requests_and_no_tokens():
+    e = np.zeros(0, np.int32)
+    cu, lens, slots, pos, left = fq.paged_batch_tables(i32(e), i32(e), i32(np.zeros((0, 3))),
+                                                       i32([4, 2]), i32([2]), 16, 5)
+    assert host(cu).tolist() == [0] and host(left).tolist() == [2]
+    assert host(slots).tolist() == [-1] * 5 and host(pos).tolist() == [0] * 5
+    cu, lens, slots, pos, left = fq.paged_batch_tables(i32([5, 0]), i32([0, 0]),
+                                                       i32([[1], [-1]]), i32(e), i32([0]), 16, 0)
+    assert host(cu).tolist() == [0, 0, 0] and host(lens).tolist() == [5, 0]
+    assert slots.numel() == 0 and host(left).tolist() == [0]
+    assert fq.check_device_error() == 0
+
+
+def test_tables_free_stack_too_short():
+    ctx, new, table, free = _tables_case(40, 16, 100, 50, 5)
+    total = int(new.sum())
+    _check_tables(ctx, new, table, 16, free, 20, total)
+    assert fq.check_device_error() == RANGE
+    _check_tables(ctx, new, table, 16, free, 0, total)
+    assert fq.check_device_error() == RANGE and fq.check_device_error() == 0
+
+
+def test_tables_lengths_out_of_range():
+    """A negative length counts as 0, one beyond the table is cut at its end, tokens beyond max_tokens
+    are cut off, and a stack height outside the stack is clamped; all recorded."""
+    table = np.array([[3, -1], [5, -1], [0, -1], [6, -1]], np.int32)
+    args = lambda ctx, new, count, cap: (i32(ctx), i32(new), i32(table), i32([9, 8, 7]),
+                                         i32([count]), 4, cap)
+    out = fq.paged_batch_tables(*args([-2, 3, 2, 4], [2, -1, 99, 0], 3, 9))
+    assert fq.check_device_error() == RANGE
+    assert host(out[0]).tolist() == [0, 2, 2, 8, 8] and host(out[1]).tolist() == [2, 3, 8, 4]
+    # request 0 starts at 0: its first block is new (7); request 2 goes on in block 0, then 8
+    assert host(out[2]).tolist() == [28, 29, 2, 3, 32, 33, 34, 35, -1]
+    assert host(out[3]).tolist() == [0, 1, 2, 3, 4, 5, 6, 7, 0] and host(out[4]).tolist() == [1]
+    out = fq.paged_batch_tables(*args([1, 3, 1, 1], [2, 2, 2, 2], 3, 5))       # 8 tokens into 5
+    assert fq.check_device_error() == RANGE
+    assert host(out[0]).tolist() == [0, 2, 4, 5, 5] and host(out[1]).tolist() == [3, 5, 2, 1]
+    assert host(out[2]).tolist() == [13, 14, 23, 28, 1] and host(out[4]).tolist() == [2]
+    out = fq.paged_batch_tables(*args([4, 4, 4, 4], [1, 0, 0, 0], 4, 1))       # 4 of 3 entries
+    assert fq.check_device_error() == RANGE
+    assert host(out[2]).tolist() == [28] and host(out[4]).tolist() == [2]
+
+
+def test_tables_step_after_step_in_a_graph():
+    """A captured decode step, replayed: the results become the next step's inputs on the device."""
+    B, bs, cap = 5, 4, 12
+    rng = np.random.default_rng(8)
+    ctx, new = i32([0, 3, 4, 11, 6]), i32([1, 2, 0, 3, 1])
+    table = np.full((B, 16), -1, np.int32)
+    free = rng.permutation(80).astype(np.int32)
+    for b, c in enumerate(host(ctx)):
+        table[b, :-(-c // bs)] = 100 + 10 * b + np.arange(-(-c // bs))
+    bt, fb, count = i32(table), i32(free), i32([80])
+    out = fq.paged_batch_tables(ctx, new, bt.clone(), fb, count, bs, cap)      # buffers
+    g = torch.cuda.CUDAGraph()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(g, stream=s):
+        fq.paged_batch_tables(ctx, new, bt, fb, count, bs, cap, out=out)
+        ctx.copy_(out[1])
+        count.copy_(out[4])
+    c, t, k = host(ctx).copy(), table, 80
+    for step in range(6):
+        n = rng.integers(0, 3, B)
+        new.copy_(i32(n))
+        g.replay()
+        t, cu, lens, slots, pos, k = spec.batch_tables(c, n, t, bs, free, k, cap)
+        for got, ref in zip((bt, *out), (t, cu, lens, slots, pos, k)):
+            np.testing.assert_array_equal(host(got), ref)
+        c = lens
+    assert fq.check_device_error() == 0
+
+
+# --- ancestor masks -------------------------------------------------------------------------------
+
+def _parents(n, rng, kind):
+    if kind == "chain":
+        return np.arange(-1, n - 1)
+    if kind == "star":
+        return np.full(n, -1)
+    return np.array([rng.integers(max(-1, i - 9), i) for i in range(n)], np.int64)
+
+
+def _check_mask(sizes, max_nodes, kind, seed, pad=0):
+    rng = np.random.default_rng(seed)
+    trees = [_parents(n, rng, kind) for n in sizes]
+    words = -(-max_nodes // 64)
+    cu = np.concatenate([[0], np.cumsum(sizes)])
+    total = int(cu[-1]) + pad
+    parents = np.concatenate(trees + [np.full(pad, 10 ** 6)])
+    ctx = rng.integers(0, 10 ** 6, len(sizes))
+    mask = torch.full((total, words + 1), -7, dtype=torch.int64, device="cuda")
+    pos = torch.full((total,), -7, dtype=torch.int64, device="cuda")
+    fq.tree_mask(i32(parents), i32(cu), max_nodes, ctx_lens=i32(ctx), out_mask=mask[:, :words],
+                 out_positions=pos)
+    want, wpos = np.full((total, words + 1), -7), np.full(total, -7)
+    for b, t in enumerate(trees):
+        sees = spec.tree_sees(t)
+        want[cu[b]:cu[b + 1], :words] = spec.pack_bits(sees, words)
+        wpos[cu[b]:cu[b + 1]] = ctx[b] + sees.sum(1) - 1
+    np.testing.assert_array_equal(host(mask), want)
+    np.testing.assert_array_equal(host(pos), wpos)
+    assert fq.check_device_error() == 0
+
+
+@pytest.mark.parametrize("kind", ["random", "chain", "star"])
+@pytest.mark.parametrize("sizes,max_nodes", [
+    ([1], 1), ([0, 1, 2, 0, 16, 7], 16), ([63, 64, 65, 1], 65), ([256, 3, 0, 200], 256),
+    ([257, 511], 512), ([1024, 1, 1000], 1024)])
+def test_mask(sizes, max_nodes, kind):
+    _check_mask(sizes, max_nodes, kind, 3, pad=5)
+
+
+def test_mask_many_sequences():
+    rng = np.random.default_rng(4)
+    _check_mask(rng.integers(0, 12, 3000).tolist(), 40, "random", 5)
+
+
+def test_mask_without_contexts_and_nodes():
+    mask, pos = fq.tree_mask(i32([-1, 0, 0]), i32([0, 3]), 8)
+    assert host(mask)[:, 0].tolist() == [1, 3, 5] and host(pos).tolist() == [0, 1, 1]
+    mask, pos = fq.tree_mask(i32(np.zeros(0)), i32([0, 0]), 8)
+    assert mask.shape == (0, 1) and pos.shape == (0,)
+    assert fq.check_device_error() == 0
+
+
+def test_mask_bad_parents_and_offsets():
+    """A parent that is not before its child counts as the context; a sequence above max_nodes is
+    written up to there; offsets outside the rows are clamped."""
+    mask, _ = fq.tree_mask(i32([-1, 1, -2, 2]), i32([0, 4]), 4)
+    assert fq.check_device_error() == RANGE
+    assert host(mask)[:, 0].tolist() == [1, 2, 4, 12]
+    out = torch.full((6, 1), -7, dtype=torch.int64, device="cuda")
+    fq.tree_mask(i32([-1, 0, 1, 2, -1, 0]), i32([0, 4, 99]), 3, out_mask=out)
+    assert fq.check_device_error() == RANGE
+    assert host(out)[:, 0].tolist() == [1, 3, 7, -7, 1, 3]
+    out.fill_(-7)
+    fq.tree_mask(i32([-1, 0, 1, 2, -1, 0]), i32([-3, 2, 1]), 3, out_mask=out)
+    assert fq.check_device_error() == RANGE
+    assert host(out)[:, 0].tolist() == [1, 3, -7, -7, -7, -7]
+
+
+# --- accepted rows --------------------------------------------------------------------------------
+
+def _accept_case(B, bs, row, layers, seed, n_hi=20, path_hi=12):
+    rng = np.random.default_rng(seed)
+    n, ctx = rng.integers(0, n_hi + 1, B), rng.integers(0, 50, B)
+    width = max(1, int((-(-(ctx + n) // bs)).max()))
+    table = rng.permutation(B * width + 3)[:B * width].reshape(B, width).astype(np.int32)
+    slots = (B * width + 3) * bs
+    k, v = (rng.integers(0, 256, (layers, slots, row)).astype(np.uint8) for _ in range(2))
+    path, plen = np.full((B, path_hi), -9, np.int32), np.zeros(B, np.int32)
+    for b in range(B):
+        plen[b] = rng.integers(0, min(path_hi, n[b]) + 1)
+        path[b, :plen[b]] = np.sort(rng.permutation(n[b])[:plen[b]])
+    return k, v, table, ctx, n, path, plen
+
+
+@pytest.mark.parametrize("B,bs,row,layers", [
+    (1, 16, 16, 1), (9, 1, 48, 2), (30, 7, 1024, 1), (12, 64, 272, 5), (3, 16, 4096, 2)])
+def test_accept(B, bs, row, layers):
+    k, v, table, ctx, n, path, plen = _accept_case(B, bs, row, layers, B)
+    (wk, wv), lens = spec.accept([k, v], table, ctx, path, plen, bs)
+    dk, dv = torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda()
+    cu = i32(np.concatenate([[0], np.cumsum(n)]))
+    if layers == 1:
+        dk, dv = dk[0], dv[0]
+        wk, wv = wk[0], wv[0]
+    got = fq.kv_cache_accept(dk, dv, i32(table), i32(ctx), cu, i32(path), i32(plen), bs)
+    np.testing.assert_array_equal(host(got), lens)
+    np.testing.assert_array_equal(host(dk), wk)
+    np.testing.assert_array_equal(host(dv), wv)
+    assert fq.check_device_error() == 0
+
+
+def test_accept_long_overlapping_path():
+    """1000 of 1024 nodes, in place from some index on, shifted by ever more behind it."""
+    rng = np.random.default_rng(6)
+    path = np.sort(rng.permutation(1024)[:1000])
+    path[:30] = np.arange(30)
+    k = rng.integers(0, 256, (1, 1100, 32)).astype(np.uint8)
+    table = rng.permutation(110).reshape(1, 110).astype(np.int32)
+    (wk, wv), lens = spec.accept([k, k], table, [13], [path], [1000], 10)
+    dk, dv = torch.from_numpy(k).cuda(), torch.from_numpy(k).cuda()
+    fq.kv_cache_accept(dk, dv, i32(table), i32([13]), i32([0, 1024]), i32(path[None]), i32([1000]), 10)
+    np.testing.assert_array_equal(host(dk), wk)
+    np.testing.assert_array_equal(host(dv), wv)
+    assert fq.check_device_error() == 0
+
+
+def test_accept_bad_paths_move_nothing():
+    """Paths that repeat or fall, leave the nodes or are too long, a bad block and a bad context: those
+    sequences keep their rows and lengths, the good one beside them moves."""
+    B, bs = 7, 4
+    rng = np.random.default_rng(7)
+    table = np.arange(B * 4).reshape(B, 4).astype(np.int32)
+    k = rng.integers(0, 256, (B * 16, 16)).astype(np.uint8)
+    path = np.array([[0, 2, 2], [2, 1, 3], [0, 1, 5], [0, 2, 4], [0, 2, 4], [0, 2, 4], [0, 2, 4]])
+    plen, ctx = [3, 3, 3, 4, 3, 3, 3], [1, 2, 3, 4, 5, 14, 7]
+    table[4, 2] = 10 ** 6                               # holds the accepted node 4 of sequence 4
+    (wk, _), _ = spec.accept([k, k], table[6:], [7], path[6:], [3], bs)
+    dk, dv = torch.from_numpy(k).cuda(), torch.from_numpy(k).cuda()
+    got = fq.kv_cache_accept(dk, dv, i32(table), i32(ctx), i32(np.arange(B + 1) * 5), i32(path),
+                             i32(plen), bs)
+    assert fq.check_device_error() == RANGE
+    assert host(got).tolist() == [1, 2, 3, 4, 5, 14, 10]
+    np.testing.assert_array_equal(host(dk), wk)
+    np.testing.assert_array_equal(host(dv), wk)

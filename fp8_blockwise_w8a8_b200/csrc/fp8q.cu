@@ -124,7 +124,11 @@ int device_state(DeviceState **out) {
                              kTablesMaxSmem) != cudaSuccess ||
         cudaFuncSetAttribute(fp8q::k_tree_mask<1024>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             tree_mask_smem(fp8q::kTreeMaxNodes)) != cudaSuccess)
+                             tree_mask_smem(fp8q::kTreeMaxNodes)) != cudaSuccess ||
+        cudaFuncSetAttribute(fp8q::k_tree_attn<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             fp8q::TreeLayout<128>::kSmem) != cudaSuccess ||
+        cudaFuncSetAttribute(fp8q::k_tree_attn<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             fp8q::TreeLayout<64>::kSmem) != cudaSuccess)
       return FP8Q_ERR_LAUNCH;
     st.attrs_set = true;
   }
@@ -380,10 +384,27 @@ int tree_attn_shape_status(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_
   return FP8Q_OK;
 }
 
+// CTAs of the tree attention at most: two per SM, and no more than the sizes can give work.
+int64_t tree_attn_ctas(int64_t B, int64_t Hq, int64_t Hkv, int64_t max_nodes,
+                       int64_t max_seq_len) {
+  const int64_t row_tiles = (max_nodes * (Hq / Hkv) + fp8q::kTreeM - 1) / fp8q::kTreeM;
+  const int64_t cost = B * Hkv * row_tiles *
+                       (max_seq_len / fp8q::kTreeN + 1 + fp8q::kTreeItemCost);
+  const int64_t most = (cost + fp8q::kTreeMinCost - 1) / fp8q::kTreeMinCost;
+  return most < fp8q::kTreeMaxCtas ? most : fp8q::kTreeMaxCtas;
+}
+
+int64_t tree_attn_row_cap(int64_t Hq, int64_t Hkv, int64_t max_nodes) {
+  const int64_t rows = max_nodes * (Hq / Hkv);
+  return rows < fp8q::kTreeM ? (rows + 1) / 2 * 2 : fp8q::kTreeM;  // even: 16-byte aligned slots
+}
+
+// Per CTA: what its pieces are, and two partial states of row_cap rows.
 int64_t tree_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
                                   int64_t max_nodes, int64_t max_seq_len) {
-  if (B == 0 || max_nodes == 0 || max_seq_len == 0) return 0;
-  return 16;
+  if (B == 0 || max_nodes == 0) return 0;
+  return tree_attn_ctas(B, Hq, Hkv, max_nodes, max_seq_len) *
+         (4 * fp8q::kTreeMetaInts + 8 * tree_attn_row_cap(Hq, Hkv, max_nodes) * (D + 2));
 }
 
 
@@ -1060,7 +1081,7 @@ int fp8q_paged_batch_tables(const int32_t *ctx_lens, const int32_t *new_lens, in
 int fp8q_tree_mask(const int32_t *parents, const int32_t *cu_nodes, const int32_t *ctx_lens,
                    int64_t B, int64_t total, int64_t max_nodes, int64_t *mask, int64_t ldm,
                    int64_t *positions, cudaStream_t stream) {
-  if (B < 0 || B > INT32_MAX || total < 0 || total > INT32_MAX || max_nodes < 0 ||
+  if (B < 0 || B > 65535 || total < 0 || total > INT32_MAX || max_nodes < 0 ||
       max_nodes > fp8q::kTreeMaxNodes)
     return FP8Q_ERR_SHAPE;
   const int64_t words = (max_nodes + 63) / 64;
@@ -1150,13 +1171,35 @@ int fp8q_attention_tree(const void *q_e4m3, int64_t ldq, const void *k_cache, co
   a.max_nodes = static_cast<int>(max_nodes);
   a.max_seq_len = static_cast<int>(max_seq_len);
   a.sm_scale = sm_scale;
-  a.ws = static_cast<float *>(workspace);
   a.out = static_cast<uint16_t *>(out_bf16);
   a.ldo = ldo;
-  const dim3 grid(static_cast<unsigned>((max_nodes + 3) / 4), static_cast<unsigned>(Hq),
-                  static_cast<unsigned>(B));
-  if (D == 128) fp8q::k_tree_attn<128><<<grid, 128, 0, stream>>>(a);
-  else fp8q::k_tree_attn<64><<<grid, 128, 0, stream>>>(a);
+  const int64_t ctas = tree_attn_ctas(B, Hq, Hkv, max_nodes, max_seq_len);
+  a.row_cap = static_cast<int>(tree_attn_row_cap(Hq, Hkv, max_nodes));
+  a.meta = static_cast<int32_t *>(workspace);
+  a.part = reinterpret_cast<float *>(a.meta + ctas * fp8q::kTreeMetaInts);
+  const unsigned grid = static_cast<unsigned>(ctas < 2 * st->sms ? ctas : 2 * st->sms);
+  if (D == 128)
+    fp8q::k_tree_attn<128><<<grid, fp8q::kTreeThreads, fp8q::TreeLayout<128>::kSmem, stream>>>(a);
+  else
+    fp8q::k_tree_attn<64><<<grid, fp8q::kTreeThreads, fp8q::TreeLayout<64>::kSmem, stream>>>(a);
+  if ((rc = launch_status()) != FP8Q_OK) return rc;
+  // the merge as a programmatic dependent launch: scheduled while the first kernel drains
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, static_cast<unsigned>((a.row_cap + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t err = D == 128
+                              ? cudaLaunchKernelEx(&cfg, fp8q::k_tree_attn_combine<128>, a)
+                              : cudaLaunchKernelEx(&cfg, fp8q::k_tree_attn_combine<64>, a);
+  if (err != cudaSuccess) {
+    cudaGetLastError();
+    return FP8Q_ERR_LAUNCH;
+  }
   return launch_status();
 }
 

@@ -176,7 +176,8 @@ __device__ __forceinline__ int tree_rows(const int32_t *cu, int b, int64_t total
   return static_cast<int>(n);
 }
 
-// One CTA per sequence.  Bit j of row i is set iff j is i or an ancestor of i.  Pointer doubling:
+// One CTA per sequence, which also looks through the offsets up to its own: where they decrease the
+// batch ends, so that no two sequences write the same rows.  Bit j of row i is set iff j is i or an ancestor of i.  Pointer doubling:
 // row i holds the nodes from i up to (not including) anc[i]; a round ORs in the row of anc[i] and
 // jumps to anc[anc[i]], so a tree of depth d takes ceil(log2 d) rounds instead of d steps.  Each
 // round reads into registers, then writes, so no row is read while it changes.
@@ -185,8 +186,9 @@ __global__ void __launch_bounds__(T) k_tree_mask(const TreeMaskArgs a) {
   extern __shared__ uint64_t s_bits[];                         // [n][W], then anc [n]
   const int b = blockIdx.x, tid = threadIdx.x, W = a.words;
   int64_t first;
-  bool bad;
+  bool bad, falls = false;
   const int n = tree_rows(a.cu, b, a.total, a.max_nodes, &first, &bad);
+  for (int i = tid; i <= b; i += T) falls |= a.cu[i + 1] < a.cu[i];
   int32_t *s_anc = reinterpret_cast<int32_t *>(s_bits + static_cast<int64_t>(a.max_nodes) * W);
   for (int i = tid; i < n; i += T) {
     int p = a.parents[first + i];
@@ -198,7 +200,7 @@ __global__ void __launch_bounds__(T) k_tree_mask(const TreeMaskArgs a) {
     for (int w = 0; w < W; ++w) s_bits[i * W + w] = w == i / 64 ? 1ull << (i % 64) : 0ull;
   }
   if (bad) record_error(9 /* FP8Q_ERR_RANGE */);
-  __syncthreads();
+  if (__syncthreads_or(falls)) return;
   const int items = n * W;
   for (;;) {
     uint64_t add[kTreeMaskItems];

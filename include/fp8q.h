@@ -377,9 +377,10 @@ int fp8q_paged_batch_tables(const int32_t *ctx_lens, const int32_t *new_lens, in
  *   ctx_lens   [B] int32 or NULL (zeros); positions [total] int64 or NULL, written: ctx_lens[b]
  *              plus the node's depth (0 for a child of the context), its rotary position
  *   max_nodes  a HOST bound on the nodes of a sequence, <= 1024
- * Recorded as FP8Q_ERR_RANGE: a parent outside [-1, i) (taken as -1); offsets that decrease or
- * leave [0, total], a sequence of more than max_nodes nodes (the rest of its rows are not written).
- * Rows behind the last sequence are left as they were.  B, total <= 2^31 - 1. */
+ * Recorded as FP8Q_ERR_RANGE: a parent outside [-1, i) (taken as -1); offsets that leave [0, total]
+ * (clamped); a sequence of more than max_nodes nodes (the rest of its rows are not written); offsets
+ * that decrease, cu_nodes[b + 1] < cu_nodes[b] (the batch ends before sequence b).  Rows behind the
+ * last sequence are left as they were.  B <= 65535, total <= 2^31 - 1. */
 int fp8q_tree_mask(const int32_t *parents, const int32_t *cu_nodes, const int32_t *ctx_lens,
                    int64_t B, int64_t total, int64_t max_nodes, int64_t *mask, int64_t ldm,
                    int64_t *positions, cudaStream_t stream);

@@ -164,6 +164,20 @@ int make_u8_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, 
   return r == CUDA_SUCCESS ? FP8Q_OK : FP8Q_ERR_LAUNCH;
 }
 
+// 2-D uint8 tensor map over the cache's rows [rows][cols], box = box_rows rows of box_cols bytes.
+int make_u8_row_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols,
+                    uint32_t box_rows, uint32_t box_cols, CUtensorMapSwizzle swizzle) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols)};
+  const cuuint32_t box[2] = {box_cols, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base),
+                              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FP8Q_OK : FP8Q_ERR_LAUNCH;
+}
+
 // 2-D bf16 tensor map over a row-major [rows][ld] output, box = 32 rows x 64 columns (128 bytes),
 // 128-byte swizzle: the tile-store target of the block GEMM.
 int make_bf16_out_map(CUtensorMap *map, void *base, int64_t rows, int64_t cols, int64_t ld) {
@@ -382,6 +396,12 @@ int tree_attn_shape_status(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_
       max_seq_len < 0 || max_seq_len > INT32_MAX - 128)
     return FP8Q_ERR_SHAPE;
   return FP8Q_OK;
+}
+
+fp8q::TreeDiv tree_div(int64_t d) {
+  uint32_t l = 0;
+  while ((int64_t{1} << l) < d) ++l;
+  return {static_cast<uint32_t>((uint64_t{1} << (31 + l)) / static_cast<uint64_t>(d) + 1), 31 + l};
 }
 
 // CTAs of the tree attention at most: two per SM, and no more than the sizes can give work.
@@ -1178,10 +1198,29 @@ int fp8q_attention_tree(const void *q_e4m3, int64_t ldq, const void *k_cache, co
   a.meta = static_cast<int32_t *>(workspace);
   a.part = reinterpret_cast<float *>(a.meta + ctas * fp8q::kTreeMetaInts);
   const unsigned grid = static_cast<unsigned>(ctas < 2 * st->sms ? ctas : 2 * st->sms);
+  // rows per copy; blocks without a power of two of 4 or more go by gathers (box of one row)
+  const int64_t pow2 = block_size & -block_size;
+  a.box = static_cast<int>(pow2 > 64 ? 64 : pow2);
+  const uint32_t box = a.box < 4 ? 1 : static_cast<uint32_t>(a.box);
+  a.by_block = tree_div(block_size);
+  a.by_group = tree_div(Hq / Hkv);
+  // a cache without slots: every position is out of range and loads row 0, here of q
+  const void *k_rows = num_slots > 0 ? k_cache : q_e4m3, *v_rows = num_slots > 0 ? v_cache : q_e4m3;
+  const int64_t map_rows = num_slots > 0 ? num_slots : 1;
+  CUtensorMap tm_k, tm_v;
+  if ((rc = get_encoder()) != FP8Q_OK ||
+      (rc = make_u8_row_map(&tm_k, k_rows, map_rows, Hkv * D, box, static_cast<uint32_t>(D),
+                            D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B)) !=
+          FP8Q_OK ||
+      (rc = make_u8_row_map(&tm_v, v_rows, map_rows, Hkv * D, box, static_cast<uint32_t>(D),
+                            CU_TENSOR_MAP_SWIZZLE_NONE)) != FP8Q_OK)
+    return rc;
   if (D == 128)
-    fp8q::k_tree_attn<128><<<grid, fp8q::kTreeThreads, fp8q::TreeLayout<128>::kSmem, stream>>>(a);
+    fp8q::k_tree_attn<128><<<grid, fp8q::kTreeThreads, fp8q::TreeLayout<128>::kSmem, stream>>>(
+        tm_k, tm_v, a);
   else
-    fp8q::k_tree_attn<64><<<grid, fp8q::kTreeThreads, fp8q::TreeLayout<64>::kSmem, stream>>>(a);
+    fp8q::k_tree_attn<64><<<grid, fp8q::kTreeThreads, fp8q::TreeLayout<64>::kSmem, stream>>>(
+        tm_k, tm_v, a);
   if ((rc = launch_status()) != FP8Q_OK) return rc;
   // the merge as a programmatic dependent launch: scheduled while the first kernel drains
   cudaLaunchConfig_t cfg = {};

@@ -17,6 +17,15 @@
 
 namespace fp8q {
 
+// p / d as p * mul >> shift for 0 <= p < 2^31: mul = floor(2^(31 + l) / d) + 1 and shift = 31 + l, where
+// 2^l >= d is the least power of two.
+struct TreeDiv {
+  uint32_t mul, shift;
+  __device__ __forceinline__ int operator()(int p) const {
+    return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(p)) * mul >> shift);
+  }
+};
+
 struct TreeAttnArgs {
   const uint8_t *q;            // [total][ldq] codes
   int64_t ldq;
@@ -33,6 +42,8 @@ struct TreeAttnArgs {
   float sm_scale;
   uint16_t *out;               // [total][ldo] bf16
   int64_t ldo;
+  int box;                     // rows per copy: the power of two in block_size, at most 64; 1: gathers
+  TreeDiv by_block, by_group;  // by block_size and by G = Hq / Hkv
   int row_cap;                 // rows of a partial slot: min(128, max_nodes * Hq / Hkv)
   int32_t *meta;               // [CTAs][kTreeMetaInts]
   float *part;                 // [CTAs][2][row_cap][D + 2]: o, then m, l
@@ -64,10 +75,9 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeAttnArgs &a, int b, bool r
 // ---------------------------------------------------------------------------------------------
 constexpr int kTreeM = 128;          // query rows (node, head of the group) per row tile: TMEM lanes
 constexpr int kTreeN = 64;           // cached positions per tile
-constexpr int kTreeThreads = 288;    // 4 softmax warps, 4 load warps, 1 MMA warp
+constexpr int kTreeThreads = 320;    // 4 softmax warps, 4 convert warps, MMA warp, load warp
 constexpr int kTreeMaxCtas = 296;    // 2 per SM of 148
-constexpr int kTreeKStages = 3;      // K tiles in shared memory; 2 in flight ahead of the one in use
-constexpr int kTreeAhead = 2;
+constexpr int kTreeStages = 3;       // K and V tiles (codes) in shared memory
 constexpr int kTreeItemCost = 2;     // cost of starting a row tile, in position tiles
 constexpr int kTreeMinCost = 4;      // least cost per CTA
 constexpr int kTreeMetaInts = 8;
@@ -77,11 +87,12 @@ constexpr float kTreeBias = 7.0f;    // weights are 2^(z - reference + 7): at mo
 template <int D>
 struct TreeLayout {
   static constexpr int kQ = 0;                                   // [128][128 B], swizzled
-  static constexpr int kK = kQ + kTreeM * 128;                   // [stage][64][128 B], swizzled
-  static constexpr int kV16 = kK + kTreeKStages * kTreeN * 128;  // [2][D / 64][64][128 B], swizzled
+  static constexpr int kK = kQ + kTreeM * 128;                   // [stage][64][D], swizzled
+  static constexpr int kTile = kTreeN * D;
+  static constexpr int kV16 = kK + kTreeStages * kTile;          // [2][D / 64][64][128 B], swizzled
   static constexpr int kV16Bytes = kTreeN * D * 2;
-  static constexpr int kV8 = kV16 + 2 * kV16Bytes;               // [stage][64 * D], by thread
-  static constexpr int kSmem = kV8 + kTreeKStages * kTreeN * D + 1024;
+  static constexpr int kV8 = kV16 + 2 * kV16Bytes;               // [stage][64][D]
+  static constexpr int kSmem = kV8 + kTreeStages * kTile + 1024;
   // TMEM columns: scores, two weight buffers (two fp16 a column), values
   static constexpr int kColS = 0, kColP = 64, kColO = 128, kCols = 256;
   static constexpr uint32_t kIdescQK = (1u << 4) | (static_cast<uint32_t>(kTreeN >> 3) << 17) |
@@ -96,54 +107,56 @@ struct TreeLayout {
 __device__ __forceinline__ int tree_row_tiles(int n, int G) {
   return (n * G + kTreeM - 1) / kTreeM;
 }
-__device__ __forceinline__ int tree_tiles(int n, int ctx, int G, int rt) {
-  const int last = (min(n * G, (rt + 1) * kTreeM) - 1) / G;      // the tile's last node
-  return (ctx + last) / kTreeN + 1;
+__device__ __forceinline__ int tree_tiles(const TreeAttnArgs &a, const TreeSeq &s, int G, int rt) {
+  const int last = a.by_group(min(s.n * G, (rt + 1) * kTreeM) - 1);  // the tile's last node
+  return (s.ctx + last) / kTreeN + 1;
 }
-__device__ __forceinline__ int64_t tree_group_cost(const TreeSeq &s, int G) {
+__device__ __forceinline__ int64_t tree_group_cost(const TreeAttnArgs &a, const TreeSeq &s, int G) {
   int64_t c = 0;
+#pragma unroll 1
   for (int rt = tree_row_tiles(s.n, G) - 1; rt >= 0; --rt)
-    c += tree_tiles(s.n, s.ctx, G, rt) + kTreeItemCost;
+    c += tree_tiles(a, s, G, rt) + kTreeItemCost;
   return c;
 }
 
-// The pieces of work of one CTA: a range of the cost axis on which the items (sequence, kv head, row
-// tile) stand one behind the other, each as long as its position tiles plus kTreeItemCost.  A piece
-// is the range's share of one item: tiles [t, t_end) of nt.
+// A share of one item (sequence, kv head, row tile): its position tiles [t, t_end) of nt.  The load
+// warp hands the pieces of a CTA to the other roles, the last one with t_end = 0.
+struct TreePiece {
+  int64_t first;                 // row of the sequence's node 0
+  int b, n, ctx, g, row0, rows, t, t_end, nt;
+};
+
+// The pieces of work of one CTA: a range of the cost axis on which the items stand one behind the
+// other, each as long as its position tiles plus kTreeItemCost.
 struct TreeCursor {
   TreeSeq s;
   int64_t rem;
   int B, b, g, rt, t, t_end, nt;
   bool live;
 
-  __device__ __forceinline__ void item(int G, int off) {
-    nt = tree_tiles(s.n, s.ctx, G, rt);
-    const int cost = nt + kTreeItemCost;
-    const int64_t take = min(static_cast<int64_t>(cost - off), rem);
-    t = max(0, off - kTreeItemCost);
-    t_end = max(0, off + static_cast<int>(take) - kTreeItemCost);
-    rem -= take;
-  }
+  // From the sequence b0, `off` behind its start; cost 0: nothing.
   __device__ __forceinline__ void init(const TreeAttnArgs &a, int G, int num, int b0, int64_t off,
                                        int64_t cost) {
     B = num;
     rem = cost;
+    b = b0;
+    g = rt = t = t_end = 0;
     live = cost > 0;
     if (!live) return;
-    b = b0;
     s = tree_seq(a, b, false);
-    const int64_t per_g = tree_group_cost(s, G);
+    const int64_t per_g = tree_group_cost(a, s, G);
     g = static_cast<int>(off / per_g);
-    int64_t o = off - g * per_g;
-    for (rt = 0;; ++rt) {
-      const int c = tree_tiles(s.n, s.ctx, G, rt) + kTreeItemCost;
-      if (o < c) break;
-      o -= c;
+    off -= g * per_g;
+    int tiles;
+    while (off >= (tiles = tree_tiles(a, s, G, rt) + kTreeItemCost)) {
+      off -= tiles;
+      ++rt;
     }
-    item(G, static_cast<int>(o));
-    if (t >= t_end) next_piece(a, G);
+    --rt;
+    next(a, G, static_cast<int>(off));
   }
-  __device__ __forceinline__ void next_piece(const TreeAttnArgs &a, int G) {
+  // The next piece, `off` into its item.
+  __device__ __forceinline__ void next(const TreeAttnArgs &a, int G, int off) {
     do {
       if (rem <= 0) {
         live = false;
@@ -162,10 +175,14 @@ struct TreeCursor {
           } while (s.n == 0);
         }
       }
-      item(G, 0);
+      nt = tree_tiles(a, s, G, rt);
+      const int64_t take = min(static_cast<int64_t>(nt + kTreeItemCost - off), rem);
+      t = max(0, off - kTreeItemCost);
+      t_end = max(0, off + static_cast<int>(take) - kTreeItemCost);
+      rem -= take;
+      off = 0;
     } while (t >= t_end);
   }
-  __device__ __forceinline__ int rows(int G) const { return min(kTreeM, s.n * G - rt * kTreeM); }
 };
 
 // Bits of the nodes j0 .. j0 + 63 that node i sees (negative j: the context, seen).
@@ -200,10 +217,47 @@ __device__ __forceinline__ uint64_t tree_sdesc_v(uint32_t saddr) {
          (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
          (static_cast<uint64_t>(2) << 61);
 }
+// Descriptor of codes with rows of B = 64 or 128 bytes under the swizzle of that width: 8-row groups
+// 8 B bytes apart.
+template <int B>
 __device__ __forceinline__ uint64_t tree_sdesc_k(uint32_t saddr) {
   return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(1) << 16) |
-         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
-         (static_cast<uint64_t>(2) << 61);
+         (static_cast<uint64_t>(8 * B >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+         (static_cast<uint64_t>(B == 128 ? 2 : 4) << 61);
+}
+
+// Bounded waits by a warp and by one thread, short in code: about 2^20 polls of a microsecond at most,
+// then the timeout is recorded and the CTA's roles give up.
+__device__ __forceinline__ bool tree_poll(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(1000u)
+      : "memory");
+  return ok != 0;
+}
+constexpr uint32_t kTreePolls = 1u << 20;
+template <bool WARP>
+__device__ __forceinline__ bool tree_wait(const uint64_t &barrier, uint32_t parity,
+                                          volatile int *abort_flag) {
+  const uint32_t bar = smem_u32(&barrier);
+#pragma unroll 1
+  for (uint32_t n = 0;; ++n) {
+    const bool ok = tree_poll(bar, parity & 1u);
+    if (WARP ? __all_sync(0xffffffffu, ok) : ok) return true;
+    const bool stop = *abort_flag != 0 || n >= kTreePolls;
+    if (WARP ? __any_sync(0xffffffffu, stop) : stop) break;
+  }
+  if (atomicExch(const_cast<int *>(abort_flag), 1) == 0) record_error(6 /* FP8Q_ERR_TIMEOUT */);
+  return false;
+}
+// The calling warp's share of an arrival.
+__device__ __forceinline__ void tree_arrive(const uint64_t &barrier) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&barrier));
 }
 
 template <int N>
@@ -221,9 +275,13 @@ __device__ __forceinline__ void tree_st(uint32_t taddr, const uint32_t (&r)[N]) 
 }
 
 // What the CTA's roles share.
+constexpr int kTreePieces = 4;   // descriptors in the ring
 struct TreeShared {
-  uint64_t k_full[kTreeKStages], v_full[2], s_full, s_free, p_full[2], pv_done[2], sm_sync, drain;
+  uint64_t k_full[kTreeStages], k_free[kTreeStages], v8_full[kTreeStages], v8_free[kTreeStages];
+  uint64_t piece_full[kTreePieces], piece_free[kTreePieces];
+  uint64_t q_full, v_full[2], s_full, s_free, p_full[2], pv_done[2], sm_sync, drain;
   uint64_t valid[8];             // per tile (mod 8): the positions that exist, one bit each
+  TreePiece piece[kTreePieces];
   int start_b;
   int64_t start_off;
   int64_t warp_sum[kTreeThreads / 32];
@@ -234,20 +292,29 @@ struct TreeShared {
   float o[4][32][17];
 };
 
+// The next piece of the ring for the calling warp; false where there is none.
+__device__ __forceinline__ bool tree_take(TreeShared &sh, uint32_t ip, TreePiece &pc) {
+  const uint32_t i = ip % kTreePieces;
+  if (!tree_wait<true>(sh.piece_full[i], ip / kTreePieces, &sh.abort)) return false;
+  pc = sh.piece[i];
+  tree_arrive(sh.piece_free[i]);
+  return pc.t_end > 0;
+}
+
 // The dims of kv head g that are NaN in a value row seen by row (node i) among the positions of
 // [t, t_end) whose column within its tile lies in [c0, c0 + nc).  Runs only where V holds NaN codes.
 template <int D>
-__device__ __noinline__ uint4 tree_nan_dims(const TreeAttnArgs &a, const TreeCursor &c, int i, int c0,
+__device__ __noinline__ uint4 tree_nan_dims(const TreeAttnArgs &a, const TreePiece &c, int i, int c0,
                                             int nc) {
   uint32_t dims[4] = {};
   const int words = (a.max_nodes + 63) / 64;
-  const int64_t *mrow = a.mask ? a.mask + (c.s.first + i) * a.ldm : nullptr;
+  const int64_t *mrow = a.mask ? a.mask + (c.first + i) * a.ldm : nullptr;
   for (int tile = c.t; tile < c.t_end; ++tile) {
-    const uint64_t bits = tree_bits(mrow, words, i, tile * kTreeN - c.s.ctx);
+    const uint64_t bits = tree_bits(mrow, words, i, tile * kTreeN - c.ctx);
     for (int col = c0; col < c0 + nc; ++col) {
       const int pos = tile * kTreeN + col;
-      if (!((bits >> col) & 1) || pos >= c.s.ctx + c.s.n) continue;
-      const int32_t blk = a.block_table[c.b * a.max_blocks + pos / a.block_size];
+      if (!((bits >> col) & 1) || pos >= c.ctx + c.n) continue;
+      const int32_t blk = a.block_table[c.b * a.max_blocks + a.by_block(pos)];
       if (blk < 0 || blk >= a.num_blocks) continue;
       const int64_t slot = static_cast<int64_t>(blk) * a.block_size + pos % a.block_size;
       const uint32_t *v = reinterpret_cast<const uint32_t *>(a.v_cache + (slot * a.Hkv + c.g) * D);
@@ -268,34 +335,41 @@ struct TreeRow {
   float ref, l;                  // reference of the weights (log2 units), their sum
 };
 
-// One position tile: the scores of NC columns of this thread's row become weights in TMEM.
-template <int D, int NC>
-__device__ __forceinline__ bool tree_tile(TreeShared &sh, uint32_t tmem, uint32_t col0, uint32_t it,
-                                          bool first, uint64_t seen, float c2, TreeRow &st) {
-  using L = TreeLayout<D>;
-  const int lane = threadIdx.x & 31;
-  if (!wait_warp(smem_u32(&sh.s_full), it & 1u, &sh.abort)) return false;
-  tc_fence_after();
-  uint32_t sr[NC];
-  tree_ld<NC>(tmem + L::kColS + col0, sr);
-  seen &= sh.valid[it & 7u];
-  tc_fence_before();
-  __syncwarp();
-  if (lane == 0) mbar_arrive(smem_u32(&sh.s_free));
-  const uint64_t mine = seen >> col0;
-  const uint64_t all = NC == 64 ? ~0ull : (1ull << (NC & 63)) - 1;
-  if (!__all_sync(0xffffffffu, (mine & all) == all)) {
+// NC scores of this thread's row from TMEM; what is not seen (bit 0 on) becomes -inf.
+template <int NC>
+__device__ __forceinline__ void tree_scores(uint32_t taddr, uint64_t seen, uint32_t (&sr)[NC]) {
+  tree_ld<NC>(taddr, sr);
+  const uint32_t bits = static_cast<uint32_t>(seen), all = NC == 32 ? ~0u : (1u << (NC & 31)) - 1;
+  if (!__all_sync(0xffffffffu, (bits & all) == all)) {
 #pragma unroll
     for (int j = 0; j < NC; ++j)
-      if (!((mine >> j) & 1)) sr[j] = 0xFF800000u;               // -inf
+      if (!((bits >> j) & 1)) sr[j] = 0xFF800000u;
   }
+}
+
+// One position tile: the scores of NC * chunks columns of this thread's row become weights in TMEM.
+// The last chunk's scores stay in registers between the maximum and the weights, the others are read
+// again.
+template <int D, int NC>
+__device__ __forceinline__ bool tree_tile(TreeShared &sh, uint32_t tmem, uint32_t col0, int chunks,
+                                          uint32_t it, bool first, uint64_t seen, float c2,
+                                          TreeRow &st) {
+  using L = TreeLayout<D>;
+  if (!tree_wait<true>(sh.s_full, it, &sh.abort)) return false;
+  tc_fence_after();
+  uint32_t sr[NC];
+  seen = (seen & sh.valid[it & 7u]) >> col0;
   float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  int c = 0;
+#pragma unroll 1
+  do {
+    tree_scores<NC>(tmem + L::kColS + col0 + NC * c, seen >> (NC * c), sr);
 #pragma unroll
-  for (int j = 0; j < NC; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(sr[j]));
+    for (int j = 0; j < NC; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(sr[j]));
+  } while (++c < chunks);
   const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
   // P buffer it & 1 was read by the MMA of tile it - 2
-  if (it >= 2 && !wait_warp(smem_u32(&sh.pv_done[it & 1u]), ((it - 2) >> 1) & 1u, &sh.abort))
-    return false;
+  if (it >= 2 && !tree_wait<true>(sh.pv_done[it & 1u], (it - 2) >> 1, &sh.abort)) return false;
   const bool up = top > st.ref + kTreeLag;                       // also the first score seen
   if (__any_sync(0xffffffffu, up)) {
     const bool held = up && st.ref != -INFINITY;                 // values to rescale
@@ -303,50 +377,57 @@ __device__ __forceinline__ bool tree_tile(TreeShared &sh, uint32_t tmem, uint32_
     st.ref = up ? top : st.ref;
     st.l *= f;
     if (!first && __any_sync(0xffffffffu, held)) {
-      if (!wait_warp(smem_u32(&sh.pv_done[(it - 1) & 1u]), ((it - 1) >> 1) & 1u, &sh.abort))
-        return false;
+      if (!tree_wait<true>(sh.pv_done[(it - 1) & 1u], (it - 1) >> 1, &sh.abort)) return false;
       tc_fence_after();
 #pragma unroll 1
-      for (int c = 0; c < D; c += 16) {
+      for (int d = 0; d < D; d += 16) {
         uint32_t o[16];
-        tree_ld<16>(tmem + L::kColO + c, o);
+        tree_ld<16>(tmem + L::kColO + d, o);
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-        tree_st<16>(tmem + L::kColO + c, o);
+        tree_st<16>(tmem + L::kColO + d, o);
       }
     }
   }
   const float bias = kTreeBias - (st.ref == -INFINITY ? 0.0f : st.ref);
   float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  uint32_t pk[NC / 2];
+#pragma unroll 1
+  while (true) {
+    --c;
+    if (c == 0) {                                                // the last read of the scores
+      tc_fence_before();
+      tree_arrive(sh.s_free);
+    }
+    uint32_t pk[NC / 2];
 #pragma unroll
-  for (int j = 0; j < NC; j += 2) {
-    const float p0 = tree_ex2(fmaf(__uint_as_float(sr[j]), c2, bias));
-    const float p1 = tree_ex2(fmaf(__uint_as_float(sr[j + 1]), c2, bias));
-    sum[j & 3] += p0;
-    sum[(j & 3) + 1] += p1;
-    pk[j / 2] = f32x2_to_f16x2(p0, p1);
+    for (int j = 0; j < NC; j += 2) {
+      const float p0 = tree_ex2(fmaf(__uint_as_float(sr[j]), c2, bias));
+      const float p1 = tree_ex2(fmaf(__uint_as_float(sr[j + 1]), c2, bias));
+      sum[j & 3] += p0;
+      sum[(j & 3) + 1] += p1;
+      pk[j / 2] = f32x2_to_f16x2(p0, p1);
+    }
+    tree_st<NC / 2>(tmem + L::kColP + 32 * (it & 1u) + (col0 + NC * c) / 2, pk);
+    if (c == 0) break;
+    tree_scores<NC>(tmem + L::kColS + col0 + NC * (c - 1), seen >> (NC * (c - 1)), sr);
   }
   st.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-  tree_st<NC / 2>(tmem + L::kColP + 32 * (it & 1u) + col0 / 2, pk);
   tmem_st_wait();
   tc_fence_before();
-  __syncwarp();
-  if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[it & 1u]));
+  tree_arrive(sh.p_full[it & 1u]);
   return true;
 }
 
 // Bounded barrier of the four softmax warps.
 __device__ __forceinline__ bool tree_sync4(TreeShared &sh, uint32_t &phase) {
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&sh.sm_sync));
-  const bool ok = wait_warp(smem_u32(&sh.sm_sync), phase & 1u, &sh.abort);
-  ++phase;
-  return ok;
+  tree_arrive(sh.sm_sync);
+  return tree_wait<true>(sh.sm_sync, phase++, &sh.abort);
 }
 
 template <int D>
-__global__ void __launch_bounds__(kTreeThreads, 2) k_tree_attn(const TreeAttnArgs a) {
+__global__ void __launch_bounds__(kTreeThreads, 2)
+    k_tree_attn(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                const TreeAttnArgs a) {
   using L = TreeLayout<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ TreeShared sh;
@@ -356,7 +437,17 @@ __global__ void __launch_bounds__(kTreeThreads, 2) k_tree_attn(const TreeAttnArg
   const int G = a.Hq / a.Hkv;
 
   if (tid == 0) {
-    for (int i = 0; i < kTreeKStages; ++i) mbar_init(smem_u32(&sh.k_full[i]), 4);
+    for (int i = 0; i < kTreeStages; ++i) {
+      mbar_init(smem_u32(&sh.k_full[i]), 1);
+      mbar_init(smem_u32(&sh.k_free[i]), 1);
+      mbar_init(smem_u32(&sh.v8_full[i]), 1);
+      mbar_init(smem_u32(&sh.v8_free[i]), 4);
+    }
+    for (int i = 0; i < kTreePieces; ++i) {
+      mbar_init(smem_u32(&sh.piece_full[i]), 1);
+      mbar_init(smem_u32(&sh.piece_free[i]), 9);
+    }
+    mbar_init(smem_u32(&sh.q_full), 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sh.v_full[i]), 4);
       mbar_init(smem_u32(&sh.p_full[i]), 4);
@@ -385,7 +476,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) k_tree_attn(const TreeAttnArg
     bool falls = false;
     for (int b = tid * per; b < min(B, (tid + 1) * per); ++b) {
       falls |= a.cu[b + 1] < a.cu[b];
-      mine += tree_group_cost(tree_seq(a, b, blockIdx.x == 0), G) * a.Hkv;
+      mine += tree_group_cost(a, tree_seq(a, b, blockIdx.x == 0), G) * a.Hkv;
     }
     upto = mine;
 #pragma unroll
@@ -422,7 +513,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) k_tree_attn(const TreeAttnArg
     int64_t off = lo - (upto - mine);
     int b = tid * per;
     for (;; ++b) {
-      const int64_t c = tree_group_cost(tree_seq(a, b, false), G) * a.Hkv;
+      const int64_t c = tree_group_cost(a, tree_seq(a, b, false), G) * a.Hkv;
       if (off < c) break;
       off -= c;
     }
@@ -434,179 +525,240 @@ __global__ void __launch_bounds__(kTreeThreads, 2) k_tree_attn(const TreeAttnArg
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
 
-  if (warp >= 4 && warp < 8) {
-    // ---------------------------------------------------------------- load and convert
-    constexpr int NR = D / 32;                                   // rows of a tile per thread
-    constexpr int LPR = D / 16;                                  // lanes per row
-    const int lw = warp - 4, lt = tid - 128, ch = lane % LPR;
-    const int64_t row = static_cast<int64_t>(a.Hkv) * D;
-    const float c = a.sm_scale * a.scale3[0] * a.scale3[1];
-    const uint32_t qflip = c < 0.0f ? 0x80808080u : 0u;          // a negative scale negates Q
-    TreeCursor pre, cur;
-    if (works) pre.init(a, G, B, sh.start_b, sh.start_off, hi - lo);
-    pre.live = works && pre.live;
-    cur = pre;
-    int32_t blk[NR];
-    int off[NR];
-    // block ids of the prefetch cursor's tile
-    auto look_up = [&]() {
+  if (warp == 9) {
+    // ---------------------------------------------------------------- load
+    // A lane copies `box` consecutive positions of one block: lanes 0 .. 64 / box - 1 K's rows, as many
+    // from lane 16 on V's.  Blocks of odd size or 2 mod 4 go by gathers of four rows each instead; then
+    // lane i holds the slots of the positions i and i + 32.
+    TreeCursor pre;
+    pre.init(a, G, B, sh.start_b, sh.start_off, hi - lo);
+    const bool gather = a.box < 4;
+    const int chunks = gather ? 16 : kTreeN / a.box, i16 = lane & 15;
+    const int first = gather ? lane : min(i16, chunks - 1) * a.box;
+    int blk[2], off[2];
+    auto look_up = [&]() {                                       // block ids of the cursor's tile
       if (!pre.live) return;
 #pragma unroll
-      for (int j = 0; j < NR; ++j) {
-        const int pos = pre.t * kTreeN + 16 * lw + j * (32 / LPR) + lane / LPR;
-        const int q = pos / a.block_size;
+      for (int j = 0; j < 2; ++j) {
+        if (j == 1 && !gather) break;
+        const int pos = pre.t * kTreeN + 32 * j + first;
+        const int q = a.by_block(pos);
         off[j] = pos - q * a.block_size;
         blk[j] = -1;
         if (pos < pre.s.ctx + pre.s.n) blk[j] = a.block_table[pre.b * a.max_blocks + q];
         else off[j] = -1;                                        // behind the sequence
       }
     };
-    uint32_t pit = 0;                                            // tiles issued
-    auto issue = [&]() {
-      if (pre.live) {
-        const uint32_t st = pit % kTreeKStages;
-        uint32_t bits = 0;
+    auto slot_of = [&](int j, bool *ok) {                        // row 0 for a place not seen
+      *ok = blk[j] >= 0 && blk[j] < a.num_blocks;
+      if (!*ok && off[j] >= 0) record_error(9 /* FP8Q_ERR_RANGE */);
+      return *ok ? blk[j] * a.block_size + off[j] : 0;
+    };
+    uint32_t ip = 0;
+    auto publish = [&]() {                                       // the piece, or the end
+      const uint32_t i = ip % kTreePieces;
+      if (!tree_wait<true>(sh.piece_free[i], (ip / kTreePieces) ^ 1u, &sh.abort)) return false;
+      if (lane == 0)
+        sh.piece[i] = TreePiece{pre.s.first, pre.b, pre.s.n, pre.s.ctx, pre.g, pre.rt * kTreeM,
+                                min(kTreeM, pre.s.n * G - pre.rt * kTreeM), pre.t,
+                                pre.live ? pre.t_end : 0, pre.nt};
+      tree_arrive(sh.piece_full[i]);
+      ++ip;
+      return true;
+    };
+    look_up();
+    uint32_t it = 0, st = 0, ph = 1u;
+    bool fresh = true;
+    for (;; ++it) {
+      if (fresh && !publish()) break;
+      if (!pre.live) break;
+      uint64_t there;
+      int32_t rows[4];
+      bool ok;
+      rows[0] = slot_of(0, &ok);
+      there = __ballot_sync(0xffffffffu, ok);
+      if (gather) {
+        const int32_t lo32 = rows[0], hi32 = slot_of(1, &ok);
+        there |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, ok)) << 32;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int from = (4 * lane + r) & 31;
+          const int32_t v0 = __shfl_sync(0xffffffffu, lo32, from);
+          const int32_t v1 = __shfl_sync(0xffffffffu, hi32, from);
+          rows[r] = lane & 8 ? v1 : v0;
+        }
+      } else if (lane == 0) {
+        uint64_t bits = 0;
+        const uint64_t ones = a.box == 64 ? ~0ull : (1ull << a.box) - 1;
+        for (int c = 0; c < chunks; ++c)
+          if ((there >> c) & 1u) bits |= ones << (c * a.box);
+        const int left = pre.s.ctx + pre.s.n - pre.t * kTreeN;   // positions that exist
+        there = left < 64 ? bits & ((1ull << left) - 1) : bits;
+      }
+      const int x = pre.g * D;
+      if (!tree_wait<true>(sh.k_free[st], ph, &sh.abort) ||
+          !tree_wait<true>(sh.v8_free[st], ph, &sh.abort))
+        break;
+      const uint32_t k_bar = smem_u32(&sh.k_full[st]), v_bar = smem_u32(&sh.v8_full[st]);
+      if (lane == 0) {
+        sh.valid[it & 7u] = there;
+        mbar_arrive_expect_tx(k_bar, L::kTile);
+        mbar_arrive_expect_tx(v_bar, L::kTile);
+      }
+      __syncwarp();
+      const uint32_t dst = sbase + (lane < 16 ? L::kK : L::kV8) + st * L::kTile +
+                           i16 * (gather ? 4 : a.box) * D;
+      const void *map = lane < 16 ? &tm_k : &tm_v;
+      const uint32_t bar = lane < 16 ? k_bar : v_bar;
+      if (gather) tma_gather4(dst, map, x, rows, bar);
+      else if (i16 < chunks) tma_load_2d(dst, map, x, rows[0], bar);
+      if (++st == kTreeStages) {
+        st = 0;
+        ph ^= 1u;
+      }
+      fresh = ++pre.t >= pre.t_end;
+      if (fresh) pre.next(a, G, 0);
+      look_up();
+    }
+    // after a wait that gave up: no copy in flight at exit
+    for (uint32_t i = it < kTreeStages ? 0 : it - kTreeStages; i < it; ++i) {
+      wait_drain(smem_u32(&sh.k_full[i % kTreeStages]), (i / kTreeStages) & 1u);
+      wait_drain(smem_u32(&sh.v8_full[i % kTreeStages]), (i / kTreeStages) & 1u);
+    }
+  } else if (warp >= 4 && warp < 8) {
+    // ---------------------------------------------------------------- queries, V codes to fp16
+    constexpr int NR = D / 32;                                   // rows of a tile per thread
+    constexpr int LPR = D / 16;                                  // lanes per row
+    const int lw = warp - 4, lt = tid - 128, ch = lane % LPR;
+    const float c = a.sm_scale * a.scale3[0] * a.scale3[1];
+    const uint32_t qflip = c < 0.0f ? 0x80808080u : 0u;          // a negative scale negates Q
+    TreePiece pc;
+    uint32_t it = 0, st = 0, ph = 0;
+    bool ok = true;
+    for (uint32_t ip = 0; ok && tree_take(sh, ip, pc); ++ip) {
+      // Q rows of the piece, once the scores of the piece before are complete: row r is head
+      // g G + r % G of node r / G; up to 32 (64) rows are repeated 4 (2) times down the tile
+      if (it > 0 && !tree_wait<true>(sh.s_full, it - 1, &sh.abort)) break;
+      const int step = pc.rows <= 32 ? 32 : (pc.rows <= 64 ? 64 : 128);
+#pragma unroll 4
+      for (int i = lt; i < kTreeM * LPR; i += 128) {
+        const int r = i / LPR, c16 = i % LPR, rr = r & (step - 1);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (rr < pc.rows) {
+          const int idx = pc.row0 + rr, node = a.by_group(idx), h = pc.g * G + (idx - node * G);
+          v = *reinterpret_cast<const uint4 *>(a.q + (pc.first + node) * a.ldq + h * D + c16 * 16);
+          v.x ^= qflip; v.y ^= qflip; v.z ^= qflip; v.w ^= qflip;
+        }
+        *reinterpret_cast<uint4 *>(smem + L::kQ + r * 128 + ((c16 ^ (r & 7)) << 4)) = v;
+      }
+      fence_proxy_async_shared();
+      tree_arrive(sh.q_full);
+#pragma unroll 1
+      for (int t = pc.t; t < pc.t_end; ++t, ++it) {
+        if (!(ok = tree_wait<true>(sh.v8_full[st], ph, &sh.abort))) break;
+        uint4 v8[NR];
 #pragma unroll
         for (int j = 0; j < NR; ++j) {
           const int p = 16 * lw + j * (32 / LPR) + lane / LPR;
-          const bool there = blk[j] >= 0 && blk[j] < a.num_blocks;
-          if (!there && off[j] >= 0) record_error(9 /* FP8Q_ERR_RANGE */);
-          const int64_t at =
-              there ? (static_cast<int64_t>(blk[j]) * a.block_size + off[j]) * row + pre.g * D + ch * 16
-                    : 0;
-          const uint32_t nb = there ? 16u : 0u;
-          cp_async16(sbase + L::kK + st * kTreeN * 128 + p * 128 + ((ch ^ (p & 7)) << 4),
-                     a.k_cache + at, nb);
-          cp_async16(sbase + L::kV8 + st * kTreeN * D + (j * 128 + lt) * 16, a.v_cache + at, nb);
-          bits |= there ? 1u << (p & 15) : 0u;
+          v8[j] = *reinterpret_cast<const uint4 *>(smem + L::kV8 + st * L::kTile + p * D + ch * 16);
         }
-        bits = __reduce_or_sync(0xffffffffu, bits);
-        if (lane == 0)
-          reinterpret_cast<uint16_t *>(&sh.valid[pit & 7u])[lw] = static_cast<uint16_t>(bits);
-        ++pit;
-        if (++pre.t >= pre.t_end) pre.next_piece(a, G);
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      look_up();
-    };
-    look_up();
+        const uint32_t there = static_cast<uint32_t>(sh.valid[it & 7u] >> (16 * lw));
+        tree_arrive(sh.v8_free[st]);
+        if (++st == kTreeStages) {
+          st = 0;
+          ph ^= 1u;
+        }
+        if (it >= 2 && !(ok = tree_wait<true>(sh.pv_done[it & 1u], (it - 2) >> 1, &sh.abort))) break;
+        // V codes to fp16 (exact); a NaN code becomes 0 here and is put back where it is seen
+        uint8_t *v16 = smem + L::kV16 + (it & 1u) * L::kV16Bytes;
+        bool nan = false;
 #pragma unroll
-    for (int i = 0; i < kTreeAhead; ++i) issue();
-    bool fresh = true, ok = true;
-    int piece = 0;
-    for (uint32_t it = 0; cur.live; ++it) {
-      const uint32_t st = it % kTreeKStages;
-      if (fresh) {
-        // Q rows of the piece, once the scores of the piece before are complete: row r is head
-        // g G + r % G of node r / G; up to 32 (64) rows are repeated 4 (2) times down the tile
-        if (it > 0 && !wait_warp(smem_u32(&sh.s_full), (it - 1) & 1u, &sh.abort)) { ok = false; break; }
-        const int rows = cur.rows(G), step = rows <= 32 ? 32 : (rows <= 64 ? 64 : 128);
-        for (int i = lt; i < kTreeM * LPR; i += 128) {
-          const int r = i / LPR, c16 = i % LPR, rr = r % step;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (rr < rows) {
-            const int idx = cur.rt * kTreeM + rr, node = idx / G, h = cur.g * G + idx % G;
-            v = *reinterpret_cast<const uint4 *>(a.q + (cur.s.first + node) * a.ldq + h * D + c16 * 16);
-            v.x ^= qflip; v.y ^= qflip; v.z ^= qflip; v.w ^= qflip;
+        for (int j = 0; j < NR; ++j) {
+          const int p16 = j * (32 / LPR) + lane / LPR, p = 16 * lw + p16;
+          uint32_t w[4] = {v8[j].x, v8[j].y, v8[j].z, v8[j].w};
+          uint32_t h[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t n7 = ((w[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+            if (n7) {
+              nan |= ((there >> p16) & 1u) != 0;
+              w[k] &= ~((n7 >> 7) * 0xFFu);
+            }
+            h[2 * k] = e4m3x2_to_f16x2(w[k] & 0xFFFFu);
+            h[2 * k + 1] = e4m3x2_to_f16x2(w[k] >> 16);
           }
-          *reinterpret_cast<uint4 *>(smem + L::kQ + r * 128 + ((c16 ^ (r & 7)) << 4)) = v;
-        }
-        fresh = false;
-        ++piece;
-      }
-      asm volatile("cp.async.wait_group %0;" ::"n"(kTreeAhead - 1) : "memory");
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.k_full[st]));
-      // the K stage of tile it - 1 is free once its scores are complete
-      if (it > 0 && !wait_warp(smem_u32(&sh.s_full), (it - 1) & 1u, &sh.abort)) { ok = false; break; }
-      uint4 v8[NR];
+          // the halves of a row's dims are stored in opposite order, so that a quarter warp covers
+          // all banks
+          const int half = D == 128 ? ch >> 2 : 0, c0 = (ch & 3) * 2;
+          uint8_t *dst = v16 + half * 8192 + p * 128;
 #pragma unroll
-      for (int j = 0; j < NR; ++j)
-        v8[j] = *reinterpret_cast<const uint4 *>(smem + L::kV8 + st * kTreeN * D + (j * 128 + lt) * 16);
-      issue();
-      if (it >= 2 && !wait_warp(smem_u32(&sh.pv_done[it & 1u]), ((it - 2) >> 1) & 1u, &sh.abort)) {
-        ok = false;
-        break;
-      }
-      // V codes to fp16 (exact); a NaN code becomes 0 here and is put back where it is seen
-      uint8_t *v16 = smem + L::kV16 + (it & 1u) * L::kV16Bytes;
-      bool nan = false;
-#pragma unroll
-      for (int j = 0; j < NR; ++j) {
-        const int p = 16 * lw + j * (32 / LPR) + lane / LPR;
-        uint32_t w[4] = {v8[j].x, v8[j].y, v8[j].z, v8[j].w};
-        uint32_t h[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t n7 = ((w[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-          if (n7) {
-            nan = true;
-            w[k] &= ~((n7 >> 7) * 0xFFu);
+          for (int k = 0; k < 2; ++k) {
+            const int e = k ^ half;
+            *reinterpret_cast<uint4 *>(dst + (((c0 + e) ^ (p & 7)) << 4)) =
+                e ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
           }
-          h[2 * k] = e4m3x2_to_f16x2(w[k] & 0xFFFFu);
-          h[2 * k + 1] = e4m3x2_to_f16x2(w[k] >> 16);
         }
-        // the halves of a row's dims are stored in opposite order, so that a quarter warp covers
-        // all banks
-        const int half = D == 128 ? ch >> 2 : 0, c0 = (ch & 3) * 2;
-        uint8_t *dst = v16 + half * 8192 + p * 128;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int e = k ^ half;
-          *reinterpret_cast<uint4 *>(dst + (((c0 + e) ^ (p & 7)) << 4)) =
-              e ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
-        }
-      }
-      if (nan) atomicMax(&sh.nan_piece, piece);
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.v_full[it & 1u]));
-      if (++cur.t >= cur.t_end) {
-        cur.next_piece(a, G);
-        fresh = true;
+        if (nan) atomicMax(&sh.nan_piece, static_cast<int>(ip + 1));
+        fence_proxy_async_shared();
+        tree_arrive(sh.v_full[it & 1u]);
       }
     }
-    (void)ok;
-    asm volatile("cp.async.wait_group 0;" ::: "memory");         // none in flight at exit
   } else if (warp == 8) {
     // ---------------------------------------------------------------- MMA issue
     if (lane == 0) {
-      TreeCursor cur;
-      if (works) cur.init(a, G, B, sh.start_b, sh.start_off, hi - lo);
-      cur.live = works && cur.live;
-      const uint64_t qd = tree_sdesc_k(sbase + L::kQ);
-      auto scores = [&](uint32_t it) {
-        const uint32_t st = it % kTreeKStages;
-        if (!wait_one(smem_u32(&sh.k_full[st]), (it / kTreeKStages) & 1u, &sh.abort)) return false;
-        tc_fence_after();
-        const uint64_t kd = tree_sdesc_k(sbase + L::kK + st * kTreeN * 128);
-#pragma unroll
-        for (int kk = 0; kk < D / 32; ++kk)
-          mma_f8f6f4(tmem + L::kColS, qd + 2 * kk, kd + 2 * kk, L::kIdescQK, kk > 0 ? 1u : 0u);
-        mma_commit(smem_u32(&sh.s_full));
-        return true;
-      };
-      bool ok = !cur.live || scores(0), first = true;
-      for (uint32_t it = 0; cur.live && ok; ++it) {
-        const bool fresh = first;
-        first = false;
-        if (++cur.t >= cur.t_end) {
-          cur.next_piece(a, G);
-          first = true;
+      const uint64_t qd = tree_sdesc_k<128>(sbase + L::kQ);
+      uint32_t ip = 0;
+      int left = 0;
+      bool fresh = false, before = false;
+      auto next = [&]() {                                        // the next tile, if there is one
+        fresh = left == 0;
+        if (fresh) {
+          const uint32_t i = ip % kTreePieces;
+          if (!tree_wait<false>(sh.piece_full[i], ip / kTreePieces, &sh.abort)) return false;
+          left = sh.piece[i].t_end - (sh.piece[i].t_end > 0 ? sh.piece[i].t : 0);
+          mbar_arrive(smem_u32(&sh.piece_free[i]));
+          ++ip;
         }
-        if (cur.live)
-          ok = wait_one(smem_u32(&sh.s_free), it & 1u, &sh.abort) && scores(it + 1);
-        if (!ok || !wait_one(smem_u32(&sh.p_full[it & 1u]), (it >> 1) & 1u, &sh.abort) ||
-            !wait_one(smem_u32(&sh.v_full[it & 1u]), (it >> 1) & 1u, &sh.abort))
-          break;
-        tc_fence_after();
-        const uint64_t vd = tree_sdesc_v(sbase + L::kV16 + (it & 1u) * L::kV16Bytes);
+        return left-- > 0;
+      };
+      uint32_t st = 0, ph = 0;
+      bool live = next();
+      // the scores of tile it, then the values of tile it - 1
+#pragma unroll 1
+      for (uint32_t it = 0;; ++it) {
+        if (live) {
+          if ((it > 0 && !tree_wait<false>(sh.s_free, it - 1, &sh.abort)) ||
+              (fresh && !tree_wait<false>(sh.q_full, ip - 1, &sh.abort)) ||
+              !tree_wait<false>(sh.k_full[st], ph, &sh.abort))
+            break;
+          tc_fence_after();
+          const uint64_t kd = tree_sdesc_k<D>(sbase + L::kK + st * L::kTile);
 #pragma unroll
-        for (int kk = 0; kk < kTreeN / 16; ++kk)
-          mma_f16_ts(tmem + L::kColO, tmem + L::kColP + 32 * (it & 1u) + 8 * kk, vd + 128 * kk,
-                     L::kIdescPV, fresh && kk == 0 ? 0u : 1u);
-        mma_commit(smem_u32(&sh.pv_done[it & 1u]));
+          for (int kk = 0; kk < D / 32; ++kk)
+            mma_f8f6f4(tmem + L::kColS, qd + 2 * kk, kd + 2 * kk, L::kIdescQK, kk > 0 ? 1u : 0u);
+          mma_commit(smem_u32(&sh.s_full));
+          mma_commit(smem_u32(&sh.k_free[st]));
+          if (++st == kTreeStages) {
+            st = 0;
+            ph ^= 1u;
+          }
+        }
+        if (it > 0) {
+          const uint32_t i = (it - 1) & 1u, pp = (it - 1) >> 1;
+          if (!tree_wait<false>(sh.p_full[i], pp, &sh.abort) ||
+              !tree_wait<false>(sh.v_full[i], pp, &sh.abort))
+            break;
+          tc_fence_after();
+          const uint64_t vd = tree_sdesc_v(sbase + L::kV16 + i * L::kV16Bytes);
+#pragma unroll
+          for (int kk = 0; kk < kTreeN / 16; ++kk)
+            mma_f16_ts(tmem + L::kColO, tmem + L::kColP + 32 * i + 8 * kk, vd + 128 * kk,
+                       L::kIdescPV, before && kk == 0 ? 0u : 1u);
+          mma_commit(smem_u32(&sh.pv_done[i]));
+        }
+        if (!live) break;
+        before = fresh;
+        live = next();
       }
       mma_commit(smem_u32(&sh.drain));                           // all MMAs done before dealloc
       wait_drain(smem_u32(&sh.drain), 0);
@@ -614,161 +766,114 @@ __global__ void __launch_bounds__(kTreeThreads, 2) k_tree_attn(const TreeAttnArg
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- softmax and output
-    TreeCursor cur;
-    if (works) cur.init(a, G, B, sh.start_b, sh.start_off, hi - lo);
-    cur.live = works && cur.live;
     float c2 = fabsf(a.sm_scale * a.scale3[0] * a.scale3[1]) * 1.4426950408889634f;
     c2 = c2 < 1e-37f ? 1e-37f : c2;                              // so that -inf stays -inf
     const float sv = a.scale3[2];
     const uint32_t tw = tmem + (static_cast<uint32_t>(32 * warp) << 16);
     const int words = (a.max_nodes + 63) / 64;
     uint32_t it = 0, phase = 0;
-    int piece = 0;
     bool ok = true;
-    for (; cur.live && ok; cur.next_piece(a, G)) {
-      ++piece;
-      const int rows = cur.rows(G), rep = rows <= 32 ? 4 : (rows <= 64 ? 2 : 1);
-      const int r = rep == 4 ? lane : (rep == 2 ? 32 * (warp & 1) + lane : 32 * warp + lane);
-      const int nc = kTreeN / rep;
-      const uint32_t col0 = rep == 4 ? 16 * warp : (rep == 2 ? 32 * (warp >> 1) : 0);
-      const bool live = r < rows;
-      const int node = (cur.rt * kTreeM + r) / G;
-      const int64_t *mrow = a.mask && live ? a.mask + (cur.s.first + node) * a.ldm : nullptr;
+    TreePiece pc;
+    for (uint32_t ip = 0; ok && tree_take(sh, ip, pc); ++ip) {
+      const int shift = pc.rows <= 32 ? 2 : (pc.rows <= 64 ? 1 : 0), rep = 1 << shift;
+      const int w0 = warp & ((4 >> shift) - 1), r = 32 * w0 + lane, nc = kTreeN >> shift;
+      const uint32_t col0 = nc * (warp >> (2 - shift));
+      const bool live = r < pc.rows;
+      const int node = a.by_group(pc.row0 + r);
+      const int64_t *mrow = a.mask && live ? a.mask + (pc.first + node) * a.ldm : nullptr;
       if (rep > 1) {                                             // weights of the other columns: 0
-        const uint32_t z[32] = {};
-        tree_st<32>(tw + L::kColP, z);
-        tree_st<32>(tw + L::kColP + 32, z);
+        const uint32_t z[16] = {};
+#pragma unroll 1
+        for (int i = 0; i < 64; i += 16) tree_st<16>(tw + L::kColP + i, z);
       }
       TreeRow st{-INFINITY, 0.0f};
-      for (int t = cur.t; t < cur.t_end && ok; ++t, ++it) {
+      for (int t = pc.t; t < pc.t_end && ok; ++t, ++it) {
         // a row that does not exist counts as seeing all (its scores are 0, its results unused)
-        const uint64_t seen = live ? tree_bits(mrow, words, node, t * kTreeN - cur.s.ctx) : ~0ull;
-        const bool first = t == cur.t;
-        ok = rep == 4   ? tree_tile<D, 16>(sh, tw, col0, it, first, seen, c2, st)
-             : rep == 2 ? tree_tile<D, 32>(sh, tw, col0, it, first, seen, c2, st)
-                        : tree_tile<D, 64>(sh, tw, col0, it, first, seen, c2, st);
+        const uint64_t seen = live ? tree_bits(mrow, words, node, t * kTreeN - pc.ctx) : ~0ull;
+        const bool first = t == pc.t;
+        ok = rep == 4 ? tree_tile<D, 16>(sh, tw, col0, 1, it, first, seen, c2, st)
+                      : tree_tile<D, 32>(sh, tw, col0, 2 >> shift, it, first, seen, c2, st);
       }
-      if (!ok || !wait_warp(smem_u32(&sh.pv_done[(it - 1) & 1u]), ((it - 1) >> 1) & 1u, &sh.abort))
-        break;
+      if (!ok || !tree_wait<true>(sh.pv_done[(it - 1) & 1u], (it - 1) >> 1, &sh.abort)) break;
       tc_fence_after();
       uint4 nan = make_uint4(0, 0, 0, 0);
-      const bool any_nan = *reinterpret_cast<volatile int *>(&sh.nan_piece) >= piece;
-      if (any_nan && live) nan = tree_nan_dims<D>(a, cur, node, col0, nc);
-      auto is_nan = [&](int d) {
-        const uint32_t w = d < 64 ? (d < 32 ? nan.x : nan.y) : (d < 96 ? nan.z : nan.w);
-        return ((w >> (d & 31)) & 1) != 0;
-      };
-      const bool whole = cur.t == 0 && cur.t_end == cur.nt;
-      const int slot = cur.t > 0 ? 0 : 1;
+      const bool any_nan = *reinterpret_cast<volatile int *>(&sh.nan_piece) > static_cast<int>(ip);
+      if (any_nan && live) nan = tree_nan_dims<D>(a, pc, node, col0, nc);
+      const bool whole = pc.t == 0 && pc.t_end == pc.nt;
+      const int slot = pc.t > 0 ? 0 : 1;
       float *part = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * a.row_cap * (D + 2);
-      float *ml = part + static_cast<int64_t>(a.row_cap) * D;
-      if (warp == 0 && lane == 0 && !whole) {
-        if (slot == 0) meta[0] = cur.t_end == cur.nt ? 2 : 1;    // a part; 2: the item's last
+      if (tid == 0 && !whole) {
+        if (slot == 0) meta[0] = pc.t_end == pc.nt ? 2 : 1;      // a part; 2: the item's last
         else {
           meta[1] = 1;                                           // the item's first part
-          meta[2] = static_cast<int>(cur.s.first);
-          meta[3] = cur.rt * kTreeM;
-          meta[4] = rows;
-          meta[5] = cur.g;
+          meta[2] = static_cast<int>(pc.first);
+          meta[3] = pc.row0;
+          meta[4] = pc.rows;
+          meta[5] = pc.g;
         }
       }
-      if (rep == 1) {
-        const float f = whole ? (st.l == 0.0f ? 0.0f : sv / st.l) : 1.0f;
-        const int h = cur.g * G + (cur.rt * kTreeM + r) % G;
-        uint16_t *out = a.out + (cur.s.first + node) * a.ldo + h * D;
-#pragma unroll
-        for (int c = 0; c < D; c += 16) {
-          uint32_t o[16];
-          tree_ld<16>(tw + L::kColO + c, o);
-          float v[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            v[j] = st.l == 0.0f ? 0.0f : __uint_as_float(o[j]) * f;
-            if (is_nan(c + j)) v[j] = NAN;
-          }
-          if (!live) continue;
-          if (whole) {
-            uint32_t pk[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-              pk[j] = *reinterpret_cast<const uint32_t *>(&b2);
-            }
-            *reinterpret_cast<uint4 *>(out + c) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-            *reinterpret_cast<uint4 *>(out + c + 8) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 16; j += 4)
-              *reinterpret_cast<float4 *>(part + r * D + c + j) =
-                  make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-          }
+      // Repeats of a row hold different positions: their states are merged, then summed by rows, `rep`
+      // threads per row and 16 / rep columns each.
+      sh.ml[warp][lane][0] = st.ref;
+      sh.ml[warp][lane][1] = st.l;
+      if (!tree_sync4(sh, phase)) break;
+      auto merged = [&](int w, int ln, float &l) {
+        float M = -INFINITY;
+        for (int i = w; i < 4; i += 4 >> shift) M = fmaxf(M, sh.ml[i][ln][0]);
+        l = 0.0f;
+        for (int i = w; i < 4; i += 4 >> shift) {
+          const float m = sh.ml[i][ln][0];
+          l += sh.ml[i][ln][1] * (m == M ? 1.0f : tree_ex2(m - M));
         }
-        if (live && !whole) {
-          ml[2 * r] = st.ref;
-          ml[2 * r + 1] = st.l;
+        return M;
+      };
+      const int tr = tid >> shift, cpt = 16 >> shift, tc = (tid & (rep - 1)) * cpt;
+      float l;
+      const float mine_M = merged(w0, lane, l);
+      const float f = st.l == 0.0f ? 0.0f : (st.ref == mine_M ? 1.0f : tree_ex2(st.ref - mine_M));
+      const float M = merged(tr >> 5, tr & 31, l);
+      const float scale = whole ? (l == 0.0f ? 0.0f : sv / l) : 1.0f;
+      const int idx = pc.row0 + tr, nd = a.by_group(idx), h = pc.g * G + (idx - nd * G);
+      uint16_t *out = a.out + (pc.first + nd) * a.ldo + h * D + tc;
+      float *po = part + tr * D + tc;
+#pragma unroll 1
+      for (int c = 0; c < D && ok; c += 16) {
+        uint32_t o[16];
+        tree_ld<16>(tw + L::kColO + c, o);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) sh.o[warp][lane][j] = __uint_as_float(o[j]) * f;
+        if (any_nan) {
+          const uint32_t w = (c < 64 ? (c < 32 ? nan.x : nan.y) : (c < 96 ? nan.z : nan.w)) >> (c & 31);
+          for (int j = 0; j < 16; ++j)
+            if ((w >> j) & 1u) sh.o[warp][lane][j] = NAN;
         }
-      } else {
-        // the repeats of a row hold different positions: merge them
-        sh.ml[warp][lane][0] = st.ref;
-        sh.ml[warp][lane][1] = st.l;
-        if (!tree_sync4(sh, phase)) break;
-        auto merged = [&](int w0, int ln, float &M, float &l) {
-          M = -INFINITY;
-          l = 0.0f;
-          for (int w = w0; w < 4; w += 4 / rep) M = fmaxf(M, sh.ml[w][ln][0]);
-          for (int w = w0; w < 4; w += 4 / rep) {
-            const float m = sh.ml[w][ln][0];
-            l += sh.ml[w][ln][1] * (m == M ? 1.0f : tree_ex2(m - M));
-          }
-        };
-        float M, l;
-        merged(rep == 4 ? 0 : warp & 1, lane, M, l);
-        const float f = st.ref == M ? 1.0f : tree_ex2(st.ref - M);
-        // summed by rows: `rep` threads per row, 16 / rep columns each
-        const int tr = tid / rep, tc = (tid % rep) * (16 / rep);
-        float tM, tl;
-        merged(rep == 4 ? 0 : tr / 32, tr % 32, tM, tl);
-        const float scale = whole ? (tl == 0.0f ? 0.0f : sv / tl) : 1.0f;
-        const int idx = cur.rt * kTreeM + tr, h = cur.g * G + idx % G;
-        uint16_t *out = a.out + (cur.s.first + idx / G) * a.ldo + h * D + tc;
-        for (int c = 0; c < D && ok; c += 16) {
-          uint32_t o[16];
-          tree_ld<16>(tw + L::kColO + c, o);
+        if (!(ok = tree_sync4(sh, phase))) break;
+        if (tr < pc.rows) {
+#pragma unroll 1
+          for (int j = 0; j < cpt; j += 4) {
+            float v[4] = {};
+            for (int w = tr >> 5; w < 4; w += 4 >> shift)
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            float v = st.l == 0.0f ? 0.0f : __uint_as_float(o[j]) * f;
-            if (is_nan(c + j)) v = NAN;
-            sh.o[warp][lane][j] = v;
-          }
-          if (!tree_sync4(sh, phase)) { ok = false; break; }
-          if (tr < rows) {
-            for (int j = 0; j < 16 / rep; j += 4) {
-              float v[4];
+              for (int k = 0; k < 4; ++k) v[k] += sh.o[w][tr & 31][tc + j + k];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                float x = 0.0f;
-                for (int w = rep == 4 ? 0 : tr / 32; w < 4; w += 4 / rep)
-                  x += sh.o[w][tr % 32][tc + j + k];
-                v[k] = x * scale;
-              }
-              if (whole) {
-                const __nv_bfloat162 b0 = __floats2bfloat162_rn(v[0], v[1]);
-                const __nv_bfloat162 b1 = __floats2bfloat162_rn(v[2], v[3]);
-                *reinterpret_cast<uint2 *>(out + c + j) =
-                    make_uint2(*reinterpret_cast<const uint32_t *>(&b0),
-                               *reinterpret_cast<const uint32_t *>(&b1));
-              } else {
-                *reinterpret_cast<float4 *>(part + tr * D + c + tc + j) =
-                    make_float4(v[0], v[1], v[2], v[3]);
-              }
+            for (int k = 0; k < 4; ++k) v[k] *= scale;
+            if (whole) {
+              const __nv_bfloat162 b0 = __floats2bfloat162_rn(v[0], v[1]);
+              const __nv_bfloat162 b1 = __floats2bfloat162_rn(v[2], v[3]);
+              *reinterpret_cast<uint2 *>(out + c + j) =
+                  make_uint2(*reinterpret_cast<const uint32_t *>(&b0),
+                             *reinterpret_cast<const uint32_t *>(&b1));
+            } else {
+              *reinterpret_cast<float4 *>(po + c + j) = make_float4(v[0], v[1], v[2], v[3]);
             }
           }
-          if (!tree_sync4(sh, phase)) { ok = false; break; }
         }
-        if (!whole && tr < rows && tc == 0) {
-          ml[2 * tr] = tM;
-          ml[2 * tr + 1] = tl;
-        }
+        ok = tree_sync4(sh, phase);
+      }
+      if (!whole && tr < pc.rows && tc == 0) {
+        float *ml = part + static_cast<int64_t>(a.row_cap) * D;
+        ml[2 * tr] = M;
+        ml[2 * tr + 1] = l;
       }
       tc_fence_before();
     }
@@ -792,7 +897,8 @@ __global__ void __launch_bounds__(256) k_tree_attn_combine(const TreeAttnArgs a)
   if (meta[1] == 0) return;
   const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (r >= meta[4]) return;
-  const int G = a.Hq / a.Hkv, idx = meta[3] + r, h = meta[5] * G + idx % G;
+  const int G = a.Hq / a.Hkv, idx = meta[3] + r, node = a.by_group(idx);
+  const int h = meta[5] * G + (idx - node * G);
   const int64_t slot = static_cast<int64_t>(a.row_cap) * (D + 2);
   float M = -INFINITY, l = 0.0f, o[V] = {};
   for (int j = i;; ++j) {
@@ -811,7 +917,7 @@ __global__ void __launch_bounds__(256) k_tree_attn_combine(const TreeAttnArgs a)
     if (j + 1 >= static_cast<int>(gridDim.x)) break;
   }
   const float f = l == 0.0f ? 0.0f : a.scale3[2] / l;
-  uint16_t *out = a.out + (static_cast<int64_t>(meta[2]) + idx / G) * a.ldo + h * D + V * lane;
+  uint16_t *out = a.out + (static_cast<int64_t>(meta[2]) + node) * a.ldo + h * D + V * lane;
 #pragma unroll
   for (int v = 0; v < V; v += 2) {
     const __nv_bfloat162 b2 = __floats2bfloat162_rn(l == 0.0f ? 0.0f : o[v] * f,

@@ -279,7 +279,7 @@ constexpr int kTreePieces = 4;   // descriptors in the ring
 struct TreeShared {
   uint64_t k_full[kTreeStages], k_free[kTreeStages], v8_full[kTreeStages], v8_free[kTreeStages];
   uint64_t piece_full[kTreePieces], piece_free[kTreePieces];
-  uint64_t q_full, v_full[2], s_full, s_free, p_full[2], pv_done[2], sm_sync, drain;
+  uint64_t q_full, v_full[2], s_full, s_free, p_full[2], pv_done[2], drain;
   uint64_t valid[8];             // per tile (mod 8): the positions that exist, one bit each
   TreePiece piece[kTreePieces];
   int start_b;
@@ -295,6 +295,7 @@ struct TreeShared {
 // The next piece of the ring for the calling warp; false where there is none.
 __device__ __forceinline__ bool tree_take(TreeShared &sh, uint32_t ip, TreePiece &pc) {
   const uint32_t i = ip % kTreePieces;
+  pc.t = pc.t_end = 0;
   if (!tree_wait<true>(sh.piece_full[i], ip / kTreePieces, &sh.abort)) return false;
   pc = sh.piece[i];
   tree_arrive(sh.piece_free[i]);
@@ -418,10 +419,20 @@ __device__ __forceinline__ bool tree_tile(TreeShared &sh, uint32_t tmem, uint32_
   return true;
 }
 
-// Bounded barrier of the four softmax warps.
-__device__ __forceinline__ bool tree_sync4(TreeShared &sh, uint32_t &phase) {
-  tree_arrive(sh.sm_sync);
-  return tree_wait<true>(sh.sm_sync, phase++, &sh.abort);
+// Barrier of the four softmax warps, and one that tells whether any of them gave up.  Their waits are
+// bounded and every one of them passes the same barriers.
+__device__ __forceinline__ void tree_sync4() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool tree_any4(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(v))
+      : "memory");
+  return r != 0;
 }
 
 template <int D>
@@ -455,7 +466,6 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     }
     mbar_init(smem_u32(&sh.s_full), 1);
     mbar_init(smem_u32(&sh.s_free), 4);
-    mbar_init(smem_u32(&sh.sm_sync), 4);
     mbar_init(smem_u32(&sh.drain), 1);
     sh.abort = 0;
     sh.nan_piece = 0;
@@ -527,14 +537,14 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
 
   if (warp == 9) {
     // ---------------------------------------------------------------- load
-    // A lane copies `box` consecutive positions of one block: lanes 0 .. 64 / box - 1 K's rows, as many
-    // from lane 16 on V's.  Blocks of odd size or 2 mod 4 go by gathers of four rows each instead; then
-    // lane i holds the slots of the positions i and i + 32.
+    // A copy brings `box` consecutive positions of one block; lane i holds the slot of the i-th copy's
+    // first.  Blocks of odd size or 2 mod 4 go by gathers of four rows instead; then lane i holds the
+    // slots of the positions i and i + 32.
     TreeCursor pre;
     pre.init(a, G, B, sh.start_b, sh.start_off, hi - lo);
     const bool gather = a.box < 4;
-    const int chunks = gather ? 16 : kTreeN / a.box, i16 = lane & 15;
-    const int first = gather ? lane : min(i16, chunks - 1) * a.box;
+    const int chunks = kTreeN / a.box;
+    const int first = gather ? lane : min(lane, chunks - 1) * a.box;
     int blk[2], off[2];
     auto look_up = [&]() {                                       // block ids of the cursor's tile
       if (!pre.live) return;
@@ -572,46 +582,56 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     for (;; ++it) {
       if (fresh && !publish()) break;
       if (!pre.live) break;
-      uint64_t there;
-      int32_t rows[4];
-      bool ok;
-      rows[0] = slot_of(0, &ok);
-      there = __ballot_sync(0xffffffffu, ok);
-      if (gather) {
-        const int32_t lo32 = rows[0], hi32 = slot_of(1, &ok);
-        there |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, ok)) << 32;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int from = (4 * lane + r) & 31;
-          const int32_t v0 = __shfl_sync(0xffffffffu, lo32, from);
-          const int32_t v1 = __shfl_sync(0xffffffffu, hi32, from);
-          rows[r] = lane & 8 ? v1 : v0;
-        }
-      } else if (lane == 0) {
-        uint64_t bits = 0;
-        const uint64_t ones = a.box == 64 ? ~0ull : (1ull << a.box) - 1;
-        for (int c = 0; c < chunks; ++c)
-          if ((there >> c) & 1u) bits |= ones << (c * a.box);
-        const int left = pre.s.ctx + pre.s.n - pre.t * kTreeN;   // positions that exist
-        there = left < 64 ? bits & ((1ull << left) - 1) : bits;
-      }
-      const int x = pre.g * D;
+      // the stages first: the block ids are on their way meanwhile
       if (!tree_wait<true>(sh.k_free[st], ph, &sh.abort) ||
           !tree_wait<true>(sh.v8_free[st], ph, &sh.abort))
         break;
       const uint32_t k_bar = smem_u32(&sh.k_full[st]), v_bar = smem_u32(&sh.v8_full[st]);
+      const uint32_t k_dst = sbase + L::kK + st * L::kTile, v_dst = sbase + L::kV8 + st * L::kTile;
+      const int x = pre.g * D;
+      bool ok;
+      const int32_t row0 = slot_of(0, &ok);
+      int32_t row1 = 0;
+      uint64_t there;
+      if (gather) {
+        there = __ballot_sync(0xffffffffu, ok);
+        row1 = slot_of(1, &ok);
+        there |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, ok)) << 32;
+      } else {
+        const uint64_t bits = ok ? (a.box == 64 ? ~0ull : ((1ull << a.box) - 1) << first) : 0ull;
+        there = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(bits));
+        there |= static_cast<uint64_t>(
+                     __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(bits >> 32))) << 32;
+        const int left = pre.s.ctx + pre.s.n - pre.t * kTreeN;   // positions that exist
+        if (left < 64) there &= (1ull << left) - 1;
+      }
       if (lane == 0) {
         sh.valid[it & 7u] = there;
         mbar_arrive_expect_tx(k_bar, L::kTile);
         mbar_arrive_expect_tx(v_bar, L::kTile);
       }
-      __syncwarp();
-      const uint32_t dst = sbase + (lane < 16 ? L::kK : L::kV8) + st * L::kTile +
-                           i16 * (gather ? 4 : a.box) * D;
-      const void *map = lane < 16 ? &tm_k : &tm_v;
-      const uint32_t bar = lane < 16 ? k_bar : v_bar;
-      if (gather) tma_gather4(dst, map, x, rows, bar);
-      else if (i16 < chunks) tma_load_2d(dst, map, x, rows[0], bar);
+      if (gather) {
+#pragma unroll 1
+        for (int c = 0; c < 16; ++c) {
+          const int32_t v = c < 8 ? row0 : row1;
+          int32_t rows[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) rows[r] = __shfl_sync(0xffffffffu, v, (4 * c + r) & 31);
+          if (lane == 0) {
+            tma_gather4(k_dst + 4 * D * c, &tm_k, x, rows, k_bar);
+            tma_gather4(v_dst + 4 * D * c, &tm_v, x, rows, v_bar);
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+          const int32_t row = __shfl_sync(0xffffffffu, row0, c);
+          if (lane == 0) {
+            tma_load_2d(k_dst + c * a.box * D, &tm_k, x, row, k_bar);
+            tma_load_2d(v_dst + c * a.box * D, &tm_v, x, row, v_bar);
+          }
+        }
+      }
       if (++st == kTreeStages) {
         st = 0;
         ph ^= 1u;
@@ -669,33 +689,45 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           ph ^= 1u;
         }
         if (it >= 2 && !(ok = tree_wait<true>(sh.pv_done[it & 1u], (it - 2) >> 1, &sh.abort))) break;
-        // V codes to fp16 (exact); a NaN code becomes 0 here and is put back where it is seen
+        // V codes to fp16 (exact).  Where a NaN turns up the codes are cleared of it (it is put back
+        // into the results of the rows that see it) and converted again.
         uint8_t *v16 = smem + L::kV16 + (it & 1u) * L::kV16Bytes;
         bool nan = false;
+#pragma unroll 1
+        while (true) {
+          __half2 acc = __half2half2(__ushort_as_half(0));
 #pragma unroll
-        for (int j = 0; j < NR; ++j) {
-          const int p16 = j * (32 / LPR) + lane / LPR, p = 16 * lw + p16;
-          uint32_t w[4] = {v8[j].x, v8[j].y, v8[j].z, v8[j].w};
-          uint32_t h[8];
+          for (int j = 0; j < NR; ++j) {
+            const int p = 16 * lw + j * (32 / LPR) + lane / LPR;
+            const uint32_t w[4] = {v8[j].x, v8[j].y, v8[j].z, v8[j].w};
+            uint32_t h[8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t n7 = ((w[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-            if (n7) {
-              nan |= ((there >> p16) & 1u) != 0;
-              w[k] &= ~((n7 >> 7) * 0xFFu);
+            for (int k = 0; k < 8; ++k) {
+              h[k] = e4m3x2_to_f16x2(k & 1 ? w[k / 2] >> 16 : w[k / 2] & 0xFFFFu);
+              acc = __hmax2_nan(acc, *reinterpret_cast<const __half2 *>(&h[k]));
             }
-            h[2 * k] = e4m3x2_to_f16x2(w[k] & 0xFFFFu);
-            h[2 * k + 1] = e4m3x2_to_f16x2(w[k] >> 16);
-          }
-          // the halves of a row's dims are stored in opposite order, so that a quarter warp covers
-          // all banks
-          const int half = D == 128 ? ch >> 2 : 0, c0 = (ch & 3) * 2;
-          uint8_t *dst = v16 + half * 8192 + p * 128;
+            // the halves of a row's dims are stored in opposite order, so that a quarter warp covers
+            // all banks
+            const int half = D == 128 ? ch >> 2 : 0, c0 = (ch & 3) * 2;
+            uint8_t *dst = v16 + half * 8192 + p * 128;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int e = k ^ half;
-            *reinterpret_cast<uint4 *>(dst + (((c0 + e) ^ (p & 7)) << 4)) =
-                e ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
+            for (int k = 0; k < 2; ++k) {
+              const int e = k ^ half;
+              *reinterpret_cast<uint4 *>(dst + (((c0 + e) ^ (p & 7)) << 4)) =
+                  e ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
+            }
+          }
+          if (!__hisnan(__low2half(acc)) && !__hisnan(__high2half(acc))) break;
+#pragma unroll
+          for (int j = 0; j < NR; ++j) {
+            const int p16 = j * (32 / LPR) + lane / LPR;
+            uint32_t *w[4] = {&v8[j].x, &v8[j].y, &v8[j].z, &v8[j].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t n7 = ((*w[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+              nan |= n7 != 0 && ((there >> p16) & 1u) != 0;
+              *w[k] &= ~((n7 >> 7) * 0xFFu);
+            }
           }
         }
         if (nan) atomicMax(&sh.nan_piece, static_cast<int>(ip + 1));
@@ -771,10 +803,10 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     const float sv = a.scale3[2];
     const uint32_t tw = tmem + (static_cast<uint32_t>(32 * warp) << 16);
     const int words = (a.max_nodes + 63) / 64;
-    uint32_t it = 0, phase = 0;
-    bool ok = true;
+    uint32_t it = 0;
     TreePiece pc;
-    for (uint32_t ip = 0; ok && tree_take(sh, ip, pc); ++ip) {
+    for (uint32_t ip = 0;; ++ip) {
+      bool ok = tree_take(sh, ip, pc);
       const int shift = pc.rows <= 32 ? 2 : (pc.rows <= 64 ? 1 : 0), rep = 1 << shift;
       const int w0 = warp & ((4 >> shift) - 1), r = 32 * w0 + lane, nc = kTreeN >> shift;
       const uint32_t col0 = nc * (warp >> (2 - shift));
@@ -794,7 +826,10 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         ok = rep == 4 ? tree_tile<D, 16>(sh, tw, col0, 1, it, first, seen, c2, st)
                       : tree_tile<D, 32>(sh, tw, col0, 2 >> shift, it, first, seen, c2, st);
       }
-      if (!ok || !tree_wait<true>(sh.pv_done[(it - 1) & 1u], (it - 1) >> 1, &sh.abort)) break;
+      ok = ok && tree_wait<true>(sh.pv_done[(it - 1) & 1u], (it - 1) >> 1, &sh.abort);
+      sh.ml[warp][lane][0] = st.ref;
+      sh.ml[warp][lane][1] = st.l;
+      if (tree_any4(!ok)) break;                                 // no more pieces, or given up
       tc_fence_after();
       uint4 nan = make_uint4(0, 0, 0, 0);
       const bool any_nan = *reinterpret_cast<volatile int *>(&sh.nan_piece) > static_cast<int>(ip);
@@ -814,9 +849,6 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       }
       // Repeats of a row hold different positions: their states are merged, then summed by rows, `rep`
       // threads per row and 16 / rep columns each.
-      sh.ml[warp][lane][0] = st.ref;
-      sh.ml[warp][lane][1] = st.l;
-      if (!tree_sync4(sh, phase)) break;
       auto merged = [&](int w, int ln, float &l) {
         float M = -INFINITY;
         for (int i = w; i < 4; i += 4 >> shift) M = fmaxf(M, sh.ml[i][ln][0]);
@@ -837,7 +869,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       uint16_t *out = a.out + (pc.first + nd) * a.ldo + h * D + tc;
       float *po = part + tr * D + tc;
 #pragma unroll 1
-      for (int c = 0; c < D && ok; c += 16) {
+      for (int c = 0; c < D; c += 16) {
         uint32_t o[16];
         tree_ld<16>(tw + L::kColO + c, o);
 #pragma unroll
@@ -847,7 +879,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           for (int j = 0; j < 16; ++j)
             if ((w >> j) & 1u) sh.o[warp][lane][j] = NAN;
         }
-        if (!(ok = tree_sync4(sh, phase))) break;
+        tree_sync4();
         if (tr < pc.rows) {
 #pragma unroll 1
           for (int j = 0; j < cpt; j += 4) {
@@ -868,7 +900,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
             }
           }
         }
-        ok = tree_sync4(sh, phase);
+        tree_sync4();
       }
       if (!whole && tr < pc.rows && tc == 0) {
         float *ml = part + static_cast<int64_t>(a.row_cap) * D;
@@ -900,21 +932,46 @@ __global__ void __launch_bounds__(256) k_tree_attn_combine(const TreeAttnArgs a)
   const int G = a.Hq / a.Hkv, idx = meta[3] + r, node = a.by_group(idx);
   const int h = meta[5] * G + (idx - node * G);
   const int64_t slot = static_cast<int64_t>(a.row_cap) * (D + 2);
+  const float *base = a.part + r * D + V * lane;
+  const int64_t ml = static_cast<int64_t>(a.row_cap) * D + 2 * r;
   float M = -INFINITY, l = 0.0f, o[V] = {};
-  for (int j = i;; ++j) {
-    const float *part = a.part + (2 * static_cast<int64_t>(j) + (j == i ? 1 : 0)) * slot;
-    const float m = part[static_cast<int64_t>(a.row_cap) * D + 2 * r];
-    const float lj = part[static_cast<int64_t>(a.row_cap) * D + 2 * r + 1];
-    if (lj != 0.0f) {
-      const float top = fmaxf(M, m);
-      const float f = M == top ? 1.0f : tree_ex2(M - top), fj = m == top ? 1.0f : tree_ex2(m - top);
-      l = l * f + lj * fj;
-#pragma unroll
-      for (int v = 0; v < V; ++v) o[v] = o[v] * f + part[r * D + V * lane + v] * fj;
-      M = top;
+  // 32 parts at a time: their maxima and sums by lanes, then the values one after the other
+  for (int j0 = i;; j0 += 32) {
+    const int j = j0 + lane;
+    const bool in = j < static_cast<int>(gridDim.x);
+    const int kind = j == i ? 1 : (in ? a.meta[j * kTreeMetaInts] : 2);
+    const uint32_t ends = __ballot_sync(0xffffffffu, kind != 1);
+    const int last = ends ? __ffs(ends) - 1 : 31, num = last + (in ? 1 : 0);
+    const int n = __shfl_sync(0xffffffffu, num, last);           // behind the grid: not a part
+    float m = -INFINITY, lj = 0.0f;
+    if (lane < n) {
+      const float *p = a.part + (2 * static_cast<int64_t>(j) + (j == i ? 1 : 0)) * slot + ml;
+      m = p[0];
+      lj = p[1];
+      if (lj == 0.0f) m = -INFINITY;
     }
-    if (j > i && a.meta[j * kTreeMetaInts] != 1) break;
-    if (j + 1 >= static_cast<int>(gridDim.x)) break;
+    float top = m;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    top = fmaxf(top, M);
+    // a part without weight has l = 0; a NaN sum stays one
+    const float w = lj == 0.0f ? 0.0f : (m == top ? 1.0f : tree_ex2(m - top));
+    const float keep = l == 0.0f ? 0.0f : (M == top ? 1.0f : tree_ex2(M - top));
+    float sum = lj * w;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    l = l * keep + sum;
+#pragma unroll
+    for (int v = 0; v < V; ++v) o[v] *= keep;
+    M = top;
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+      const float *p = base + (2 * static_cast<int64_t>(j0 + k) + (j0 + k == i ? 1 : 0)) * slot;
+#pragma unroll
+      for (int v = 0; v < V; ++v) o[v] += p[v] * wk;
+    }
+    if (ends) break;
   }
   const float f = l == 0.0f ? 0.0f : a.scale3[2] / l;
   uint16_t *out = a.out + (static_cast<int64_t>(meta[2]) + node) * a.ldo + h * D + V * lane;

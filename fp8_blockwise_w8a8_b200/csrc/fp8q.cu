@@ -1198,6 +1198,7 @@ int fp8q_attention_tree(const void *q_e4m3, int64_t ldq, const void *k_cache, co
   a.meta = static_cast<int32_t *>(workspace);
   a.part = reinterpret_cast<float *>(a.meta + ctas * fp8q::kTreeMetaInts);
   const unsigned grid = static_cast<unsigned>(ctas < 2 * st->sms ? ctas : 2 * st->sms);
+  a.grid_recip = ~uint64_t{0} / grid;
   // rows per copy; blocks without a power of two of 4 or more go by gathers (box of one row)
   const int64_t pow2 = block_size & -block_size;
   a.box = static_cast<int>(pow2 > 64 ? 64 : pow2);
@@ -1205,22 +1206,18 @@ int fp8q_attention_tree(const void *q_e4m3, int64_t ldq, const void *k_cache, co
   a.by_block = tree_div(block_size);
   a.by_group = tree_div(Hq / Hkv);
   // a cache without slots: every position is out of range and loads row 0, here of q
-  const void *k_rows = num_slots > 0 ? k_cache : q_e4m3, *v_rows = num_slots > 0 ? v_cache : q_e4m3;
-  const int64_t map_rows = num_slots > 0 ? num_slots : 1;
-  CUtensorMap tm_k, tm_v;
+  CUtensorMap tm_k;
   if ((rc = get_encoder()) != FP8Q_OK ||
-      (rc = make_u8_row_map(&tm_k, k_rows, map_rows, Hkv * D, box, static_cast<uint32_t>(D),
+      (rc = make_u8_row_map(&tm_k, num_slots > 0 ? k_cache : q_e4m3, num_slots > 0 ? num_slots : 1,
+                            Hkv * D, box, static_cast<uint32_t>(D),
                             D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B)) !=
-          FP8Q_OK ||
-      (rc = make_u8_row_map(&tm_v, v_rows, map_rows, Hkv * D, box, static_cast<uint32_t>(D),
-                            CU_TENSOR_MAP_SWIZZLE_NONE)) != FP8Q_OK)
+          FP8Q_OK)
     return rc;
   if (D == 128)
-    fp8q::k_tree_attn<128><<<grid, fp8q::kTreeThreads, fp8q::TreeLayout<128>::kSmem, stream>>>(
-        tm_k, tm_v, a);
+    fp8q::k_tree_attn<128><<<grid, fp8q::kTreeThreads, fp8q::TreeLayout<128>::kSmem, stream>>>(tm_k,
+                                                                                               a);
   else
-    fp8q::k_tree_attn<64><<<grid, fp8q::kTreeThreads, fp8q::TreeLayout<64>::kSmem, stream>>>(
-        tm_k, tm_v, a);
+    fp8q::k_tree_attn<64><<<grid, fp8q::kTreeThreads, fp8q::TreeLayout<64>::kSmem, stream>>>(tm_k, a);
   if ((rc = launch_status()) != FP8Q_OK) return rc;
   // the merge as a programmatic dependent launch: scheduled while the first kernel drains
   cudaLaunchConfig_t cfg = {};

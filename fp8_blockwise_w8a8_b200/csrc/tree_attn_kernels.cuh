@@ -43,6 +43,7 @@ struct TreeAttnArgs {
   uint16_t *out;               // [total][ldo] bf16
   int64_t ldo;
   int box;                     // rows per copy: the power of two in block_size, at most 64; 1: gathers
+  uint64_t grid_recip;         // floor((2^64 - 1) / gridDim.x)
   TreeDiv by_block, by_group;  // by block_size and by G = Hq / Hkv
   int row_cap;                 // rows of a partial slot: min(128, max_nodes * Hq / Hkv)
   int32_t *meta;               // [CTAs][kTreeMetaInts]
@@ -75,9 +76,9 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeAttnArgs &a, int b, bool r
 // ---------------------------------------------------------------------------------------------
 constexpr int kTreeM = 128;          // query rows (node, head of the group) per row tile: TMEM lanes
 constexpr int kTreeN = 64;           // cached positions per tile
-constexpr int kTreeThreads = 320;    // 4 softmax warps, 4 convert warps, MMA warp, load warp
+constexpr int kTreeThreads = 352;    // 4 softmax warps, 4 for V, one each for the MMAs, K and Q
 constexpr int kTreeMaxCtas = 296;    // 2 per SM of 148
-constexpr int kTreeStages = 3;       // K and V tiles (codes) in shared memory
+constexpr int kTreeStages = 4;       // K tiles in shared memory
 constexpr int kTreeItemCost = 2;     // cost of starting a row tile, in position tiles
 constexpr int kTreeMinCost = 4;      // least cost per CTA
 constexpr int kTreeMetaInts = 8;
@@ -91,8 +92,8 @@ struct TreeLayout {
   static constexpr int kTile = kTreeN * D;
   static constexpr int kV16 = kK + kTreeStages * kTile;          // [2][D / 64][64][128 B], swizzled
   static constexpr int kV16Bytes = kTreeN * D * 2;
-  static constexpr int kV8 = kV16 + 2 * kV16Bytes;               // [stage][64][D]
-  static constexpr int kSmem = kV8 + kTreeStages * kTile + 1024;
+  static constexpr int kV8 = kV16 + 2 * kV16Bytes;               // [pair of V warps][64][D]
+  static constexpr int kSmem = kV8 + 2 * kTile + 1024;
   // TMEM columns: scores, two weight buffers (two fp16 a column), values
   static constexpr int kColS = 0, kColP = 64, kColO = 128, kCols = 256;
   static constexpr uint32_t kIdescQK = (1u << 4) | (static_cast<uint32_t>(kTreeN >> 3) << 17) |
@@ -145,8 +146,10 @@ struct TreeCursor {
     if (!live) return;
     s = tree_seq(a, b, false);
     const int64_t per_g = tree_group_cost(a, s, G);
-    g = static_cast<int>(off / per_g);
-    off -= g * per_g;
+    while (off >= per_g) {
+      off -= per_g;
+      ++g;
+    }
     int tiles;
     while (off >= (tiles = tree_tiles(a, s, G, rt) + kTreeItemCost)) {
       off -= tiles;
@@ -276,12 +279,17 @@ __device__ __forceinline__ void tree_st(uint32_t taddr, const uint32_t (&r)[N]) 
 
 // What the CTA's roles share.
 constexpr int kTreePieces = 4;   // descriptors in the ring
+struct TreeTile {                // for the V warps
+  int32_t slot[kTreeN];          // cache rows of the tile's positions, -1 where there is none
+  int32_t g, piece;              // kv head (-1: no more tiles), 1 + index of the piece
+};
 struct TreeShared {
-  uint64_t k_full[kTreeStages], k_free[kTreeStages], v8_full[kTreeStages], v8_free[kTreeStages];
+  uint64_t k_full[kTreeStages], k_free[kTreeStages], t_full[kTreeStages], t_free[kTreeStages];
   uint64_t piece_full[kTreePieces], piece_free[kTreePieces];
-  uint64_t q_full, v_full[2], s_full, s_free, p_full[2], pv_done[2], drain;
+  uint64_t q_full, q_free, v_full[2], s_full, s_free, p_full[2], pv_done[2], drain;
   uint64_t valid[8];             // per tile (mod 8): the positions that exist, one bit each
   TreePiece piece[kTreePieces];
+  TreeTile tile[kTreeStages];
   int start_b;
   int64_t start_off;
   int64_t warp_sum[kTreeThreads / 32];
@@ -289,7 +297,7 @@ struct TreeShared {
   int abort;
   int nan_piece;                 // 1 + index of the last piece with a NaN code in V
   float ml[4][32][2];
-  float o[4][32][17];
+  float4 o[4][32][5];            // 16 columns, rows 80 bytes apart
 };
 
 // The next piece of the ring for the calling warp; false where there is none.
@@ -319,8 +327,8 @@ __device__ __noinline__ uint4 tree_nan_dims(const TreeAttnArgs &a, const TreePie
       if (blk < 0 || blk >= a.num_blocks) continue;
       const int64_t slot = static_cast<int64_t>(blk) * a.block_size + pos % a.block_size;
       const uint32_t *v = reinterpret_cast<const uint32_t *>(a.v_cache + (slot * a.Hkv + c.g) * D);
-#pragma unroll
       for (int w = 0; w < D / 32; ++w)
+#pragma unroll 1
         for (int x = 0; x < 8; ++x) {
           const uint32_t word = v[8 * w + x];
           for (int y = 0; y < 4; ++y)
@@ -336,39 +344,38 @@ struct TreeRow {
   float ref, l;                  // reference of the weights (log2 units), their sum
 };
 
-// NC scores of this thread's row from TMEM; what is not seen (bit 0 on) becomes -inf.
-template <int NC>
-__device__ __forceinline__ void tree_scores(uint32_t taddr, uint64_t seen, uint32_t (&sr)[NC]) {
-  tree_ld<NC>(taddr, sr);
-  const uint32_t bits = static_cast<uint32_t>(seen), all = NC == 32 ? ~0u : (1u << (NC & 31)) - 1;
-  if (!__all_sync(0xffffffffu, (bits & all) == all)) {
+// Sixteen scores of this thread's row from TMEM; what is not seen (bit 0 on) becomes -inf.
+__device__ __forceinline__ void tree_scores(uint32_t taddr, uint64_t seen, uint32_t (&sr)[16]) {
+  tree_ld<16>(taddr, sr);
+  const uint32_t bits = static_cast<uint32_t>(seen) & 0xFFFFu;
+  if (!__all_sync(0xffffffffu, bits == 0xFFFFu)) {
 #pragma unroll
-    for (int j = 0; j < NC; ++j)
+    for (int j = 0; j < 16; ++j)
       if (!((bits >> j) & 1)) sr[j] = 0xFF800000u;
   }
 }
 
-// One position tile: the scores of NC * chunks columns of this thread's row become weights in TMEM.
+// One position tile: the scores of 16 * chunks columns of this thread's row become weights in TMEM.
 // The last chunk's scores stay in registers between the maximum and the weights, the others are read
-// again.
-template <int D, int NC>
+// again.  Loops over short bodies: the roles' code together has to stay in the instruction caches.
+template <int D>
 __device__ __forceinline__ bool tree_tile(TreeShared &sh, uint32_t tmem, uint32_t col0, int chunks,
                                           uint32_t it, bool first, uint64_t seen, float c2,
                                           TreeRow &st) {
   using L = TreeLayout<D>;
   if (!tree_wait<true>(sh.s_full, it, &sh.abort)) return false;
   tc_fence_after();
-  uint32_t sr[NC];
+  uint32_t sr[16];
   seen = (seen & sh.valid[it & 7u]) >> col0;
-  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  float mx[2] = {-INFINITY, -INFINITY};
   int c = 0;
 #pragma unroll 1
   do {
-    tree_scores<NC>(tmem + L::kColS + col0 + NC * c, seen >> (NC * c), sr);
+    tree_scores(tmem + L::kColS + col0 + 16 * c, seen >> (16 * c), sr);
 #pragma unroll
-    for (int j = 0; j < NC; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(sr[j]));
+    for (int j = 0; j < 16; ++j) mx[j & 1] = fmaxf(mx[j & 1], __uint_as_float(sr[j]));
   } while (++c < chunks);
-  const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
+  const float top = fmaxf(mx[0], mx[1]) * c2;
   // P buffer it & 1 was read by the MMA of tile it - 2
   if (it >= 2 && !tree_wait<true>(sh.pv_done[it & 1u], (it - 2) >> 1, &sh.abort)) return false;
   const bool up = top > st.ref + kTreeLag;                       // also the first score seen
@@ -391,7 +398,7 @@ __device__ __forceinline__ bool tree_tile(TreeShared &sh, uint32_t tmem, uint32_
     }
   }
   const float bias = kTreeBias - (st.ref == -INFINITY ? 0.0f : st.ref);
-  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  float sum[2] = {0.0f, 0.0f};
 #pragma unroll 1
   while (true) {
     --c;
@@ -399,20 +406,20 @@ __device__ __forceinline__ bool tree_tile(TreeShared &sh, uint32_t tmem, uint32_
       tc_fence_before();
       tree_arrive(sh.s_free);
     }
-    uint32_t pk[NC / 2];
+    uint32_t pk[8];
 #pragma unroll
-    for (int j = 0; j < NC; j += 2) {
+    for (int j = 0; j < 16; j += 2) {
       const float p0 = tree_ex2(fmaf(__uint_as_float(sr[j]), c2, bias));
       const float p1 = tree_ex2(fmaf(__uint_as_float(sr[j + 1]), c2, bias));
-      sum[j & 3] += p0;
-      sum[(j & 3) + 1] += p1;
+      sum[0] += p0;
+      sum[1] += p1;
       pk[j / 2] = f32x2_to_f16x2(p0, p1);
     }
-    tree_st<NC / 2>(tmem + L::kColP + 32 * (it & 1u) + (col0 + NC * c) / 2, pk);
+    tree_st<8>(tmem + L::kColP + 32 * (it & 1u) + col0 / 2 + 8 * c, pk);
     if (c == 0) break;
-    tree_scores<NC>(tmem + L::kColS + col0 + NC * (c - 1), seen >> (NC * (c - 1)), sr);
+    tree_scores(tmem + L::kColS + col0 + 16 * (c - 1), seen >> (16 * (c - 1)), sr);
   }
-  st.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  st.l += sum[0] + sum[1];
   tmem_st_wait();
   tc_fence_before();
   tree_arrive(sh.p_full[it & 1u]);
@@ -437,8 +444,7 @@ __device__ __forceinline__ bool tree_any4(bool v) {
 
 template <int D>
 __global__ void __launch_bounds__(kTreeThreads, 2)
-    k_tree_attn(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                const TreeAttnArgs a) {
+    k_tree_attn(const __grid_constant__ CUtensorMap tm_k, const TreeAttnArgs a) {
   using L = TreeLayout<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ TreeShared sh;
@@ -451,16 +457,17 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     for (int i = 0; i < kTreeStages; ++i) {
       mbar_init(smem_u32(&sh.k_full[i]), 1);
       mbar_init(smem_u32(&sh.k_free[i]), 1);
-      mbar_init(smem_u32(&sh.v8_full[i]), 1);
-      mbar_init(smem_u32(&sh.v8_free[i]), 4);
+      mbar_init(smem_u32(&sh.t_full[i]), 1);
+      mbar_init(smem_u32(&sh.t_free[i]), 2);
     }
     for (int i = 0; i < kTreePieces; ++i) {
       mbar_init(smem_u32(&sh.piece_full[i]), 1);
-      mbar_init(smem_u32(&sh.piece_free[i]), 9);
+      mbar_init(smem_u32(&sh.piece_free[i]), 6);
     }
-    mbar_init(smem_u32(&sh.q_full), 4);
+    mbar_init(smem_u32(&sh.q_full), 1);
+    mbar_init(smem_u32(&sh.q_free), 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&sh.v_full[i]), 4);
+      mbar_init(smem_u32(&sh.v_full[i]), 2);
       mbar_init(smem_u32(&sh.p_full[i]), 4);
       mbar_init(smem_u32(&sh.pv_done[i]), 1);
     }
@@ -512,11 +519,11 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     if (w < warp) upto += sh.warp_sum[w];
     total += sh.warp_sum[w];
   }
-  const int64_t most = (total + kTreeMinCost - 1) / kTreeMinCost;
-  const int64_t ctas = most < gridDim.x ? most : gridDim.x;
-  const bool works = blockIdx.x < ctas;
-  const int64_t lo = works ? total * blockIdx.x / ctas : 0;
-  const int64_t hi = works ? total * (blockIdx.x + 1) / ctas : 0;
+  // an even share, at least kTreeMinCost (the last CTAs may have less, or nothing)
+  const int64_t share = max(static_cast<int64_t>(kTreeMinCost),
+                            static_cast<int64_t>(__umul64hi(total, a.grid_recip)) + 1);
+  const int64_t lo = min(total, share * blockIdx.x), hi = min(total, lo + share);
+  const bool works = lo < hi;
   int32_t *meta = a.meta + blockIdx.x * kTreeMetaInts;
   if (tid == 0) meta[0] = meta[1] = 0;
   if (works && lo >= upto - mine && lo < upto) {
@@ -543,7 +550,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     TreeCursor pre;
     pre.init(a, G, B, sh.start_b, sh.start_off, hi - lo);
     const bool gather = a.box < 4;
-    const int chunks = kTreeN / a.box;
+    const int chunks = kTreeN / a.box, log_box = __ffs(a.box) - 1;
     const int first = gather ? lane : min(lane, chunks - 1) * a.box;
     int blk[2], off[2];
     auto look_up = [&]() {                                       // block ids of the cursor's tile
@@ -582,20 +589,16 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     for (;; ++it) {
       if (fresh && !publish()) break;
       if (!pre.live) break;
-      // the stages first: the block ids are on their way meanwhile
+      // the stage first: the block ids are on their way meanwhile
       if (!tree_wait<true>(sh.k_free[st], ph, &sh.abort) ||
-          !tree_wait<true>(sh.v8_free[st], ph, &sh.abort))
+          !tree_wait<true>(sh.t_free[st], ph, &sh.abort))
         break;
-      const uint32_t k_bar = smem_u32(&sh.k_full[st]), v_bar = smem_u32(&sh.v8_full[st]);
-      const uint32_t k_dst = sbase + L::kK + st * L::kTile, v_dst = sbase + L::kV8 + st * L::kTile;
-      const int x = pre.g * D;
       bool ok;
-      const int32_t row0 = slot_of(0, &ok);
-      int32_t row1 = 0;
+      int32_t slot[2] = {slot_of(0, &ok), 0};
       uint64_t there;
       if (gather) {
         there = __ballot_sync(0xffffffffu, ok);
-        row1 = slot_of(1, &ok);
+        slot[1] = slot_of(1, &ok);
         there |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, ok)) << 32;
       } else {
         const uint64_t bits = ok ? (a.box == 64 ? ~0ull : ((1ull << a.box) - 1) << first) : 0ull;
@@ -605,33 +608,37 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         const int left = pre.s.ctx + pre.s.n - pre.t * kTreeN;   // positions that exist
         if (left < 64) there &= (1ull << left) - 1;
       }
+      const uint32_t bar = smem_u32(&sh.k_full[st]);
       if (lane == 0) {
         sh.valid[it & 7u] = there;
-        mbar_arrive_expect_tx(k_bar, L::kTile);
-        mbar_arrive_expect_tx(v_bar, L::kTile);
+        sh.tile[st].g = pre.g;
+        sh.tile[st].piece = static_cast<int>(ip);
+        mbar_arrive_expect_tx(bar, L::kTile);
       }
+      __syncwarp();
+      const uint32_t dst = sbase + L::kK + st * L::kTile;
       if (gather) {
-#pragma unroll 1
-        for (int c = 0; c < 16; ++c) {
-          const int32_t v = c < 8 ? row0 : row1;
-          int32_t rows[4];
+        int32_t rows[4];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) rows[r] = __shfl_sync(0xffffffffu, v, (4 * c + r) & 31);
-          if (lane == 0) {
-            tma_gather4(k_dst + 4 * D * c, &tm_k, x, rows, k_bar);
-            tma_gather4(v_dst + 4 * D * c, &tm_v, x, rows, v_bar);
-          }
+        for (int r = 0; r < 4; ++r) {
+          const int32_t v0 = __shfl_sync(0xffffffffu, slot[0], (4 * lane + r) & 31);
+          const int32_t v1 = __shfl_sync(0xffffffffu, slot[1], (4 * lane + r) & 31);
+          rows[r] = lane & 8 ? v1 : v0;
         }
+        if (lane < 16) tma_gather4(dst + 4 * D * lane, &tm_k, pre.g * D, rows, bar);
       } else {
-#pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
-          const int32_t row = __shfl_sync(0xffffffffu, row0, c);
-          if (lane == 0) {
-            tma_load_2d(k_dst + c * a.box * D, &tm_k, x, row, k_bar);
-            tma_load_2d(v_dst + c * a.box * D, &tm_v, x, row, v_bar);
-          }
+        if (lane < chunks) tma_load_2d(dst + lane * a.box * D, &tm_k, pre.g * D, slot[0], bar);
+        const int32_t row = slot[0];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int p = 32 * j + lane;
+          slot[j] = __shfl_sync(0xffffffffu, row, p >> log_box) + (p & (a.box - 1));
         }
       }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        sh.tile[st].slot[32 * j + lane] = (there >> (32 * j + lane)) & 1u ? slot[j] : -1;
+      tree_arrive(sh.t_full[st]);
       if (++st == kTreeStages) {
         st = 0;
         ph ^= 1u;
@@ -640,101 +647,115 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       if (fresh) pre.next(a, G, 0);
       look_up();
     }
-    // after a wait that gave up: no copy in flight at exit
-    for (uint32_t i = it < kTreeStages ? 0 : it - kTreeStages; i < it; ++i) {
-      wait_drain(smem_u32(&sh.k_full[i % kTreeStages]), (i / kTreeStages) & 1u);
-      wait_drain(smem_u32(&sh.v8_full[i % kTreeStages]), (i / kTreeStages) & 1u);
+    // the end, for both pairs of V warps
+    for (int i = 0; i < 2; ++i) {
+      if (!tree_wait<true>(sh.t_free[st], ph, &sh.abort)) break;
+      if (lane == 0) sh.tile[st].g = -1;
+      tree_arrive(sh.t_full[st]);
+      if (++st == kTreeStages) {
+        st = 0;
+        ph ^= 1u;
+      }
     }
-  } else if (warp >= 4 && warp < 8) {
-    // ---------------------------------------------------------------- queries, V codes to fp16
-    constexpr int NR = D / 32;                                   // rows of a tile per thread
-    constexpr int LPR = D / 16;                                  // lanes per row
-    const int lw = warp - 4, lt = tid - 128, ch = lane % LPR;
+    // after a wait that gave up: no copy in flight at exit
+    for (uint32_t i = it < kTreeStages ? 0 : it - kTreeStages; i < it; ++i)
+      wait_drain(smem_u32(&sh.k_full[i % kTreeStages]), (i / kTreeStages) & 1u);
+  } else if (warp == 10) {
+    // ---------------------------------------------------------------- queries
+    constexpr int LPR = D / 16;                                  // 16-byte chunks per row
     const float c = a.sm_scale * a.scale3[0] * a.scale3[1];
     const uint32_t qflip = c < 0.0f ? 0x80808080u : 0u;          // a negative scale negates Q
     TreePiece pc;
-    uint32_t it = 0, st = 0, ph = 0;
     bool ok = true;
     for (uint32_t ip = 0; ok && tree_take(sh, ip, pc); ++ip) {
-      // Q rows of the piece, once the scores of the piece before are complete: row r is head
-      // g G + r % G of node r / G; up to 32 (64) rows are repeated 4 (2) times down the tile
-      if (it > 0 && !tree_wait<true>(sh.s_full, it - 1, &sh.abort)) break;
+      // row r is head g G + r % G of node r / G; up to 32 (64) rows are repeated 4 (2) times down the
+      // tile.  The loads are on their way while the scores of the piece before complete.
       const int step = pc.rows <= 32 ? 32 : (pc.rows <= 64 ? 64 : 128);
-#pragma unroll 4
-      for (int i = lt; i < kTreeM * LPR; i += 128) {
-        const int r = i / LPR, c16 = i % LPR, rr = r & (step - 1);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (rr < pc.rows) {
-          const int idx = pc.row0 + rr, node = a.by_group(idx), h = pc.g * G + (idx - node * G);
-          v = *reinterpret_cast<const uint4 *>(a.q + (pc.first + node) * a.ldq + h * D + c16 * 16);
-          v.x ^= qflip; v.y ^= qflip; v.z ^= qflip; v.w ^= qflip;
+#pragma unroll 1
+      for (int i0 = 0; i0 < step * LPR; i0 += 256) {
+        uint4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int i = i0 + 32 * k + lane, r = i / LPR;
+          v[k] = make_uint4(0, 0, 0, 0);
+          if (r < pc.rows) {
+            const int idx = pc.row0 + r, node = a.by_group(idx), h = pc.g * G + (idx - node * G);
+            v[k] = *reinterpret_cast<const uint4 *>(a.q + (pc.first + node) * a.ldq + h * D +
+                                                    i % LPR * 16);
+          }
         }
-        *reinterpret_cast<uint4 *>(smem + L::kQ + r * 128 + ((c16 ^ (r & 7)) << 4)) = v;
+        if (i0 == 0 && !(ok = tree_wait<true>(sh.q_free, ip ^ 1u, &sh.abort))) break;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int i = i0 + 32 * k + lane, r = i / LPR;
+          v[k].x ^= qflip; v[k].y ^= qflip; v[k].z ^= qflip; v[k].w ^= qflip;
+          for (int rr = r; r < step && rr < kTreeM; rr += step)
+            *reinterpret_cast<uint4 *>(smem + L::kQ + rr * 128 + ((i % LPR ^ (r & 7)) << 4)) = v[k];
+        }
       }
       fence_proxy_async_shared();
       tree_arrive(sh.q_full);
+    }
+  } else if (warp >= 4 && warp < 8) {
+    // ---------------------------------------------------------------- V codes to fp16
+    // Two pairs of warps take the tiles in turn, each into its own buffer.
+    constexpr int LPR = D / 16;                                  // lanes per row
+    constexpr int RPS = 64 / LPR, NR = kTreeN / RPS;             // rows per step, steps
+    const int pair = (warp - 4) >> 1, gt = tid - 128 - 64 * pair, ch = gt % LPR;
+    const int64_t row = static_cast<int64_t>(a.Hkv) * D;
+    const uint32_t stage = sbase + L::kV8 + pair * L::kTile + gt * 16;
+    for (uint32_t it = pair;; it += 2) {
+      const uint32_t st = it % kTreeStages;
+      if (!tree_wait<true>(sh.t_full[st], it / kTreeStages, &sh.abort)) break;
+      const TreeTile &tile = sh.tile[st];
+      const int32_t g = tile.g, piece = tile.piece;
+      if (g < 0) break;
+      // each thread copies and converts 16 codes of every step's row
+      const uint8_t *col = a.v_cache + g * D + ch * 16;
+#pragma unroll 2
+      for (int j = 0; j < NR; ++j) {
+        const int32_t slot = tile.slot[j * RPS + gt / LPR];
+        cp_async16(stage + j * 1024, col + static_cast<int64_t>(max(slot, 0)) * row,
+                   slot >= 0 ? 16u : 0u);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      tree_arrive(sh.t_free[st]);
+      if (it >= 2 && !tree_wait<true>(sh.pv_done[pair], (it - 2) >> 1, &sh.abort)) break;
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      // the halves of a row's dims are stored in opposite order, so that a quarter warp covers all
+      // banks
+      const int half = D == 128 ? ch >> 2 : 0, c0 = (ch & 3) * 2;
+      uint8_t *dst = smem + L::kV16 + pair * L::kV16Bytes + half * 8192 + gt / LPR * 128;
+      const int at0 = ((c0 + half) ^ (gt / LPR & 7)) << 4;       // RPS is a multiple of 8
 #pragma unroll 1
-      for (int t = pc.t; t < pc.t_end; ++t, ++it) {
-        if (!(ok = tree_wait<true>(sh.v8_full[st], ph, &sh.abort))) break;
-        uint4 v8[NR];
-#pragma unroll
-        for (int j = 0; j < NR; ++j) {
-          const int p = 16 * lw + j * (32 / LPR) + lane / LPR;
-          v8[j] = *reinterpret_cast<const uint4 *>(smem + L::kV8 + st * L::kTile + p * D + ch * 16);
-        }
-        const uint32_t there = static_cast<uint32_t>(sh.valid[it & 7u] >> (16 * lw));
-        tree_arrive(sh.v8_free[st]);
-        if (++st == kTreeStages) {
-          st = 0;
-          ph ^= 1u;
-        }
-        if (it >= 2 && !(ok = tree_wait<true>(sh.pv_done[it & 1u], (it - 2) >> 1, &sh.abort))) break;
-        // V codes to fp16 (exact).  Where a NaN turns up the codes are cleared of it (it is put back
-        // into the results of the rows that see it) and converted again.
-        uint8_t *v16 = smem + L::kV16 + (it & 1u) * L::kV16Bytes;
-        bool nan = false;
-#pragma unroll 1
+      for (int j = 0; j < NR; ++j) {
+        uint4 v8 = *reinterpret_cast<const uint4 *>(smem + (stage - sbase) + j * 1024);
+        uint32_t h[8];
         while (true) {
+          const uint32_t w[4] = {v8.x, v8.y, v8.z, v8.w};
           __half2 acc = __half2half2(__ushort_as_half(0));
 #pragma unroll
-          for (int j = 0; j < NR; ++j) {
-            const int p = 16 * lw + j * (32 / LPR) + lane / LPR;
-            const uint32_t w[4] = {v8[j].x, v8[j].y, v8[j].z, v8[j].w};
-            uint32_t h[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              h[k] = e4m3x2_to_f16x2(k & 1 ? w[k / 2] >> 16 : w[k / 2] & 0xFFFFu);
-              acc = __hmax2_nan(acc, *reinterpret_cast<const __half2 *>(&h[k]));
-            }
-            // the halves of a row's dims are stored in opposite order, so that a quarter warp covers
-            // all banks
-            const int half = D == 128 ? ch >> 2 : 0, c0 = (ch & 3) * 2;
-            uint8_t *dst = v16 + half * 8192 + p * 128;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int e = k ^ half;
-              *reinterpret_cast<uint4 *>(dst + (((c0 + e) ^ (p & 7)) << 4)) =
-                  e ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
-            }
+          for (int k = 0; k < 8; ++k) {
+            h[k] = e4m3x2_to_f16x2(k & 1 ? w[k / 2] >> 16 : w[k / 2] & 0xFFFFu);
+            acc = __hmax2_nan(acc, *reinterpret_cast<const __half2 *>(&h[k]));
           }
           if (!__hisnan(__low2half(acc)) && !__hisnan(__high2half(acc))) break;
+          // A NaN code becomes 0; it is put back into the results of the rows that see it.
+          uint32_t *x[4] = {&v8.x, &v8.y, &v8.z, &v8.w};
 #pragma unroll
-          for (int j = 0; j < NR; ++j) {
-            const int p16 = j * (32 / LPR) + lane / LPR;
-            uint32_t *w[4] = {&v8[j].x, &v8[j].y, &v8[j].z, &v8[j].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t n7 = ((*w[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-              nan |= n7 != 0 && ((there >> p16) & 1u) != 0;
-              *w[k] &= ~((n7 >> 7) * 0xFFu);
-            }
-          }
+          for (int k = 0; k < 4; ++k)
+            *x[k] &= ~(((((*x[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xFFu);
+          atomicMax(&sh.nan_piece, piece);
         }
-        if (nan) atomicMax(&sh.nan_piece, static_cast<int>(ip + 1));
-        fence_proxy_async_shared();
-        tree_arrive(sh.v_full[it & 1u]);
+        uint4 *d0 = reinterpret_cast<uint4 *>(dst + j * RPS * 128 + at0);
+        uint4 *d1 = reinterpret_cast<uint4 *>(dst + j * RPS * 128 + (at0 ^ 16));
+        *d0 = half ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
+        *d1 = half ? make_uint4(h[0], h[1], h[2], h[3]) : make_uint4(h[4], h[5], h[6], h[7]);
       }
+      fence_proxy_async_shared();
+      tree_arrive(sh.v_full[pair]);
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");         // none in flight at exit
   } else if (warp == 8) {
     // ---------------------------------------------------------------- MMA issue
     if (lane == 0) {
@@ -758,36 +779,47 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       // the scores of tile it, then the values of tile it - 1
 #pragma unroll 1
       for (uint32_t it = 0;; ++it) {
-        if (live) {
-          if ((it > 0 && !tree_wait<false>(sh.s_free, it - 1, &sh.abort)) ||
-              (fresh && !tree_wait<false>(sh.q_full, ip - 1, &sh.abort)) ||
-              !tree_wait<false>(sh.k_full[st], ph, &sh.abort))
-            break;
-          tc_fence_after();
-          const uint64_t kd = tree_sdesc_k<D>(sbase + L::kK + st * L::kTile);
+        // the values first where the next scores wait for another piece's queries
+        bool ok = true;
+#pragma unroll 1
+        for (int k = 0; k < 2 && ok; ++k) {
+          if (fresh == (k == 1)) {
+            if (!live) continue;
+            if ((it > 0 && !tree_wait<false>(sh.s_free, it - 1, &sh.abort)) ||
+                (fresh && !tree_wait<false>(sh.q_full, ip - 1, &sh.abort)) ||
+                !tree_wait<false>(sh.k_full[st], ph, &sh.abort)) {
+              ok = false;
+              continue;
+            }
+            tc_fence_after();
+            const uint64_t kd = tree_sdesc_k<D>(sbase + L::kK + st * L::kTile);
 #pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk)
-            mma_f8f6f4(tmem + L::kColS, qd + 2 * kk, kd + 2 * kk, L::kIdescQK, kk > 0 ? 1u : 0u);
-          mma_commit(smem_u32(&sh.s_full));
-          mma_commit(smem_u32(&sh.k_free[st]));
-          if (++st == kTreeStages) {
-            st = 0;
-            ph ^= 1u;
+            for (int kk = 0; kk < D / 32; ++kk)
+              mma_f8f6f4(tmem + L::kColS, qd + 2 * kk, kd + 2 * kk, L::kIdescQK, kk > 0 ? 1u : 0u);
+            mma_commit(smem_u32(&sh.s_full));
+            mma_commit(smem_u32(&sh.k_free[st]));
+            if (left == 0) mma_commit(smem_u32(&sh.q_free));     // the piece's last scores
+            if (++st == kTreeStages) {
+              st = 0;
+              ph ^= 1u;
+            }
+          } else if (it > 0) {
+            const uint32_t i = (it - 1) & 1u, pp = (it - 1) >> 1;
+            if (!tree_wait<false>(sh.p_full[i], pp, &sh.abort) ||
+                !tree_wait<false>(sh.v_full[i], pp, &sh.abort)) {
+              ok = false;
+              continue;
+            }
+            tc_fence_after();
+            const uint64_t vd = tree_sdesc_v(sbase + L::kV16 + i * L::kV16Bytes);
+#pragma unroll
+            for (int kk = 0; kk < kTreeN / 16; ++kk)
+              mma_f16_ts(tmem + L::kColO, tmem + L::kColP + 32 * i + 8 * kk, vd + 128 * kk,
+                         L::kIdescPV, before && kk == 0 ? 0u : 1u);
+            mma_commit(smem_u32(&sh.pv_done[i]));
           }
         }
-        if (it > 0) {
-          const uint32_t i = (it - 1) & 1u, pp = (it - 1) >> 1;
-          if (!tree_wait<false>(sh.p_full[i], pp, &sh.abort) ||
-              !tree_wait<false>(sh.v_full[i], pp, &sh.abort))
-            break;
-          tc_fence_after();
-          const uint64_t vd = tree_sdesc_v(sbase + L::kV16 + i * L::kV16Bytes);
-#pragma unroll
-          for (int kk = 0; kk < kTreeN / 16; ++kk)
-            mma_f16_ts(tmem + L::kColO, tmem + L::kColP + 32 * i + 8 * kk, vd + 128 * kk,
-                       L::kIdescPV, before && kk == 0 ? 0u : 1u);
-          mma_commit(smem_u32(&sh.pv_done[i]));
-        }
+        if (!ok) break;
         if (!live) break;
         before = fresh;
         live = next();
@@ -823,8 +855,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         // a row that does not exist counts as seeing all (its scores are 0, its results unused)
         const uint64_t seen = live ? tree_bits(mrow, words, node, t * kTreeN - pc.ctx) : ~0ull;
         const bool first = t == pc.t;
-        ok = rep == 4 ? tree_tile<D, 16>(sh, tw, col0, 1, it, first, seen, c2, st)
-                      : tree_tile<D, 32>(sh, tw, col0, 2 >> shift, it, first, seen, c2, st);
+        ok = tree_tile<D>(sh, tw, col0, 4 >> shift, it, first, seen, c2, st);
       }
       ok = ok && tree_wait<true>(sh.pv_done[(it - 1) & 1u], (it - 1) >> 1, &sh.abort);
       sh.ml[warp][lane][0] = st.ref;
@@ -868,36 +899,62 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       const int idx = pc.row0 + tr, nd = a.by_group(idx), h = pc.g * G + (idx - nd * G);
       uint16_t *out = a.out + (pc.first + nd) * a.ldo + h * D + tc;
       float *po = part + tr * D + tc;
+      auto store4 = [&](int c, float4 v) {
+        if (whole) {
+          const __nv_bfloat162 b0 = __floats2bfloat162_rn(v.x * scale, v.y * scale);
+          const __nv_bfloat162 b1 = __floats2bfloat162_rn(v.z * scale, v.w * scale);
+          *reinterpret_cast<uint2 *>(out + c) =
+              make_uint2(*reinterpret_cast<const uint32_t *>(&b0),
+                         *reinterpret_cast<const uint32_t *>(&b1));
+        } else {
+          *reinterpret_cast<float4 *>(po + c) = v;
+        }
+      };
 #pragma unroll 1
       for (int c = 0; c < D; c += 16) {
         uint32_t o[16];
         tree_ld<16>(tw + L::kColO + c, o);
+        float4 v[4];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) sh.o[warp][lane][j] = __uint_as_float(o[j]) * f;
+        for (int j = 0; j < 4; ++j)
+          v[j] = make_float4(__uint_as_float(o[4 * j]) * f, __uint_as_float(o[4 * j + 1]) * f,
+                             __uint_as_float(o[4 * j + 2]) * f, __uint_as_float(o[4 * j + 3]) * f);
         if (any_nan) {
           const uint32_t w = (c < 64 ? (c < 32 ? nan.x : nan.y) : (c < 96 ? nan.z : nan.w)) >> (c & 31);
-          for (int j = 0; j < 16; ++j)
-            if ((w >> j) & 1u) sh.o[warp][lane][j] = NAN;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if ((w >> (4 * j)) & 1u) v[j].x = NAN;
+            if ((w >> (4 * j)) & 2u) v[j].y = NAN;
+            if ((w >> (4 * j)) & 4u) v[j].z = NAN;
+            if ((w >> (4 * j)) & 8u) v[j].w = NAN;
+          }
         }
+        if (rep == 1) {
+          if (live) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) store4(c + 4 * j, v[j]);
+          }
+          continue;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sh.o[warp][lane][j] = v[j];
         tree_sync4();
         if (tr < pc.rows) {
-#pragma unroll 1
-          for (int j = 0; j < cpt; j += 4) {
-            float v[4] = {};
-            for (int w = tr >> 5; w < 4; w += 4 >> shift)
+          // four reads: four warps' columns, or two warps' twice as many
+          float4 x[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) v[k] += sh.o[w][tr & 31][tc + j + k];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] *= scale;
-            if (whole) {
-              const __nv_bfloat162 b0 = __floats2bfloat162_rn(v[0], v[1]);
-              const __nv_bfloat162 b1 = __floats2bfloat162_rn(v[2], v[3]);
-              *reinterpret_cast<uint2 *>(out + c + j) =
-                  make_uint2(*reinterpret_cast<const uint32_t *>(&b0),
-                             *reinterpret_cast<const uint32_t *>(&b1));
-            } else {
-              *reinterpret_cast<float4 *>(po + c + j) = make_float4(v[0], v[1], v[2], v[3]);
-            }
+          for (int j = 0; j < 4; ++j)
+            x[j] = rep == 4 ? sh.o[j][tr][tid & 3]
+                            : sh.o[(tr >> 5) + 2 * (j & 1)][tr & 31][2 * (tid & 1) + (j >> 1)];
+          const float4 s0 = make_float4(x[0].x + x[1].x, x[0].y + x[1].y, x[0].z + x[1].z,
+                                        x[0].w + x[1].w);
+          const float4 s1 = make_float4(x[2].x + x[3].x, x[2].y + x[3].y, x[2].z + x[3].z,
+                                        x[2].w + x[3].w);
+          if (rep == 4) {
+            store4(c, make_float4(s0.x + s1.x, s0.y + s1.y, s0.z + s1.z, s0.w + s1.w));
+          } else {
+            store4(c, s0);
+            store4(c + 4, s1);
           }
         }
         tree_sync4();

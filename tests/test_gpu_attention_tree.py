@@ -165,6 +165,17 @@ def test_many_short_sequences():
     _check(o, d)
 
 
+@pytest.mark.parametrize("D,bs", [(64, 7), (64, 16), (128, 7), (128, 32)])
+def test_many_items_of_few_tiles(D, bs):
+    """Several items per CTA, of one to five position tiles each: what is handed from one item to the
+    next (queries, buffers, accumulators) with every parity of the tile counts."""
+    rng = np.random.default_rng(68)
+    d = _case(32, 16, D, rng.integers(1, 10, 40).tolist(), rng.integers(0, 310, 40).tolist(), bs, 68)
+    o = fq.attention_tree(*_args(d))
+    assert fq.check_device_error() == 0
+    _check(o, d)
+
+
 @pytest.mark.parametrize("sm_scale", [0.0, -0.09, 0.5])
 def test_softmax_scales(sm_scale):
     d = _case(8, 2, 128, [12, 40], [200, 333], 16, seed=55)

@@ -48,6 +48,12 @@ __device__ __forceinline__ float2 f2_mul_rn(float2 a, float2 b) {
   return f2_unpack(d);
 }
 
+__device__ __forceinline__ float2 f2_fma_rn(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(f2_pack(a)), "l"(f2_pack(b)), "l"(f2_pack(c)));
+  return f2_unpack(d);
+}
+
 __device__ __forceinline__ float2 f2_add_rn(float2 a, float2 b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(f2_pack(a)), "l"(f2_pack(b)));

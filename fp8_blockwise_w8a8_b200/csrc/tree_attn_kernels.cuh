@@ -94,8 +94,9 @@ struct TreeLayout {
   static constexpr int kV16Bytes = kTreeN * D * 2;
   static constexpr int kV8 = kV16 + 2 * kV16Bytes;               // [pair of V warps][64][D]
   static constexpr int kSmem = kV8 + 2 * kTile + 1024;
-  // TMEM columns: scores, two weight buffers (two fp16 a column), values
-  static constexpr int kColS = 0, kColP = 64, kColO = 128, kCols = 256;
+  // TMEM columns: two score buffers, whose first halves then hold the weights (two fp16 a column),
+  // and the values
+  static constexpr int kColS = 0, kColO = 128, kCols = 256;
   static constexpr uint32_t kIdescQK = (1u << 4) | (static_cast<uint32_t>(kTreeN >> 3) << 17) |
                                        (static_cast<uint32_t>(kTreeM >> 4) << 24);
   // kind::f16, fp16 operands, B with its columns (dims) contiguous (bit 16)
@@ -286,7 +287,7 @@ struct TreeTile {                // for the V warps
 struct TreeShared {
   uint64_t k_full[kTreeStages], k_free[kTreeStages], t_full[kTreeStages], t_free[kTreeStages];
   uint64_t piece_full[kTreePieces], piece_free[kTreePieces];
-  uint64_t q_full, q_free, v_full[2], s_full, s_free, p_full[2], pv_done[2], drain;
+  uint64_t q_full, q_free, v_full[2], s_full[2], p_full[2], pv_done[2], drain;
   uint64_t valid[8];             // per tile (mod 8): the positions that exist, one bit each
   TreePiece piece[kTreePieces];
   TreeTile tile[kTreeStages];
@@ -355,29 +356,30 @@ __device__ __forceinline__ void tree_scores(uint32_t taddr, uint64_t seen, uint3
   }
 }
 
-// One position tile: the scores of 16 * chunks columns of this thread's row become weights in TMEM.
-// The last chunk's scores stay in registers between the maximum and the weights, the others are read
-// again.  Loops over short bodies: the roles' code together has to stay in the instruction caches.
+// One position tile: the scores of 16 * chunks columns of this thread's row become weights, in the
+// first half of the score buffer's columns: 8 columns per chunk, behind those already read.  The first
+// chunk's scores stay in registers between the maximum and the weights, the others are read again.
+// Loops over short bodies: the roles' code together has to stay in the instruction caches.
 template <int D>
 __device__ __forceinline__ bool tree_tile(TreeShared &sh, uint32_t tmem, uint32_t col0, int chunks,
                                           uint32_t it, bool first, uint64_t seen, float c2,
                                           TreeRow &st) {
   using L = TreeLayout<D>;
-  if (!tree_wait<true>(sh.s_full, it, &sh.abort)) return false;
+  if (!tree_wait<true>(sh.s_full[it & 1u], it >> 1, &sh.abort)) return false;
   tc_fence_after();
+  const uint32_t buf = tmem + L::kColS + 64 * (it & 1u);
   uint32_t sr[16];
   seen = (seen & sh.valid[it & 7u]) >> col0;
   float mx[2] = {-INFINITY, -INFINITY};
-  int c = 0;
+  int c = chunks;
 #pragma unroll 1
   do {
-    tree_scores(tmem + L::kColS + col0 + 16 * c, seen >> (16 * c), sr);
+    --c;
+    tree_scores(buf + col0 + 16 * c, seen >> (16 * c), sr);
 #pragma unroll
     for (int j = 0; j < 16; ++j) mx[j & 1] = fmaxf(mx[j & 1], __uint_as_float(sr[j]));
-  } while (++c < chunks);
+  } while (c > 0);
   const float top = fmaxf(mx[0], mx[1]) * c2;
-  // P buffer it & 1 was read by the MMA of tile it - 2
-  if (it >= 2 && !tree_wait<true>(sh.pv_done[it & 1u], (it - 2) >> 1, &sh.abort)) return false;
   const bool up = top > st.ref + kTreeLag;                       // also the first score seen
   if (__any_sync(0xffffffffu, up)) {
     const bool held = up && st.ref != -INFINITY;                 // values to rescale
@@ -398,28 +400,30 @@ __device__ __forceinline__ bool tree_tile(TreeShared &sh, uint32_t tmem, uint32_
     }
   }
   const float bias = kTreeBias - (st.ref == -INFINITY ? 0.0f : st.ref);
-  float sum[2] = {0.0f, 0.0f};
+  const float2 c22 = make_float2(c2, c2), bias2 = make_float2(bias, bias);
+  float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll 1
   while (true) {
-    --c;
-    if (c == 0) {                                                // the last read of the scores
-      tc_fence_before();
-      tree_arrive(sh.s_free);
-    }
     uint32_t pk[8];
 #pragma unroll
     for (int j = 0; j < 16; j += 2) {
-      const float p0 = tree_ex2(fmaf(__uint_as_float(sr[j]), c2, bias));
-      const float p1 = tree_ex2(fmaf(__uint_as_float(sr[j + 1]), c2, bias));
-      sum[0] += p0;
-      sum[1] += p1;
-      pk[j / 2] = f32x2_to_f16x2(p0, p1);
+      const float2 z = f2_fma_rn(make_float2(__uint_as_float(sr[j]), __uint_as_float(sr[j + 1])), c22,
+                                 bias2);
+      const float2 w = make_float2(tree_ex2(z.x), tree_ex2(z.y));
+      sum = f2_add_rn(sum, w);
+      pk[j / 2] = f32x2_to_f16x2(w.x, w.y);
     }
-    tree_st<8>(tmem + L::kColP + 32 * (it & 1u) + col0 / 2 + 8 * c, pk);
-    if (c == 0) break;
-    tree_scores(tmem + L::kColS + col0 + 16 * (c - 1), seen >> (16 * (c - 1)), sr);
+    tree_st<8>(buf + col0 / 2 + 8 * c, pk);
+    if (++c >= chunks) break;
+    tree_scores(buf + col0 + 16 * c, seen >> (16 * c), sr);
   }
-  st.l += sum[0] + sum[1];
+  // a repeat of a row has no weight at the other repeats' positions
+#pragma unroll 1
+  for (int i = 8 * chunks; i < 32; i += 8) {
+    const uint32_t z[8] = {};
+    tree_st<8>(buf + ((col0 / 2 + i) & 31u), z);
+  }
+  st.l += sum.x + sum.y;
   tmem_st_wait();
   tc_fence_before();
   tree_arrive(sh.p_full[it & 1u]);
@@ -470,9 +474,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       mbar_init(smem_u32(&sh.v_full[i]), 2);
       mbar_init(smem_u32(&sh.p_full[i]), 4);
       mbar_init(smem_u32(&sh.pv_done[i]), 1);
+      mbar_init(smem_u32(&sh.s_full[i]), 1);
     }
-    mbar_init(smem_u32(&sh.s_full), 1);
-    mbar_init(smem_u32(&sh.s_free), 4);
     mbar_init(smem_u32(&sh.drain), 1);
     sh.abort = 0;
     sh.nan_piece = 0;
@@ -701,7 +704,11 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     // Two pairs of warps take the tiles in turn, each into its own buffer.
     constexpr int LPR = D / 16;                                  // lanes per row
     constexpr int RPS = 64 / LPR, NR = kTreeN / RPS;             // rows per step, steps
-    const int pair = (warp - 4) >> 1, gt = tid - 128 - 64 * pair, ch = gt % LPR;
+    // a quarter warp's 16-byte stores cover all banks: its lanes hold four chunks of one half of two
+    // neighbouring rows
+    const int pair = (warp - 4) >> 1, gt = tid - 128 - 64 * pair;
+    const int ch = D == 128 ? (gt & 3) | (gt >> 1 & 4) : gt & 3;
+    const int r0 = D == 128 ? (gt >> 2 & 1) | (gt >> 4 << 1) : gt >> 2;
     const int64_t row = static_cast<int64_t>(a.Hkv) * D;
     const uint32_t stage = sbase + L::kV8 + pair * L::kTile + gt * 16;
     for (uint32_t it = pair;; it += 2) {
@@ -714,7 +721,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       const uint8_t *col = a.v_cache + g * D + ch * 16;
 #pragma unroll 2
       for (int j = 0; j < NR; ++j) {
-        const int32_t slot = tile.slot[j * RPS + gt / LPR];
+        const int32_t slot = tile.slot[j * RPS + r0];
         cp_async16(stage + j * 1024, col + static_cast<int64_t>(max(slot, 0)) * row,
                    slot >= 0 ? 16u : 0u);
       }
@@ -722,11 +729,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       tree_arrive(sh.t_free[st]);
       if (it >= 2 && !tree_wait<true>(sh.pv_done[pair], (it - 2) >> 1, &sh.abort)) break;
       asm volatile("cp.async.wait_group 0;" ::: "memory");
-      // the halves of a row's dims are stored in opposite order, so that a quarter warp covers all
-      // banks
-      const int half = D == 128 ? ch >> 2 : 0, c0 = (ch & 3) * 2;
-      uint8_t *dst = smem + L::kV16 + pair * L::kV16Bytes + half * 8192 + gt / LPR * 128;
-      const int at0 = ((c0 + half) ^ (gt / LPR & 7)) << 4;       // RPS is a multiple of 8
+      uint8_t *dst = smem + L::kV16 + pair * L::kV16Bytes + (ch >> 2) * 8192 + r0 * 128;
+      const int at0 = ((ch & 3) * 2 ^ (r0 & 7)) << 4;            // RPS is a multiple of 8
 #pragma unroll 1
       for (int j = 0; j < NR; ++j) {
         uint4 v8 = *reinterpret_cast<const uint4 *>(smem + (stage - sbase) + j * 1024);
@@ -747,10 +751,9 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
             *x[k] &= ~(((((*x[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xFFu);
           atomicMax(&sh.nan_piece, piece);
         }
-        uint4 *d0 = reinterpret_cast<uint4 *>(dst + j * RPS * 128 + at0);
-        uint4 *d1 = reinterpret_cast<uint4 *>(dst + j * RPS * 128 + (at0 ^ 16));
-        *d0 = half ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
-        *d1 = half ? make_uint4(h[0], h[1], h[2], h[3]) : make_uint4(h[4], h[5], h[6], h[7]);
+        uint8_t *d = dst + j * RPS * 128;
+        *reinterpret_cast<uint4 *>(d + at0) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4 *>(d + (at0 ^ 16)) = make_uint4(h[4], h[5], h[6], h[7]);
       }
       fence_proxy_async_shared();
       tree_arrive(sh.v_full[pair]);
@@ -779,14 +782,14 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       // the scores of tile it, then the values of tile it - 1
 #pragma unroll 1
       for (uint32_t it = 0;; ++it) {
-        // the values first where the next scores wait for another piece's queries
+        // The scores' buffer held the weights of tile it - 2, which the MMAs issued before read.  The
+        // values come first where the scores wait for another piece's queries.
         bool ok = true;
 #pragma unroll 1
         for (int k = 0; k < 2 && ok; ++k) {
           if (fresh == (k == 1)) {
             if (!live) continue;
-            if ((it > 0 && !tree_wait<false>(sh.s_free, it - 1, &sh.abort)) ||
-                (fresh && !tree_wait<false>(sh.q_full, ip - 1, &sh.abort)) ||
+            if ((fresh && !tree_wait<false>(sh.q_full, ip - 1, &sh.abort)) ||
                 !tree_wait<false>(sh.k_full[st], ph, &sh.abort)) {
               ok = false;
               continue;
@@ -795,8 +798,9 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
             const uint64_t kd = tree_sdesc_k<D>(sbase + L::kK + st * L::kTile);
 #pragma unroll
             for (int kk = 0; kk < D / 32; ++kk)
-              mma_f8f6f4(tmem + L::kColS, qd + 2 * kk, kd + 2 * kk, L::kIdescQK, kk > 0 ? 1u : 0u);
-            mma_commit(smem_u32(&sh.s_full));
+              mma_f8f6f4(tmem + L::kColS + 64 * (it & 1u), qd + 2 * kk, kd + 2 * kk, L::kIdescQK,
+                         kk > 0 ? 1u : 0u);
+            mma_commit(smem_u32(&sh.s_full[it & 1u]));
             mma_commit(smem_u32(&sh.k_free[st]));
             if (left == 0) mma_commit(smem_u32(&sh.q_free));     // the piece's last scores
             if (++st == kTreeStages) {
@@ -814,7 +818,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
             const uint64_t vd = tree_sdesc_v(sbase + L::kV16 + i * L::kV16Bytes);
 #pragma unroll
             for (int kk = 0; kk < kTreeN / 16; ++kk)
-              mma_f16_ts(tmem + L::kColO, tmem + L::kColP + 32 * i + 8 * kk, vd + 128 * kk,
+              mma_f16_ts(tmem + L::kColO, tmem + L::kColS + 64 * i + 8 * kk, vd + 128 * kk,
                          L::kIdescPV, before && kk == 0 ? 0u : 1u);
             mma_commit(smem_u32(&sh.pv_done[i]));
           }
@@ -845,11 +849,6 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       const bool live = r < pc.rows;
       const int node = a.by_group(pc.row0 + r);
       const int64_t *mrow = a.mask && live ? a.mask + (pc.first + node) * a.ldm : nullptr;
-      if (rep > 1) {                                             // weights of the other columns: 0
-        const uint32_t z[16] = {};
-#pragma unroll 1
-        for (int i = 0; i < 64; i += 16) tree_st<16>(tw + L::kColP + i, z);
-      }
       TreeRow st{-INFINITY, 0.0f};
       for (int t = pc.t; t < pc.t_end && ok; ++t, ++it) {
         // a row that does not exist counts as seeing all (its scores are 0, its results unused)

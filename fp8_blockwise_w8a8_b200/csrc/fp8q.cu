@@ -1206,18 +1206,22 @@ int fp8q_attention_tree(const void *q_e4m3, int64_t ldq, const void *k_cache, co
   a.by_block = tree_div(block_size);
   a.by_group = tree_div(Hq / Hkv);
   // a cache without slots: every position is out of range and loads row 0, here of q
-  CUtensorMap tm_k;
+  const void *k_rows = num_slots > 0 ? k_cache : q_e4m3, *v_rows = num_slots > 0 ? v_cache : q_e4m3;
+  const int64_t map_rows = num_slots > 0 ? num_slots : 1;
+  CUtensorMap tm_k, tm_v;
   if ((rc = get_encoder()) != FP8Q_OK ||
-      (rc = make_u8_row_map(&tm_k, num_slots > 0 ? k_cache : q_e4m3, num_slots > 0 ? num_slots : 1,
-                            Hkv * D, box, static_cast<uint32_t>(D),
+      (rc = make_u8_row_map(&tm_k, k_rows, map_rows, Hkv * D, box, static_cast<uint32_t>(D),
                             D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B)) !=
-          FP8Q_OK)
+          FP8Q_OK ||
+      (rc = make_u8_row_map(&tm_v, v_rows, map_rows, Hkv * D, box, static_cast<uint32_t>(D),
+                            CU_TENSOR_MAP_SWIZZLE_NONE)) != FP8Q_OK)
     return rc;
   if (D == 128)
-    fp8q::k_tree_attn<128><<<grid, fp8q::kTreeThreads, fp8q::TreeLayout<128>::kSmem, stream>>>(tm_k,
-                                                                                               a);
+    fp8q::k_tree_attn<128><<<grid, fp8q::kTreeThreads, fp8q::TreeLayout<128>::kSmem, stream>>>(
+        tm_k, tm_v, a);
   else
-    fp8q::k_tree_attn<64><<<grid, fp8q::kTreeThreads, fp8q::TreeLayout<64>::kSmem, stream>>>(tm_k, a);
+    fp8q::k_tree_attn<64><<<grid, fp8q::kTreeThreads, fp8q::TreeLayout<64>::kSmem, stream>>>(
+        tm_k, tm_v, a);
   if ((rc = launch_status()) != FP8Q_OK) return rc;
   // the merge as a programmatic dependent launch: scheduled while the first kernel drains
   cudaLaunchConfig_t cfg = {};

@@ -76,9 +76,9 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeAttnArgs &a, int b, bool r
 // ---------------------------------------------------------------------------------------------
 constexpr int kTreeM = 128;          // query rows (node, head of the group) per row tile: TMEM lanes
 constexpr int kTreeN = 64;           // cached positions per tile
-constexpr int kTreeThreads = 352;    // 4 softmax warps, 4 for V, one each for the MMAs, K and Q
+constexpr int kTreeThreads = 384;    // 4 softmax warps, 4 convert V, one each: MMAs, K, Q, copies of V
 constexpr int kTreeMaxCtas = 296;    // 2 per SM of 148
-constexpr int kTreeStages = 4;       // K tiles in shared memory
+constexpr int kTreeStages = 3;       // K and V tiles (codes) in shared memory
 constexpr int kTreeItemCost = 2;     // cost of starting a row tile, in position tiles
 constexpr int kTreeMinCost = 4;      // least cost per CTA
 constexpr int kTreeMetaInts = 8;
@@ -92,8 +92,8 @@ struct TreeLayout {
   static constexpr int kTile = kTreeN * D;
   static constexpr int kV16 = kK + kTreeStages * kTile;          // [2][D / 64][64][128 B], swizzled
   static constexpr int kV16Bytes = kTreeN * D * 2;
-  static constexpr int kV8 = kV16 + 2 * kV16Bytes;               // [pair of V warps][64][D]
-  static constexpr int kSmem = kV8 + 2 * kTile + 1024;
+  static constexpr int kV8 = kV16 + 2 * kV16Bytes;               // [stage][64][D]
+  static constexpr int kSmem = kV8 + kTreeStages * kTile + 1024;
   // TMEM columns: two score buffers, whose first halves then hold the weights (two fp16 a column),
   // and the values
   static constexpr int kColS = 0, kColO = 128, kCols = 256;
@@ -230,32 +230,28 @@ __device__ __forceinline__ uint64_t tree_sdesc_k(uint32_t saddr) {
          (static_cast<uint64_t>(B == 128 ? 2 : 4) << 61);
 }
 
-// Bounded waits by a warp and by one thread, short in code: about 2^20 polls of a microsecond at most,
-// then the timeout is recorded and the CTA's roles give up.
-__device__ __forceinline__ bool tree_poll(uint32_t bar, uint32_t parity) {
+// Bounded waits by a warp and by one thread, short in code: 2^20 polls of a microsecond at most, then
+// the CTA's abort flag is raised (it becomes the recorded timeout at the end) and the role gives up;
+// those that wait for it do the same in their turn.
+template <bool WARP>
+__device__ __forceinline__ bool tree_wait(const uint64_t &barrier, uint32_t parity, int *abort_flag) {
   uint32_t ok;
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, 0;\n"
+      "TREE_POLL_%=:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+      "@p bra TREE_DONE_%=;\n\t"
+      "add.u32 n, n, 1;\n\t"
+      "setp.lt.u32 q, n, 1048576;\n\t"
+      "@q bra TREE_POLL_%=;\n"
+      "TREE_DONE_%=:\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(1000u)
+      : "r"(smem_u32(&barrier)), "r"(parity & 1u)
       : "memory");
-  return ok != 0;
-}
-constexpr uint32_t kTreePolls = 1u << 20;
-template <bool WARP>
-__device__ __forceinline__ bool tree_wait(const uint64_t &barrier, uint32_t parity,
-                                          volatile int *abort_flag) {
-  const uint32_t bar = smem_u32(&barrier);
-#pragma unroll 1
-  for (uint32_t n = 0;; ++n) {
-    const bool ok = tree_poll(bar, parity & 1u);
-    if (WARP ? __all_sync(0xffffffffu, ok) : ok) return true;
-    const bool stop = *abort_flag != 0 || n >= kTreePolls;
-    if (WARP ? __any_sync(0xffffffffu, stop) : stop) break;
-  }
-  if (atomicExch(const_cast<int *>(abort_flag), 1) == 0) record_error(6 /* FP8Q_ERR_TIMEOUT */);
+  if (WARP ? __all_sync(0xffffffffu, ok) : ok) return true;
+  *const_cast<volatile int *>(abort_flag) = 1;
   return false;
 }
 // The calling warp's share of an arrival.
@@ -280,17 +276,19 @@ __device__ __forceinline__ void tree_st(uint32_t taddr, const uint32_t (&r)[N]) 
 
 // What the CTA's roles share.
 constexpr int kTreePieces = 4;   // descriptors in the ring
-struct TreeTile {                // for the V warps
-  int32_t slot[kTreeN];          // cache rows of the tile's positions, -1 where there is none
+struct TreeTile {                // for the copies of V
+  alignas(16) int32_t row[kTreeN];   // first cache row of each copy, or each position's row
   int32_t g, piece;              // kv head (-1: no more tiles), 1 + index of the piece
 };
 struct TreeShared {
   uint64_t k_full[kTreeStages], k_free[kTreeStages], t_full[kTreeStages], t_free[kTreeStages];
+  uint64_t v8_full[kTreeStages], v8_free[kTreeStages];
   uint64_t piece_full[kTreePieces], piece_free[kTreePieces];
   uint64_t q_full, q_free, v_full[2], s_full[2], p_full[2], pv_done[2], drain;
   uint64_t valid[8];             // per tile (mod 8): the positions that exist, one bit each
   TreePiece piece[kTreePieces];
   TreeTile tile[kTreeStages];
+  int32_t v8_piece[kTreeStages]; // 1 + index of the stage's piece, -1: no more tiles
   int start_b;
   int64_t start_off;
   int64_t warp_sum[kTreeThreads / 32];
@@ -448,7 +446,8 @@ __device__ __forceinline__ bool tree_any4(bool v) {
 
 template <int D>
 __global__ void __launch_bounds__(kTreeThreads, 2)
-    k_tree_attn(const __grid_constant__ CUtensorMap tm_k, const TreeAttnArgs a) {
+    k_tree_attn(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                const TreeAttnArgs a) {
   using L = TreeLayout<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ TreeShared sh;
@@ -462,7 +461,9 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       mbar_init(smem_u32(&sh.k_full[i]), 1);
       mbar_init(smem_u32(&sh.k_free[i]), 1);
       mbar_init(smem_u32(&sh.t_full[i]), 1);
-      mbar_init(smem_u32(&sh.t_free[i]), 2);
+      mbar_init(smem_u32(&sh.t_free[i]), 1);
+      mbar_init(smem_u32(&sh.v8_full[i]), 1);
+      mbar_init(smem_u32(&sh.v8_free[i]), 2);
     }
     for (int i = 0; i < kTreePieces; ++i) {
       mbar_init(smem_u32(&sh.piece_full[i]), 1);
@@ -553,7 +554,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     TreeCursor pre;
     pre.init(a, G, B, sh.start_b, sh.start_off, hi - lo);
     const bool gather = a.box < 4;
-    const int chunks = kTreeN / a.box, log_box = __ffs(a.box) - 1;
+    const int chunks = kTreeN / a.box;
     const int first = gather ? lane : min(lane, chunks - 1) * a.box;
     int blk[2], off[2];
     auto look_up = [&]() {                                       // block ids of the cursor's tile
@@ -629,18 +630,11 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           rows[r] = lane & 8 ? v1 : v0;
         }
         if (lane < 16) tma_gather4(dst + 4 * D * lane, &tm_k, pre.g * D, rows, bar);
-      } else {
-        if (lane < chunks) tma_load_2d(dst + lane * a.box * D, &tm_k, pre.g * D, slot[0], bar);
-        const int32_t row = slot[0];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int p = 32 * j + lane;
-          slot[j] = __shfl_sync(0xffffffffu, row, p >> log_box) + (p & (a.box - 1));
-        }
+      } else if (lane < chunks) {
+        tma_load_2d(dst + lane * a.box * D, &tm_k, pre.g * D, slot[0], bar);
       }
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        sh.tile[st].slot[32 * j + lane] = (there >> (32 * j + lane)) & 1u ? slot[j] : -1;
+      sh.tile[st].row[lane] = slot[0];
+      sh.tile[st].row[32 + lane] = slot[1];
       tree_arrive(sh.t_full[st]);
       if (++st == kTreeStages) {
         st = 0;
@@ -650,19 +644,52 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       if (fresh) pre.next(a, G, 0);
       look_up();
     }
-    // the end, for both pairs of V warps
-    for (int i = 0; i < 2; ++i) {
-      if (!tree_wait<true>(sh.t_free[st], ph, &sh.abort)) break;
+    if (tree_wait<true>(sh.t_free[st], ph, &sh.abort)) {         // the end
       if (lane == 0) sh.tile[st].g = -1;
       tree_arrive(sh.t_full[st]);
+    }
+    // after a wait that gave up: no copy in flight at exit
+    for (uint32_t i = it < kTreeStages ? 0 : it - kTreeStages; i < it; ++i)
+      wait_drain(smem_u32(&sh.k_full[i % kTreeStages]), (i / kTreeStages) & 1u);
+  } else if (warp == 11) {
+    // ---------------------------------------------------------------- copies of V
+    const bool gather = a.box < 4;
+    const int n = gather ? 4 : a.box;                            // rows per copy
+    uint32_t it = 0, st = 0, ph = 0;
+    for (int left = 0;; ++it) {
+      if (left == 0) {
+        if (!tree_wait<true>(sh.t_full[st], ph, &sh.abort)) break;
+        if (sh.tile[st].g < 0) left = 2;                         // the end, for both pairs of V warps
+      } else if (--left == 0) {
+        break;
+      }
+      int32_t rows[4];
+      const int32_t g = sh.tile[st].g, piece = sh.tile[st].piece;
+      *reinterpret_cast<int4 *>(rows) = *reinterpret_cast<const int4 *>(&sh.tile[st].row[4 * (lane & 15)]);
+      const int32_t row = sh.tile[st].row[lane];
+      if (!tree_wait<true>(sh.v8_free[st], ph ^ 1u, &sh.abort)) break;
+      const uint32_t bar = smem_u32(&sh.v8_full[st]);
+      if (lane == 0) sh.v8_piece[st] = left > 0 ? -1 : piece;
+      if (left > 0) {
+        tree_arrive(sh.v8_full[st]);
+      } else {
+        tree_arrive(sh.t_free[st]);
+        if (lane == 0) mbar_arrive_expect_tx(bar, L::kTile);
+        __syncwarp();
+        const uint32_t dst = sbase + L::kV8 + st * L::kTile + lane * n * D;
+        if (gather) {
+          if (lane < 16) tma_gather4(dst, &tm_v, g * D, rows, bar);
+        } else if (lane < kTreeN / n) {
+          tma_load_2d(dst, &tm_v, g * D, row, bar);
+        }
+      }
       if (++st == kTreeStages) {
         st = 0;
         ph ^= 1u;
       }
     }
-    // after a wait that gave up: no copy in flight at exit
     for (uint32_t i = it < kTreeStages ? 0 : it - kTreeStages; i < it; ++i)
-      wait_drain(smem_u32(&sh.k_full[i % kTreeStages]), (i / kTreeStages) & 1u);
+      wait_drain(smem_u32(&sh.v8_full[i % kTreeStages]), (i / kTreeStages) & 1u);
   } else if (warp == 10) {
     // ---------------------------------------------------------------- queries
     constexpr int LPR = D / 16;                                  // 16-byte chunks per row
@@ -709,31 +736,18 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     const int pair = (warp - 4) >> 1, gt = tid - 128 - 64 * pair;
     const int ch = D == 128 ? (gt & 3) | (gt >> 1 & 4) : gt & 3;
     const int r0 = D == 128 ? (gt >> 2 & 1) | (gt >> 4 << 1) : gt >> 2;
-    const int64_t row = static_cast<int64_t>(a.Hkv) * D;
-    const uint32_t stage = sbase + L::kV8 + pair * L::kTile + gt * 16;
+    uint32_t st = pair, ph = 0;
     for (uint32_t it = pair;; it += 2) {
-      const uint32_t st = it % kTreeStages;
-      if (!tree_wait<true>(sh.t_full[st], it / kTreeStages, &sh.abort)) break;
-      const TreeTile &tile = sh.tile[st];
-      const int32_t g = tile.g, piece = tile.piece;
-      if (g < 0) break;
-      // each thread copies and converts 16 codes of every step's row
-      const uint8_t *col = a.v_cache + g * D + ch * 16;
-#pragma unroll 2
-      for (int j = 0; j < NR; ++j) {
-        const int32_t slot = tile.slot[j * RPS + r0];
-        cp_async16(stage + j * 1024, col + static_cast<int64_t>(max(slot, 0)) * row,
-                   slot >= 0 ? 16u : 0u);
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      tree_arrive(sh.t_free[st]);
+      if (!tree_wait<true>(sh.v8_full[st], ph, &sh.abort)) break;
+      const int32_t piece = sh.v8_piece[st];
+      if (piece < 0) break;
       if (it >= 2 && !tree_wait<true>(sh.pv_done[pair], (it - 2) >> 1, &sh.abort)) break;
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      const uint8_t *src = smem + L::kV8 + st * L::kTile + r0 * D + ch * 16;
       uint8_t *dst = smem + L::kV16 + pair * L::kV16Bytes + (ch >> 2) * 8192 + r0 * 128;
       const int at0 = ((ch & 3) * 2 ^ (r0 & 7)) << 4;            // RPS is a multiple of 8
 #pragma unroll 1
       for (int j = 0; j < NR; ++j) {
-        uint4 v8 = *reinterpret_cast<const uint4 *>(smem + (stage - sbase) + j * 1024);
+        uint4 v8 = *reinterpret_cast<const uint4 *>(src + j * RPS * D);
         uint32_t h[8];
         while (true) {
           const uint32_t w[4] = {v8.x, v8.y, v8.z, v8.w};
@@ -749,16 +763,21 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             *x[k] &= ~(((((*x[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xFFu);
-          atomicMax(&sh.nan_piece, piece);
+          if ((sh.valid[it & 7u] >> (j * RPS + r0)) & 1u) atomicMax(&sh.nan_piece, piece);
         }
         uint8_t *d = dst + j * RPS * 128;
         *reinterpret_cast<uint4 *>(d + at0) = make_uint4(h[0], h[1], h[2], h[3]);
         *reinterpret_cast<uint4 *>(d + (at0 ^ 16)) = make_uint4(h[4], h[5], h[6], h[7]);
       }
       fence_proxy_async_shared();
+      tree_arrive(sh.v8_free[st]);
       tree_arrive(sh.v_full[pair]);
+      st += 2;
+      if (st >= kTreeStages) {
+        st -= kTreeStages;
+        ph ^= 1u;
+      }
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");         // none in flight at exit
   } else if (warp == 8) {
     // ---------------------------------------------------------------- MMA issue
     if (lane == 0) {
@@ -968,6 +987,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   }
 
   __syncthreads();
+  if (tid == 0 && sh.abort) record_error(6 /* FP8Q_ERR_TIMEOUT */);
   if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(tmem, L::kCols);

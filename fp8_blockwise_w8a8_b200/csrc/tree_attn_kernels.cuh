@@ -343,11 +343,13 @@ struct TreeRow {
   float ref, l;                  // reference of the weights (log2 units), their sum
 };
 
-// Sixteen scores of this thread's row from TMEM; what is not seen (bit 0 on) becomes -inf.
-__device__ __forceinline__ void tree_scores(uint32_t taddr, uint64_t seen, uint32_t (&sr)[16]) {
+// Sixteen scores of this thread's row from TMEM; where not all are seen, those that are not (bit 0 on)
+// become -inf.
+__device__ __forceinline__ void tree_scores(uint32_t taddr, bool all, uint64_t seen,
+                                            uint32_t (&sr)[16]) {
   tree_ld<16>(taddr, sr);
-  const uint32_t bits = static_cast<uint32_t>(seen) & 0xFFFFu;
-  if (!__all_sync(0xffffffffu, bits == 0xFFFFu)) {
+  if (!all) {
+    const uint32_t bits = static_cast<uint32_t>(seen);
 #pragma unroll
     for (int j = 0; j < 16; ++j)
       if (!((bits >> j) & 1)) sr[j] = 0xFF800000u;
@@ -357,23 +359,30 @@ __device__ __forceinline__ void tree_scores(uint32_t taddr, uint64_t seen, uint3
 // One position tile: the scores of 16 * chunks columns of this thread's row become weights, in the
 // first half of the score buffer's columns: 8 columns per chunk, behind those already read.  The first
 // chunk's scores stay in registers between the maximum and the weights, the others are read again.
-// Loops over short bodies: the roles' code together has to stay in the instruction caches.
+// Loops over short bodies: the roles' code together has to stay in the instruction caches.  j0: the
+// tile's first position, counted from node 0.
 template <int D>
 __device__ __forceinline__ bool tree_tile(TreeShared &sh, uint32_t tmem, uint32_t col0, int chunks,
-                                          uint32_t it, bool first, uint64_t seen, float c2,
-                                          TreeRow &st) {
+                                          uint32_t it, bool first, const int64_t *mrow, int words,
+                                          int node, int j0, float c2, TreeRow &st) {
   using L = TreeLayout<D>;
   if (!tree_wait<true>(sh.s_full[it & 1u], it >> 1, &sh.abort)) return false;
   tc_fence_after();
   const uint32_t buf = tmem + L::kColS + 64 * (it & 1u);
   uint32_t sr[16];
-  seen = (seen & sh.valid[it & 7u]) >> col0;
+  uint64_t seen = sh.valid[it & 7u];
+  const bool all = j0 <= -kTreeN && seen == ~0ull;               // within the context, all there
+  if (!all) {
+    // a row that does not exist counts as seeing all (its results are unused)
+    if (node >= 0) seen &= tree_bits(mrow, words, node, j0);
+    seen >>= col0;
+  }
   float mx[2] = {-INFINITY, -INFINITY};
   int c = chunks;
 #pragma unroll 1
   do {
     --c;
-    tree_scores(buf + col0 + 16 * c, seen >> (16 * c), sr);
+    tree_scores(buf + col0 + 16 * c, all, seen >> (16 * c), sr);
 #pragma unroll
     for (int j = 0; j < 16; ++j) mx[j & 1] = fmaxf(mx[j & 1], __uint_as_float(sr[j]));
   } while (c > 0);
@@ -413,13 +422,7 @@ __device__ __forceinline__ bool tree_tile(TreeShared &sh, uint32_t tmem, uint32_
     }
     tree_st<8>(buf + col0 / 2 + 8 * c, pk);
     if (++c >= chunks) break;
-    tree_scores(buf + col0 + 16 * c, seen >> (16 * c), sr);
-  }
-  // a repeat of a row has no weight at the other repeats' positions
-#pragma unroll 1
-  for (int i = 8 * chunks; i < 32; i += 8) {
-    const uint32_t z[8] = {};
-    tree_st<8>(buf + ((col0 / 2 + i) & 31u), z);
+    tree_scores(buf + col0 + 16 * c, all, seen >> (16 * c), sr);
   }
   st.l += sum.x + sum.y;
   tmem_st_wait();
@@ -605,12 +608,15 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         slot[1] = slot_of(1, &ok);
         there |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, ok)) << 32;
       } else {
-        const uint64_t bits = ok ? (a.box == 64 ? ~0ull : ((1ull << a.box) - 1) << first) : 0ull;
-        there = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(bits));
-        there |= static_cast<uint64_t>(
-                     __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(bits >> 32))) << 32;
         const int left = pre.s.ctx + pre.s.n - pre.t * kTreeN;   // positions that exist
-        if (left < 64) there &= (1ull << left) - 1;
+        there = ~0ull;
+        if (left < 64 || !__all_sync(0xffffffffu, ok)) {
+          const uint64_t bits = ok ? (a.box == 64 ? ~0ull : ((1ull << a.box) - 1) << first) : 0ull;
+          there = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(bits));
+          there |= static_cast<uint64_t>(
+                       __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(bits >> 32))) << 32;
+          if (left < 64) there &= (1ull << left) - 1;
+        }
       }
       const uint32_t bar = smem_u32(&sh.k_full[st]);
       if (lane == 0) {
@@ -745,7 +751,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       const uint8_t *src = smem + L::kV8 + st * L::kTile + r0 * D + ch * 16;
       uint8_t *dst = smem + L::kV16 + pair * L::kV16Bytes + (ch >> 2) * 8192 + r0 * 128;
       const int at0 = ((ch & 3) * 2 ^ (r0 & 7)) << 4;            // RPS is a multiple of 8
-#pragma unroll 1
+#pragma unroll 2
       for (int j = 0; j < NR; ++j) {
         uint4 v8 = *reinterpret_cast<const uint4 *>(src + j * RPS * D);
         uint32_t h[8];
@@ -783,7 +789,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     if (lane == 0) {
       const uint64_t qd = tree_sdesc_k<128>(sbase + L::kQ);
       uint32_t ip = 0;
-      int left = 0;
+      int left = 0, same = 0, same_before = 0;                   // log2 of the K steps a lane group takes
       bool fresh = false, before = false;
       auto next = [&]() {                                        // the next tile, if there is one
         fresh = left == 0;
@@ -791,6 +797,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           const uint32_t i = ip % kTreePieces;
           if (!tree_wait<false>(sh.piece_full[i], ip / kTreePieces, &sh.abort)) return false;
           left = sh.piece[i].t_end - (sh.piece[i].t_end > 0 ? sh.piece[i].t : 0);
+          same = sh.piece[i].rows <= 32 ? 0 : (sh.piece[i].rows <= 64 ? 1 : 2);
           mbar_arrive(smem_u32(&sh.piece_free[i]));
           ++ip;
         }
@@ -835,16 +842,25 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
             }
             tc_fence_after();
             const uint64_t vd = tree_sdesc_v(sbase + L::kV16 + i * L::kV16Bytes);
+            // A lane group (32 rows) that holds a repeat has weights at its own positions only: the
+            // other K steps leave its values alone.
 #pragma unroll
-            for (int kk = 0; kk < kTreeN / 16; ++kk)
+            for (int kk = 0; kk < kTreeN / 16; ++kk) {
+              uint32_t off[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                off[q] = (q >> same_before) == (kk >> same_before) ? 0u : 0xFFFFFFFFu;
+              const int steps = 1 << same_before;                // of the group's, the first writes
               mma_f16_ts(tmem + L::kColO, tmem + L::kColS + 64 * i + 8 * kk, vd + 128 * kk,
-                         L::kIdescPV, before && kk == 0 ? 0u : 1u);
+                         L::kIdescPV, off, before && (kk & (steps - 1)) == 0 ? 0u : 1u);
+            }
             mma_commit(smem_u32(&sh.pv_done[i]));
           }
         }
         if (!ok) break;
         if (!live) break;
         before = fresh;
+        same_before = same;
         live = next();
       }
       mma_commit(smem_u32(&sh.drain));                           // all MMAs done before dealloc
@@ -870,10 +886,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       const int64_t *mrow = a.mask && live ? a.mask + (pc.first + node) * a.ldm : nullptr;
       TreeRow st{-INFINITY, 0.0f};
       for (int t = pc.t; t < pc.t_end && ok; ++t, ++it) {
-        // a row that does not exist counts as seeing all (its scores are 0, its results unused)
-        const uint64_t seen = live ? tree_bits(mrow, words, node, t * kTreeN - pc.ctx) : ~0ull;
-        const bool first = t == pc.t;
-        ok = tree_tile<D>(sh, tw, col0, 4 >> shift, it, first, seen, c2, st);
+        ok = tree_tile<D>(sh, tw, col0, 4 >> shift, it, t == pc.t, mrow, words, live ? node : -1,
+                          t * kTreeN - pc.ctx, c2, st);
       }
       ok = ok && tree_wait<true>(sh.pv_done[(it - 1) & 1u], (it - 1) >> 1, &sh.abort);
       sh.ml[warp][lane][0] = st.ref;

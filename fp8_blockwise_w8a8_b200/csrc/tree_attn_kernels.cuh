@@ -376,6 +376,7 @@ __device__ __forceinline__ bool tree_tile(TreeShared &sh, uint32_t tmem, uint32_
     // a row that does not exist counts as seeing all (its results are unused)
     if (node >= 0) seen &= tree_bits(mrow, words, node, j0);
     seen >>= col0;
+    __syncwarp();                                                // whole warps at the TMEM loads
   }
   float mx[2] = {-INFINITY, -INFINITY};
   int c = chunks;
@@ -433,9 +434,13 @@ __device__ __forceinline__ bool tree_tile(TreeShared &sh, uint32_t tmem, uint32_
 
 // Barrier of the four softmax warps, and one that tells whether any of them gave up.  Their waits are
 // bounded and every one of them passes the same barriers.
-__device__ __forceinline__ void tree_sync4() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void tree_sync4() {
+  __syncwarp();
+  asm volatile("bar.sync 1, 128;" ::: "memory");
+}
 __device__ __forceinline__ bool tree_any4(bool v) {
   uint32_t r;
+  __syncwarp();
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
@@ -669,9 +674,9 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       } else if (--left == 0) {
         break;
       }
-      int32_t rows[4];
       const int32_t g = sh.tile[st].g, piece = sh.tile[st].piece;
-      *reinterpret_cast<int4 *>(rows) = *reinterpret_cast<const int4 *>(&sh.tile[st].row[4 * (lane & 15)]);
+      const int4 r4 = *reinterpret_cast<const int4 *>(&sh.tile[st].row[4 * (lane & 15)]);
+      const int32_t rows[4] = {r4.x, r4.y, r4.z, r4.w};
       const int32_t row = sh.tile[st].row[lane];
       if (!tree_wait<true>(sh.v8_free[st], ph ^ 1u, &sh.abort)) break;
       const uint32_t bar = smem_u32(&sh.v8_full[st]);
@@ -945,6 +950,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
 #pragma unroll 1
       for (int c = 0; c < D; c += 16) {
         uint32_t o[16];
+        __syncwarp();
         tree_ld<16>(tw + L::kColO + c, o);
         float4 v[4];
 #pragma unroll

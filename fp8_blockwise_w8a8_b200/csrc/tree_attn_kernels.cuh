@@ -756,29 +756,52 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       const uint8_t *src = smem + L::kV8 + st * L::kTile + r0 * D + ch * 16;
       uint8_t *dst = smem + L::kV16 + pair * L::kV16Bytes + (ch >> 2) * 8192 + r0 * 128;
       const int at0 = ((ch & 3) * 2 ^ (r0 & 7)) << 4;            // RPS is a multiple of 8
-#pragma unroll 2
-      for (int j = 0; j < NR; ++j) {
-        uint4 v8 = *reinterpret_cast<const uint4 *>(src + j * RPS * D);
-        uint32_t h[8];
+#pragma unroll 1
+      for (int j = 0; j < NR; j += 2) {
+        uint4 v8[2];
+        uint32_t h[16];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          v8[k] = *reinterpret_cast<const uint4 *>(src + (j + k) * RPS * D);
         while (true) {
-          const uint32_t w[4] = {v8.x, v8.y, v8.z, v8.w};
-          __half2 acc = __half2half2(__ushort_as_half(0));
+          const uint32_t w[8] = {v8[0].x, v8[0].y, v8[0].z, v8[0].w,
+                                 v8[1].x, v8[1].y, v8[1].z, v8[1].w};
+          __half2 m[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            h[k] = e4m3x2_to_f16x2(k & 1 ? w[k / 2] >> 16 : w[k / 2] & 0xFFFFu);
-            acc = __hmax2_nan(acc, *reinterpret_cast<const __half2 *>(&h[k]));
+            h[2 * k] = e4m3x2_to_f16x2(w[k] & 0xFFFFu);
+            h[2 * k + 1] = e4m3x2_to_f16x2(w[k] >> 16);
+            m[k] = __hmax2_nan(*reinterpret_cast<const __half2 *>(&h[2 * k]),
+                               *reinterpret_cast<const __half2 *>(&h[2 * k + 1]));
           }
-          if (!__hisnan(__low2half(acc)) && !__hisnan(__high2half(acc))) break;
-          // A NaN code becomes 0; it is put back into the results of the rows that see it.
-          uint32_t *x[4] = {&v8.x, &v8.y, &v8.z, &v8.w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            *x[k] &= ~(((((*x[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xFFu);
-          if ((sh.valid[it & 7u] >> (j * RPS + r0)) & 1u) atomicMax(&sh.nan_piece, piece);
+          for (int d = 4; d > 0; d /= 2)
+#pragma unroll
+            for (int k = 0; k < d; ++k) m[k] = __hmax2_nan(m[k], m[k + d]);
+          if (!__hisnan(__low2half(m[0])) && !__hisnan(__high2half(m[0]))) break;
+          // A NaN code becomes 0; it is put back into the results of the rows that see it.
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t *x[4] = {&v8[k].x, &v8[k].y, &v8[k].z, &v8[k].w};
+            uint32_t any = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t n7 = ((*x[q] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+              any |= n7;
+              *x[q] &= ~((n7 >> 7) * 0xFFu);
+            }
+            if (any && ((sh.valid[it & 7u] >> ((j + k) * RPS + r0)) & 1u))
+              atomicMax(&sh.nan_piece, piece);
+          }
         }
-        uint8_t *d = dst + j * RPS * 128;
-        *reinterpret_cast<uint4 *>(d + at0) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4 *>(d + (at0 ^ 16)) = make_uint4(h[4], h[5], h[6], h[7]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint8_t *d = dst + (j + k) * RPS * 128;
+          *reinterpret_cast<uint4 *>(d + at0) =
+              make_uint4(h[8 * k], h[8 * k + 1], h[8 * k + 2], h[8 * k + 3]);
+          *reinterpret_cast<uint4 *>(d + (at0 ^ 16)) =
+              make_uint4(h[8 * k + 4], h[8 * k + 5], h[8 * k + 6], h[8 * k + 7]);
+        }
       }
       fence_proxy_async_shared();
       tree_arrive(sh.v8_free[st]);
@@ -791,7 +814,9 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     }
   } else if (warp == 8) {
     // ---------------------------------------------------------------- MMA issue
-    if (lane == 0) {
+    // The whole warp runs the loop, so that addresses stay in uniform registers; one lane issues.
+    {
+      const bool leader = elect_one();
       const uint64_t qd = tree_sdesc_k<128>(sbase + L::kQ);
       uint32_t ip = 0;
       int left = 0, same = 0, same_before = 0;                   // log2 of the K steps a lane group takes
@@ -800,10 +825,10 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         fresh = left == 0;
         if (fresh) {
           const uint32_t i = ip % kTreePieces;
-          if (!tree_wait<false>(sh.piece_full[i], ip / kTreePieces, &sh.abort)) return false;
+          if (!tree_wait<true>(sh.piece_full[i], ip / kTreePieces, &sh.abort)) return false;
           left = sh.piece[i].t_end - (sh.piece[i].t_end > 0 ? sh.piece[i].t : 0);
           same = sh.piece[i].rows <= 32 ? 0 : (sh.piece[i].rows <= 64 ? 1 : 2);
-          mbar_arrive(smem_u32(&sh.piece_free[i]));
+          tree_arrive(sh.piece_free[i]);
           ++ip;
         }
         return left-- > 0;
@@ -820,46 +845,54 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         for (int k = 0; k < 2 && ok; ++k) {
           if (fresh == (k == 1)) {
             if (!live) continue;
-            if ((fresh && !tree_wait<false>(sh.q_full, ip - 1, &sh.abort)) ||
-                !tree_wait<false>(sh.k_full[st], ph, &sh.abort)) {
+            if ((fresh && !tree_wait<true>(sh.q_full, ip - 1, &sh.abort)) ||
+                !tree_wait<true>(sh.k_full[st], ph, &sh.abort)) {
               ok = false;
               continue;
             }
             tc_fence_after();
             const uint64_t kd = tree_sdesc_k<D>(sbase + L::kK + st * L::kTile);
+            if (leader) {
 #pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk)
-              mma_f8f6f4(tmem + L::kColS + 64 * (it & 1u), qd + 2 * kk, kd + 2 * kk, L::kIdescQK,
-                         kk > 0 ? 1u : 0u);
-            mma_commit(smem_u32(&sh.s_full[it & 1u]));
-            mma_commit(smem_u32(&sh.k_free[st]));
-            if (left == 0) mma_commit(smem_u32(&sh.q_free));     // the piece's last scores
+              for (int kk = 0; kk < D / 32; ++kk)
+                mma_f8f6f4(tmem + L::kColS + 64 * (it & 1u), qd + 2 * kk, kd + 2 * kk, L::kIdescQK,
+                           kk > 0 ? 1u : 0u);
+              mma_commit(smem_u32(&sh.s_full[it & 1u]));
+              mma_commit(smem_u32(&sh.k_free[st]));
+              if (left == 0) mma_commit(smem_u32(&sh.q_free));   // the piece's last scores
+            }
+            __syncwarp();
             if (++st == kTreeStages) {
               st = 0;
               ph ^= 1u;
             }
           } else if (it > 0) {
             const uint32_t i = (it - 1) & 1u, pp = (it - 1) >> 1;
-            if (!tree_wait<false>(sh.p_full[i], pp, &sh.abort) ||
-                !tree_wait<false>(sh.v_full[i], pp, &sh.abort)) {
+            if (!tree_wait<true>(sh.p_full[i], pp, &sh.abort) ||
+                !tree_wait<true>(sh.v_full[i], pp, &sh.abort)) {
               ok = false;
               continue;
             }
             tc_fence_after();
             const uint64_t vd = tree_sdesc_v(sbase + L::kV16 + i * L::kV16Bytes);
             // A lane group (32 rows) that holds a repeat has weights at its own positions only: the
-            // other K steps leave its values alone.
+            // other K steps leave its values alone, and its first one writes them in a new piece.
+            const uint32_t pair = same_before > 0 ? 0u : ~0u, rest = same_before > 1 ? 0u : ~0u;
+            const uint32_t acc[4] = {before ? 0u : 1u, before && same_before == 0 ? 0u : 1u,
+                                     before && same_before < 2 ? 0u : 1u,
+                                     before && same_before == 0 ? 0u : 1u};
+            if (leader) {
 #pragma unroll
-            for (int kk = 0; kk < kTreeN / 16; ++kk) {
-              uint32_t off[4];
+              for (int kk = 0; kk < kTreeN / 16; ++kk) {
+                uint32_t off[4];
 #pragma unroll
-              for (int q = 0; q < 4; ++q)
-                off[q] = (q >> same_before) == (kk >> same_before) ? 0u : 0xFFFFFFFFu;
-              const int steps = 1 << same_before;                // of the group's, the first writes
-              mma_f16_ts(tmem + L::kColO, tmem + L::kColS + 64 * i + 8 * kk, vd + 128 * kk,
-                         L::kIdescPV, off, before && (kk & (steps - 1)) == 0 ? 0u : 1u);
+                for (int q = 0; q < 4; ++q) off[q] = q == kk ? 0u : (q / 2 == kk / 2 ? pair : rest);
+                mma_f16_ts(tmem + L::kColO, tmem + L::kColS + 64 * i + 8 * kk, vd + 128 * kk,
+                           L::kIdescPV, off, acc[kk]);
+              }
+              mma_commit(smem_u32(&sh.pv_done[i]));
             }
-            mma_commit(smem_u32(&sh.pv_done[i]));
+            __syncwarp();
           }
         }
         if (!ok) break;
@@ -868,8 +901,10 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         same_before = same;
         live = next();
       }
-      mma_commit(smem_u32(&sh.drain));                           // all MMAs done before dealloc
-      wait_drain(smem_u32(&sh.drain), 0);
+      if (leader) {
+        mma_commit(smem_u32(&sh.drain));                         // all MMAs done before dealloc
+        wait_drain(smem_u32(&sh.drain), 0);
+      }
     }
     __syncwarp();
   } else {

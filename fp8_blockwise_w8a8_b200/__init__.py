@@ -20,7 +20,6 @@ from ._lib import (FP8Q_ERR_ALIGN, FP8Q_ERR_ARCH, FP8Q_ERR_ARG, FP8Q_ERR_LAUNCH,
                    FP8Q_ERR_NOT_POW2, FP8Q_ERR_RANGE, FP8Q_ERR_SHAPE, FP8Q_ERR_TIMEOUT, FP8Q_OK, FP8Q_SCALE_E8M0, FP8Q_SCALE_F32,
                    Fp8qError)
 
-import contextlib
 import ctypes
 
 __all__ = ["quant_weight_block", "rmsnorm_quant_token", "add_rmsnorm_quant", "gemm_w8a8_block",
@@ -217,27 +216,29 @@ def attention_decode(q_codes: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
 
 
 def _expect(device, **tensors):
-    """Checks of the speculative-decoding calls: each value is (tensor, dtype, shape), a shape entry
-    of None standing for any size; contiguous CUDA tensors, all on `device`."""
+    """Checks of the speculative-decoding calls: each value is (tensor, dtype, shape); contiguous
+    tensors, all on `device`."""
     for name, (t, dtype, shape) in tensors.items():
-        if t.device != device or t.dtype != dtype or not t.is_contiguous():
+        if t.dtype != dtype or t.device != device or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}")
-        if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-            raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
-@contextlib.contextmanager
-def _launch(device, stream):
-    """Makes the tensors' device and the launch stream current, so that what is allocated inside
-    belongs to that stream; yields the stream's handle."""
+def _on_stream(device, stream, run):
+    """run(handle of the launch stream) with the tensors' device and that stream current, so that what
+    is allocated inside belongs to it.  Nothing is switched in the common case, the current stream of
+    the current device (a switch costs 12 us, most of a small call)."""
     if device.type != "cuda":
         raise ValueError(f"expected CUDA tensors, not {device}")
     if stream is None:
+        if device.index == torch.cuda.current_device():
+            return run(torch._C._cuda_getCurrentRawStream(device.index))
         stream = torch.cuda.current_stream(device)
     elif stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
     with torch.cuda.stream(stream):
-        yield stream.cuda_stream
+        return run(stream.cuda_stream)
 
 
 def paged_batch_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
@@ -251,25 +252,26 @@ def paged_batch_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_tab
     dev, B = ctx_lens.device, ctx_lens.shape[0]
     i32, i64 = torch.int32, torch.int64
     _expect(dev, ctx_lens=(ctx_lens, i32, (B,)), new_lens=(new_lens, i32, (B,)),
-            block_table=(block_table, i32, (B, None)), free_blocks=(free_blocks, i32, (None,)),
-            free_count=(free_count, i32, (1,)))
-    with _launch(dev, stream) as st:
-        if out is None:
-            out = (torch.empty(B + 1, dtype=i32, device=dev), torch.empty(B, dtype=i32, device=dev),
-                   torch.empty(max_tokens, dtype=i64, device=dev),
-                   torch.empty(max_tokens, dtype=i64, device=dev),
-                   torch.empty(1, dtype=i32, device=dev))
-        else:
-            _expect(dev, cu_tokens=(out[0], i32, (B + 1,)), seq_lens=(out[1], i32, (B,)),
-                    slots=(out[2], i64, (max_tokens,)), positions=(out[3], i64, (max_tokens,)),
-                    free_left=(out[4], i32, (1,)))
-        cu, lens, slots, positions, left = out
+            block_table=(block_table, i32, (B, *block_table.shape[-1:])),
+            free_blocks=(free_blocks, i32, (free_blocks.numel(),)), free_count=(free_count, i32, (1,)))
+    if out is not None:
+        _expect(dev, cu_tokens=(out[0], i32, (B + 1,)), seq_lens=(out[1], i32, (B,)),
+                slots=(out[2], i64, (max_tokens,)), positions=(out[3], i64, (max_tokens,)),
+                free_left=(out[4], i32, (1,)))
+
+    def run(st):
+        cu, lens, slots, positions, left = out or (
+            ctx_lens.new_empty(B + 1), ctx_lens.new_empty(B),
+            torch.empty(max_tokens, dtype=i64, device=dev),
+            torch.empty(max_tokens, dtype=i64, device=dev), ctx_lens.new_empty(1))
         rc = _lib.lib().fp8q_paged_batch_tables(
-            _ptr(ctx_lens), _ptr(new_lens), B, int(block_size), _ptr(block_table),
-            block_table.shape[1], _ptr(free_blocks), free_blocks.shape[0], _ptr(free_count),
-            _ptr(left), int(max_tokens), _ptr(cu), _ptr(lens), _ptr(slots), _ptr(positions), st)
-    _lib.check(rc, "fp8q_paged_batch_tables")
-    return cu, lens, slots, positions, left
+            ctx_lens.data_ptr(), new_lens.data_ptr(), B, int(block_size), block_table.data_ptr(),
+            block_table.shape[1], free_blocks.data_ptr(), free_blocks.shape[0],
+            free_count.data_ptr(), left.data_ptr(), int(max_tokens), cu.data_ptr(),
+            lens.data_ptr(), slots.data_ptr(), positions.data_ptr(), st)
+        _lib.check(rc, "fp8q_paged_batch_tables")
+        return cu, lens, slots, positions, left
+    return _on_stream(dev, stream, run)
 
 
 def tree_mask(parents: torch.Tensor, cu_nodes: torch.Tensor, max_nodes: int, ctx_lens=None,
@@ -283,19 +285,23 @@ def tree_mask(parents: torch.Tensor, cu_nodes: torch.Tensor, max_nodes: int, ctx
             cu_nodes=(cu_nodes, torch.int32, (B + 1,)))
     if ctx_lens is not None:
         _expect(dev, ctx_lens=(ctx_lens, torch.int32, (B,)))
-    with _launch(dev, stream) as st:
+    if out_mask is not None and (out_mask.dtype != torch.int64 or out_mask.device != dev
+                                 or out_mask.shape[0] != total or out_mask.shape[1] < words):
+        raise ValueError(f"out_mask must be int64 [{total}, >= {words}] on {dev}")
+    if out_positions is not None:
+        _expect(dev, out_positions=(out_positions, torch.int64, (total,)))
+
+    def run(st):
         mask = (torch.empty((total, words), dtype=torch.int64, device=dev) if out_mask is None
                 else out_mask)
         pos = (torch.empty(total, dtype=torch.int64, device=dev) if out_positions is None
                else out_positions)
-        if (mask.dtype != torch.int64 or mask.device != dev or mask.shape[0] != total
-                or mask.shape[1] < words):
-            raise ValueError(f"out_mask must be int64 [{total}, >= {words}] on {dev}")
-        _expect(dev, out_positions=(pos, torch.int64, (total,)))
-        rc = _lib.lib().fp8q_tree_mask(_ptr(parents), _ptr(cu_nodes), _ptr(ctx_lens), B, total,
-                                       int(max_nodes), _ptr(mask), _ld(mask), _ptr(pos), st)
-    _lib.check(rc, "fp8q_tree_mask")
-    return mask, pos
+        rc = _lib.lib().fp8q_tree_mask(parents.data_ptr(), cu_nodes.data_ptr(), _ptr(ctx_lens), B,
+                                       total, int(max_nodes), mask.data_ptr(), _ld(mask),
+                                       pos.data_ptr(), st)
+        _lib.check(rc, "fp8q_tree_mask")
+        return mask, pos
+    return _on_stream(dev, stream, run)
 
 
 def attention_tree_workspace_bytes(B: int, Hq: int, Hkv: int, D: int, max_nodes: int,
@@ -321,7 +327,7 @@ def attention_tree(q_codes: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     slots = k_cache.shape[0]
     _expect(dev, k_cache=(k_cache, torch.uint8, (slots, Hkv * D)),
             v_cache=(v_cache, torch.uint8, (slots, Hkv * D)), scale3=(scale3, torch.float32, (3,)),
-            block_table=(block_table, torch.int32, (B, None)),
+            block_table=(block_table, torch.int32, (B, *block_table.shape[-1:])),
             ctx_lens=(ctx_lens, torch.int32, (B,)), cu_nodes=(cu_nodes, torch.int32, (B + 1,)))
     if q_codes.dtype != torch.uint8 or q_codes.shape[1] != Hq * D:
         raise ValueError(f"q_codes must be uint8 [total, {Hq * D}]")
@@ -330,24 +336,28 @@ def attention_tree(q_codes: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
                              or mask.shape[0] != total or mask.shape[1] < words):
         raise ValueError(f"mask must be int64 [{total}, >= {words}] on {dev}")
     if sm_scale is None:
-        sm_scale = 1.0 / float(np.sqrt(D))
-    with _launch(dev, stream) as st:
-        if workspace is None:
+        sm_scale = D ** -0.5
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    if out is not None and (out.dtype != torch.bfloat16 or out.device != dev
+                            or tuple(out.shape) != (total, Hq * D)):
+        raise ValueError(f"out must be bf16 [{total}, {Hq * D}] on {dev}")
+
+    def run(st):
+        ws = workspace
+        if ws is None:
             n = attention_tree_workspace_bytes(B, Hq, Hkv, D, max_nodes, max_seq_len)
-            workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+            ws = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
         o = torch.empty((total, Hq * D), dtype=torch.bfloat16, device=dev) if out is None else out
-        if o.dtype != torch.bfloat16 or o.device != dev or tuple(o.shape) != (total, Hq * D):
-            raise ValueError(f"out must be bf16 [{total}, {Hq * D}] on {dev}")
         rc = _lib.lib().fp8q_attention_tree(
-            _ptr(q_codes), _ld(q_codes), _ptr(k_cache), _ptr(v_cache), slots, _ptr(scale3),
-            _ptr(block_table), block_table.shape[1], _ptr(ctx_lens), _ptr(cu_nodes), _ptr(mask),
-            _ld(mask) if mask is not None else 0, B, total, Hq, Hkv, D, int(block_size),
-            int(max_nodes), int(max_seq_len), float(sm_scale), _ptr(o), _ld(o), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), st)
-    _lib.check(rc, "fp8q_attention_tree")
-    return o
+            q_codes.data_ptr(), _ld(q_codes), k_cache.data_ptr(), v_cache.data_ptr(), slots,
+            scale3.data_ptr(), block_table.data_ptr(), block_table.shape[1], ctx_lens.data_ptr(),
+            cu_nodes.data_ptr(), _ptr(mask), 0 if mask is None else _ld(mask), B, total, Hq, Hkv, D,
+            int(block_size), int(max_nodes), int(max_seq_len), float(sm_scale), o.data_ptr(), _ld(o),
+            ws.data_ptr(), ws.numel() * ws.element_size(), st)
+        _lib.check(rc, "fp8q_attention_tree")
+        return o
+    return _on_stream(dev, stream, run)
 
 
 def kv_cache_accept(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
@@ -364,18 +374,22 @@ def kv_cache_accept(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: t
     slots, row = k_cache.shape[-2:]
     shape = tuple(k_cache.shape)
     _expect(dev, k_cache=(k_cache, torch.uint8, shape), v_cache=(v_cache, torch.uint8, shape),
-            block_table=(block_table, i32, (B, None)), ctx_lens=(ctx_lens, i32, (B,)),
-            cu_nodes=(cu_nodes, i32, (B + 1,)), path=(path, i32, (B, None)),
-            path_lens=(path_lens, i32, (B,)))
-    with _launch(dev, stream) as st:
-        o = torch.empty(B, dtype=i32, device=dev) if out_lens is None else out_lens
-        _expect(dev, out_lens=(o, i32, (B,)))
+            block_table=(block_table, i32, (B, *block_table.shape[-1:])),
+            ctx_lens=(ctx_lens, i32, (B,)), cu_nodes=(cu_nodes, i32, (B + 1,)),
+            path=(path, i32, (B, *path.shape[-1:])), path_lens=(path_lens, i32, (B,)))
+    if out_lens is not None:
+        _expect(dev, out_lens=(out_lens, i32, (B,)))
+
+    def run(st):
+        o = ctx_lens.new_empty(B) if out_lens is None else out_lens
         rc = _lib.lib().fp8q_kv_cache_accept(
-            _ptr(k_cache), _ptr(v_cache), slots, layers, slots * row, row, _ptr(block_table),
-            block_table.shape[1], int(block_size), _ptr(ctx_lens), _ptr(cu_nodes), _ptr(path),
-            path.shape[1], _ptr(path_lens), B, _ptr(o), st)
-    _lib.check(rc, "fp8q_kv_cache_accept")
-    return o
+            k_cache.data_ptr(), v_cache.data_ptr(), slots, layers, slots * row, row,
+            block_table.data_ptr(), block_table.shape[1], int(block_size), ctx_lens.data_ptr(),
+            cu_nodes.data_ptr(), path.data_ptr(), path.shape[1], path_lens.data_ptr(), B,
+            o.data_ptr(), st)
+        _lib.check(rc, "fp8q_kv_cache_accept")
+        return o
+    return _on_stream(dev, stream, run)
 
 
 def grouped_gemm_w8a8_block(aq: torch.Tensor, sa: torch.Tensor, wq: torch.Tensor,

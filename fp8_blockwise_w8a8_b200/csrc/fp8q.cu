@@ -34,11 +34,8 @@ struct DeviceState {
 constexpr int64_t kStaticScratchBytes = int64_t{24} << 20;
 __device__ __align__(256) uint8_t g_splitk_static_scratch[kStaticScratchBytes];
 
-// Shared memory of the table builder at its largest batch, and of the ancestor-mask kernel.
+// Shared memory of the table builder at its largest batch.
 constexpr int kTablesMaxSmem = 2 * 4 * (fp8q::kTablesMaxB + 1);
-constexpr int tree_mask_smem(int max_nodes) {
-  return max_nodes * ((max_nodes + 63) / 64) * 8 + max_nodes * 4;
-}
 
 std::mutex g_mu;
 DeviceState g_dev[kMaxDevices];
@@ -122,9 +119,6 @@ int device_state(DeviceState **out) {
             cudaSuccess ||
         cudaFuncSetAttribute(fp8q::k_paged_tables, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kTablesMaxSmem) != cudaSuccess ||
-        cudaFuncSetAttribute(fp8q::k_tree_mask<1024>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             tree_mask_smem(fp8q::kTreeMaxNodes)) != cudaSuccess ||
         cudaFuncSetAttribute(fp8q::k_tree_attn<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              fp8q::TreeLayout<128>::kSmem) != cudaSuccess ||
         cudaFuncSetAttribute(fp8q::k_tree_attn<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1091,7 +1085,7 @@ int fp8q_paged_batch_tables(const int32_t *ctx_lens, const int32_t *new_lens, in
   a.seq_lens = seq_lens;
   a.slots = slots;
   a.positions = positions;
-  const int64_t need = (max_tokens + fp8q::kTablesThreads - 1) / fp8q::kTablesThreads;
+  const int64_t need = (max_tokens + 4 * fp8q::kTablesThreads - 1) / (4 * fp8q::kTablesThreads);
   const int64_t cap = 2 * static_cast<int64_t>(st->sms);
   const int grid = static_cast<int>(need < 1 ? 1 : (need < cap ? need : cap));
   fp8q::k_paged_tables<<<grid, fp8q::kTablesThreads, 8 * (B + 1), stream>>>(a);
@@ -1120,16 +1114,15 @@ int fp8q_tree_mask(const int32_t *parents, const int32_t *cu_nodes, const int32_
   a.ctx_lens = ctx_lens;
   a.total = total;
   a.max_nodes = static_cast<int>(max_nodes);
-  a.words = static_cast<int>(words);
   a.mask = mask;
   a.ldm = ldm;
   a.positions = positions;
-  const int smem = tree_mask_smem(a.max_nodes);
-  const unsigned grid = static_cast<unsigned>(B);
-  if (max_nodes <= 256)
-    fp8q::k_tree_mask<128><<<grid, 128, smem, stream>>>(a);
+  const dim3 grid(static_cast<unsigned>(B), static_cast<unsigned>(words));
+  // up to a word of nodes two warps do; else four nodes per thread
+  if (max_nodes <= 64)
+    fp8q::k_tree_mask<64, 1><<<grid, 64, 0, stream>>>(a);
   else
-    fp8q::k_tree_mask<1024><<<grid, 1024, smem, stream>>>(a);
+    fp8q::k_tree_mask<256, fp8q::kTreeMaxNodes / 256><<<grid, 256, 0, stream>>>(a);
   return launch_status();
 }
 

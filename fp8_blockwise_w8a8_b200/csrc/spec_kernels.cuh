@@ -116,33 +116,74 @@ __global__ void __launch_bounds__(kTablesThreads) k_paged_tables(const TablesArg
   }
   if (lead && bad) record_error(9 /* FP8Q_ERR_RANGE */);
   __syncthreads();
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kTablesThreads + tid; t < a.max_tokens;
-       t += static_cast<int64_t>(gridDim.x) * kTablesThreads) {
-    if (t >= total) {                          // behind the last token: a slot no cache write uses
-      a.slots[t] = -1;
-      a.positions[t] = 0;
-      continue;
+  // Four consecutive tokens per thread: one bisection, a division and a block id where the request
+  // or the block changes, 16-byte stores where the arrays allow them.
+  const bool wide = ((reinterpret_cast<uintptr_t>(a.slots) |
+                      reinterpret_cast<uintptr_t>(a.positions)) & 15u) == 0;
+  for (int64_t t0 = 4 * (static_cast<int64_t>(blockIdx.x) * kTablesThreads + tid);
+       t0 < a.max_tokens; t0 += 4 * static_cast<int64_t>(gridDim.x) * kTablesThreads) {
+    int64_t slot[4], position[4];
+    int lo = 0;
+    int64_t end = t0;                          // of the request: none yet
+    uint32_t pos = 0, blk = 0, off = 0, have = 0;
+    int32_t id = -1;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t t = t0 + j;
+      slot[j] = -1;                            // behind the last token: a slot no cache write uses
+      position[j] = 0;
+      if (t >= total) continue;
+      bool fetch = false;
+      if (t >= end) {
+        int hi = a.B;                          // s_cu[lo] <= t < s_cu[hi]
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (s_cu[mid] <= t) lo = mid; else hi = mid;
+        }
+        end = s_cu[lo + 1];
+        const int64_t c0 = a.ctx_lens[lo];
+        const uint32_t c = static_cast<uint32_t>(c0 < 0 ? 0 : (c0 > a.capacity ? a.capacity : c0));
+        pos = c + static_cast<uint32_t>(t - s_cu[lo]);
+        blk = pos / bs;
+        off = pos - blk * bs;
+        have = c / bs + (c % bs != 0);
+        fetch = true;
+      } else {
+        ++pos;
+        if (++off == bs) {
+          off = 0;
+          ++blk;
+          fetch = true;
+        }
+      }
+      if (fetch) {
+        int32_t *entry = a.block_table + lo * a.max_blocks + blk;
+        if (blk < have) {
+          id = *entry;
+        } else {
+          const int64_t k = static_cast<int64_t>(s_nb[lo]) + (blk - have);
+          id = k < avail ? a.free_blocks[avail - 1 - k] : -1;
+          if (off == 0) *entry = id;
+        }
+      }
+      slot[j] = id < 0 ? -1 : static_cast<int64_t>(id) * bs + off;
+      position[j] = pos;
     }
-    int lo = 0, hi = a.B;                      // s_cu[lo] <= t < s_cu[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s_cu[mid] <= t) lo = mid; else hi = mid;
-    }
-    const int64_t c0 = a.ctx_lens[lo];
-    const uint32_t c = static_cast<uint32_t>(c0 < 0 ? 0 : (c0 > a.capacity ? a.capacity : c0));
-    const uint32_t pos = c + static_cast<uint32_t>(t - s_cu[lo]);
-    const uint32_t blk = pos / bs, off = pos % bs, have = (c + bs - 1) / bs;
-    int32_t *entry = a.block_table + lo * a.max_blocks + blk;
-    int32_t id;
-    if (blk < have) {
-      id = *entry;
+    if (wide && t0 + 3 < a.max_tokens) {
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        *reinterpret_cast<longlong2 *>(a.slots + t0 + j) = make_longlong2(slot[j], slot[j + 1]);
+        *reinterpret_cast<longlong2 *>(a.positions + t0 + j) =
+            make_longlong2(position[j], position[j + 1]);
+      }
     } else {
-      const int64_t k = static_cast<int64_t>(s_nb[lo]) + (blk - have);
-      id = k < avail ? a.free_blocks[avail - 1 - k] : -1;
-      if (off == 0) *entry = id;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (t0 + j < a.max_tokens) {
+          a.slots[t0 + j] = slot[j];
+          a.positions[t0 + j] = position[j];
+        }
     }
-    a.slots[t] = id < 0 ? -1 : static_cast<int64_t>(id) * bs + off;
-    a.positions[t] = pos;
   }
 }
 
@@ -150,14 +191,13 @@ __global__ void __launch_bounds__(kTablesThreads) k_paged_tables(const TablesArg
 // Ancestor masks
 // ---------------------------------------------------------------------------------------------
 constexpr int kTreeMaxNodes = 1024;
-constexpr int kTreeMaskItems = 16;   // (node, word) pairs per thread at most
 
 struct TreeMaskArgs {
   const int32_t *parents;            // [total]
   const int32_t *cu;                 // [B + 1]
   const int32_t *ctx_lens;           // [B] or null
   int64_t total;
-  int max_nodes, words;
+  int max_nodes;
   int64_t *mask;                     // [total][ldm]
   int64_t ldm;
   int64_t *positions;                // [total] or null
@@ -176,70 +216,68 @@ __device__ __forceinline__ int tree_rows(const int32_t *cu, int b, int64_t total
   return static_cast<int>(n);
 }
 
-// One CTA per sequence, which also looks through the offsets up to its own: where they decrease the
-// batch ends, so that no two sequences write the same rows.  Bit j of row i is set iff j is i or an ancestor of i.  Pointer doubling:
-// row i holds the nodes from i up to (not including) anc[i]; a round ORs in the row of anc[i] and
-// jumps to anc[anc[i]], so a tree of depth d takes ceil(log2 d) rounds instead of d steps.  Each
-// round reads into registers, then writes, so no row is read while it changes.
-template <int T>
+// One CTA per sequence and word of the rows: a word needs no other one.  Every CTA also looks through
+// the offsets up to its sequence: where they decrease the batch ends, so that no two sequences write
+// the same rows.  Pointer doubling: row i holds the nodes from i up to (not including) anc[i]; a
+// round ORs in the row of anc[i] and jumps to anc[anc[i]], so a tree of depth d takes ceil(log2 d)
+// rounds instead of d steps.  Word w needs no ancestor below its first node 64 w: anc is cut there.
+// The first word's CTA counts the depths along the way.  Each round reads into registers, then
+// writes, so no row is read while it changes.
+template <int T, int ITEMS>
 __global__ void __launch_bounds__(T) k_tree_mask(const TreeMaskArgs a) {
-  extern __shared__ uint64_t s_bits[];                         // [n][W], then anc [n]
-  const int b = blockIdx.x, tid = threadIdx.x, W = a.words;
+  __shared__ uint64_t s_bits[T * ITEMS];
+  __shared__ int32_t s_anc[T * ITEMS], s_depth[T * ITEMS];
+  const int b = blockIdx.x, w = blockIdx.y, tid = threadIdx.x;
   int64_t first;
   bool bad, falls = false;
   const int n = tree_rows(a.cu, b, a.total, a.max_nodes, &first, &bad);
   for (int i = tid; i <= b; i += T) falls |= a.cu[i + 1] < a.cu[i];
-  int32_t *s_anc = reinterpret_cast<int32_t *>(s_bits + static_cast<int64_t>(a.max_nodes) * W);
-  for (int i = tid; i < n; i += T) {
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    const int i = tid + k * T;
+    if (i >= n) continue;
     int p = a.parents[first + i];
     if (p < -1 || p >= i) {                                    // parents come first
       bad = true;
       p = -1;
     }
-    s_anc[i] = p;
-    for (int w = 0; w < W; ++w) s_bits[i * W + w] = w == i / 64 ? 1ull << (i % 64) : 0ull;
+    s_anc[i] = p >= 64 * w ? p : -1;
+    s_bits[i] = i / 64 == w ? 1ull << (i % 64) : 0ull;
+    s_depth[i] = p >= 0;
   }
-  if (bad) record_error(9 /* FP8Q_ERR_RANGE */);
+  if (bad && w == 0) record_error(9 /* FP8Q_ERR_RANGE */);
   if (__syncthreads_or(falls)) return;
-  const int items = n * W;
   for (;;) {
-    uint64_t add[kTreeMaskItems];
-    int next[kTreeMaskItems];
+    uint64_t add[ITEMS];
+    int next[ITEMS], up[ITEMS];
     bool more = false;
 #pragma unroll
-    for (int k = 0; k < kTreeMaskItems; ++k) {
-      const int it = tid + k * T;
-      if (it < items) {
-        const int i = it / W, w = it - i * W, p = s_anc[i];
-        add[k] = p >= 0 ? s_bits[p * W + w] : 0ull;
-        next[k] = p >= 0 ? s_anc[p] : -1;
-        more |= next[k] >= 0;
-      }
+    for (int k = 0; k < ITEMS; ++k) {
+      const int i = tid + k * T, p = i < n ? s_anc[i] : -1;
+      add[k] = p >= 0 ? s_bits[p] : 0ull;
+      up[k] = p >= 0 ? s_depth[p] : 0;
+      next[k] = p >= 0 ? s_anc[p] : -1;
+      more |= next[k] >= 0;
     }
     more = __syncthreads_or(more);
 #pragma unroll
-    for (int k = 0; k < kTreeMaskItems; ++k) {
-      const int it = tid + k * T;
-      if (it < items) {
-        const int i = it / W, w = it - i * W;
-        s_bits[it] |= add[k];
-        if (w == 0) s_anc[i] = next[k];
-      }
+    for (int k = 0; k < ITEMS; ++k) {
+      const int i = tid + k * T;
+      if (i >= n) continue;
+      s_bits[i] |= add[k];
+      s_depth[i] += up[k];
+      s_anc[i] = next[k];
     }
     __syncthreads();
     if (!more) break;
   }
-  for (int it = tid; it < items; it += T) {
-    const int i = it / W, w = it - i * W;
-    a.mask[(first + i) * a.ldm + w] = static_cast<int64_t>(s_bits[it]);
-  }
-  if (a.positions) {
-    const int64_t c = a.ctx_lens ? a.ctx_lens[b] : 0;
-    for (int i = tid; i < n; i += T) {
-      int depth = -1;
-      for (int w = 0; w <= i / 64; ++w) depth += __popcll(s_bits[i * W + w]);
-      a.positions[first + i] = c + depth;
-    }
+  const int64_t c = a.positions && a.ctx_lens ? a.ctx_lens[b] : 0;
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    const int i = tid + k * T;
+    if (i >= n) continue;
+    a.mask[(first + i) * a.ldm + w] = static_cast<int64_t>(s_bits[i]);
+    if (a.positions && w == 0) a.positions[first + i] = c + s_depth[i];
   }
 }
 

@@ -79,7 +79,7 @@ constexpr int kTreeN = 64;           // cached positions per tile
 constexpr int kTreeThreads = 384;    // 4 softmax warps, 4 convert V, one each: MMAs, K, Q, copies of V
 constexpr int kTreeMaxCtas = 296;    // 2 per SM of 148
 constexpr int kTreeStages = 3;       // K and V tiles (codes) in shared memory
-constexpr int kTreeItemCost = 2;     // cost of starting a row tile, in position tiles
+constexpr int kTreeItemCost = 4;     // cost of starting a row tile, in position tiles
 constexpr int kTreeMinCost = 4;      // least cost per CTA
 constexpr int kTreeMetaInts = 8;
 constexpr float kTreeLag = 8.0f;     // the reference lags the running maximum by at most 2^8

@@ -63,6 +63,7 @@ __device__ __forceinline__ int64_t cta_exclusive_scan(int64_t v, int64_t *s_warp
 // block is always a new token, so that token writes the table entry and no thread reads an entry
 // that this launch writes.  Every CTA makes the prefix sums itself (2 B words from L2): one launch,
 // no exchange between CTAs.
+template <int R>
 __global__ void __launch_bounds__(kTablesThreads) k_paged_tables(const TablesArgs a) {
   extern __shared__ int32_t s_tab[];          // [B + 1] token offsets, [B + 1] new-block offsets
   __shared__ int64_t s_warp[kTablesThreads / 32];
@@ -116,19 +117,19 @@ __global__ void __launch_bounds__(kTablesThreads) k_paged_tables(const TablesArg
   }
   if (lead && bad) record_error(9 /* FP8Q_ERR_RANGE */);
   __syncthreads();
-  // Four consecutive tokens per thread: one bisection, a division and a block id where the request
-  // or the block changes, 16-byte stores where the arrays allow them.
-  const bool wide = ((reinterpret_cast<uintptr_t>(a.slots) |
+  // R consecutive tokens per thread: a bisection where the request changes, a block id where the block
+  // changes, 16-byte stores where the arrays allow them.
+  const bool wide = R > 1 && ((reinterpret_cast<uintptr_t>(a.slots) |
                       reinterpret_cast<uintptr_t>(a.positions)) & 15u) == 0;
-  for (int64_t t0 = 4 * (static_cast<int64_t>(blockIdx.x) * kTablesThreads + tid);
-       t0 < a.max_tokens; t0 += 4 * static_cast<int64_t>(gridDim.x) * kTablesThreads) {
-    int64_t slot[4], position[4];
+  for (int64_t t0 = R * (static_cast<int64_t>(blockIdx.x) * kTablesThreads + tid);
+       t0 < a.max_tokens; t0 += R * static_cast<int64_t>(gridDim.x) * kTablesThreads) {
+    int64_t slot[R], position[R];
     int lo = 0;
     int64_t end = t0;                          // of the request: none yet
     uint32_t pos = 0, blk = 0, off = 0, have = 0;
     int32_t id = -1;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < R; ++j) {
       const int64_t t = t0 + j;
       slot[j] = -1;                            // behind the last token: a slot no cache write uses
       position[j] = 0;
@@ -169,16 +170,16 @@ __global__ void __launch_bounds__(kTablesThreads) k_paged_tables(const TablesArg
       slot[j] = id < 0 ? -1 : static_cast<int64_t>(id) * bs + off;
       position[j] = pos;
     }
-    if (wide && t0 + 3 < a.max_tokens) {
+    if (wide && t0 + R <= a.max_tokens) {
 #pragma unroll
-      for (int j = 0; j < 4; j += 2) {
+      for (int j = 0; j + 1 < R; j += 2) {
         *reinterpret_cast<longlong2 *>(a.slots + t0 + j) = make_longlong2(slot[j], slot[j + 1]);
         *reinterpret_cast<longlong2 *>(a.positions + t0 + j) =
             make_longlong2(position[j], position[j + 1]);
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < R; ++j)
         if (t0 + j < a.max_tokens) {
           a.slots[t0 + j] = slot[j];
           a.positions[t0 + j] = position[j];

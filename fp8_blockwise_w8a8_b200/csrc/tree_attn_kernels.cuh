@@ -1054,6 +1054,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
 template <int D>
 __global__ void __launch_bounds__(256) k_tree_attn_combine(const TreeAttnArgs a) {
   constexpr int V = D / 32;
+  static_assert(V == 2 || V == 4, "vector loads of the parts");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int i = blockIdx.x;
   const int32_t *meta = a.meta + i * kTreeMetaInts;
@@ -1066,6 +1067,13 @@ __global__ void __launch_bounds__(256) k_tree_attn_combine(const TreeAttnArgs a)
   const float *base = a.part + r * D + V * lane;
   const int64_t ml = static_cast<int64_t>(a.row_cap) * D + 2 * r;
   float M = -INFINITY, l = 0.0f, o[V] = {};
+  auto add = [&](const float *p, float wk) {
+    alignas(16) float v[V];
+    if constexpr (V == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(p);
+    else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(p);
+#pragma unroll
+    for (int k = 0; k < V; ++k) o[k] += v[k] * wk;
+  };
   // 32 parts at a time: their maxima and sums by lanes, then the values one after the other
   for (int j0 = i;; j0 += 32) {
     const int j = j0 + lane;
@@ -1095,13 +1103,11 @@ __global__ void __launch_bounds__(256) k_tree_attn_combine(const TreeAttnArgs a)
 #pragma unroll
     for (int v = 0; v < V; ++v) o[v] *= keep;
     M = top;
+    const int k0 = j0 == i ? 1 : 0;                              // part i is the CTA's second slot
+    if (k0) add(base + (2 * static_cast<int64_t>(i) + 1) * slot, __shfl_sync(0xffffffffu, w, 0));
+    const float *p = base + 2 * static_cast<int64_t>(j0 + k0) * slot;
 #pragma unroll 8
-    for (int k = 0; k < n; ++k) {
-      const float wk = __shfl_sync(0xffffffffu, w, k);
-      const float *p = base + (2 * static_cast<int64_t>(j0 + k) + (j0 + k == i ? 1 : 0)) * slot;
-#pragma unroll
-      for (int v = 0; v < V; ++v) o[v] += p[v] * wk;
-    }
+    for (int k = k0; k < n; ++k, p += 2 * slot) add(p, __shfl_sync(0xffffffffu, w, k));
     if (ends) break;
   }
   const float f = l == 0.0f ? 0.0f : a.scale3[2] / l;

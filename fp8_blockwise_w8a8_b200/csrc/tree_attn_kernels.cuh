@@ -312,7 +312,7 @@ __device__ __forceinline__ bool tree_take(TreeShared &sh, uint32_t ip, TreePiece
 // The dims of kv head g that are NaN in a value row seen by row (node i) among the positions of
 // [t, t_end) whose column within its tile lies in [c0, c0 + nc).  Runs only where V holds NaN codes.
 template <int D>
-__device__ __noinline__ uint4 tree_nan_dims(const TreeAttnArgs &a, const TreePiece &c, int i, int c0,
+__device__ __noinline__ uint4 tree_nan_dims(const TreeAttnArgs &a, TreePiece c, int i, int c0,
                                             int nc) {
   uint32_t dims[4] = {};
   const int words = (a.max_nodes + 63) / 64;
@@ -455,7 +455,7 @@ __device__ __forceinline__ bool tree_any4(bool v) {
 template <int D>
 __global__ void __launch_bounds__(kTreeThreads, 2)
     k_tree_attn(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                const TreeAttnArgs a) {
+                const __grid_constant__ TreeAttnArgs a) {
   using L = TreeLayout<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ TreeShared sh;

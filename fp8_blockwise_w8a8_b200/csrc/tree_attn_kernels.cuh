@@ -42,6 +42,7 @@ struct TreeAttnArgs {
   float sm_scale;
   uint16_t *out;               // [total][ldo] bf16
   int64_t ldo;
+  int log_hkv;                 // ceil(log2(Hkv))
   int box;                     // rows per copy: the power of two in block_size, at most 64; 1: gathers
   uint64_t grid_recip;         // floor((2^64 - 1) / gridDim.x)
   TreeDiv by_block, by_group;  // by block_size and by G = Hq / Hkv
@@ -78,19 +79,20 @@ constexpr int kTreeM = 128;          // query rows (node, head of the group) per
 constexpr int kTreeN = 64;           // cached positions per tile
 constexpr int kTreeThreads = 384;    // 4 softmax warps, 4 convert V, one each: MMAs, K, Q, copies of V
 constexpr int kTreeMaxCtas = 296;    // 2 per SM of 148
-constexpr int kTreeStages = 3;       // K and V tiles (codes) in shared memory
+constexpr int kTreeStages = 3;       // V tiles (codes) in shared memory, position tiles known ahead
 constexpr int kTreeItemCost = 4;     // cost of starting a row tile, in position tiles
 constexpr int kTreeMinCost = 4;      // least cost per CTA
 constexpr int kTreeMetaInts = 8;
 constexpr float kTreeLag = 8.0f;     // the reference lags the running maximum by at most 2^8
 constexpr float kTreeBias = 7.0f;    // weights are 2^(z - reference + 7): at most 2^15 in fp16
 
-template <int D>
+template <int D, bool M>
 struct TreeLayout {
+  static constexpr int kKStages = M ? 4 : 3;                     // K tiles (codes) in shared memory
   static constexpr int kQ = 0;                                   // [128][128 B], swizzled
   static constexpr int kK = kQ + kTreeM * 128;                   // [stage][64][D], swizzled
   static constexpr int kTile = kTreeN * D;
-  static constexpr int kV16 = kK + kTreeStages * kTile;          // [2][D / 64][64][128 B], swizzled
+  static constexpr int kV16 = kK + kKStages * kTile;          // [2][D / 64][64][128 B], swizzled
   static constexpr int kV16Bytes = kTreeN * D * 2;
   static constexpr int kV8 = kV16 + 2 * kV16Bytes;               // [stage][64][D]
   static constexpr int kSmem = kV8 + kTreeStages * kTile + 1024;
@@ -113,47 +115,60 @@ __device__ __forceinline__ int tree_tiles(const TreeAttnArgs &a, const TreeSeq &
   const int last = a.by_group(min(s.n * G, (rt + 1) * kTreeM) - 1);  // the tile's last node
   return (s.ctx + last) / kTreeN + 1;
 }
-__device__ __forceinline__ int64_t tree_group_cost(const TreeAttnArgs &a, const TreeSeq &s, int G) {
+// Log2 of the repeats of up to 32 (64) rows in a row tile of 128.
+__device__ __forceinline__ int tree_shift(int rows) { return rows <= 32 ? 2 : (rows <= 64 ? 1 : 0); }
+// Log2 of the kv heads that share a row tile (log_hkv > 0): as many as fit, 32 or 64 rows each.
+__device__ __forceinline__ int tree_heads(const TreeAttnArgs &a, const TreeSeq &s, int G) {
+  return min(tree_shift(s.n * G), a.log_hkv);
+}
+// Position tiles of all heads, and kTreeItemCost for each item (row tile of a group of heads).
+__device__ __forceinline__ int64_t tree_seq_cost(const TreeAttnArgs &a, const TreeSeq &s, int G) {
+  const int groups = (a.Hkv + (1 << tree_heads(a, s, G)) - 1) >> tree_heads(a, s, G);
   int64_t c = 0;
 #pragma unroll 1
   for (int rt = tree_row_tiles(s.n, G) - 1; rt >= 0; --rt)
-    c += tree_tiles(a, s, G, rt) + kTreeItemCost;
+    c += static_cast<int64_t>(tree_tiles(a, s, G, rt)) * a.Hkv + groups * kTreeItemCost;
   return c;
 }
 
-// A share of one item (sequence, kv head, row tile): its position tiles [t, t_end) of nt.  The load
-// warp hands the pieces of a CTA to the other roles, the last one with t_end = 0.
+// A share of one item (sequence, heads g .. g + hc - 1, row tile): its position tiles [t, t_end) of
+// nt.  The load warp hands the pieces of a CTA to the other roles, the last one with t_end = 0.
 struct TreePiece {
   int64_t first;                 // row of the sequence's node 0
-  int b, n, ctx, g, row0, rows, t, t_end, nt;
+  int b, n, ctx, g, hc, hsh, row0, rows, t, t_end, nt;
 };
 
 // The pieces of work of one CTA: a range of the cost axis on which the items stand one behind the
-// other, each as long as its position tiles plus kTreeItemCost.
+// other, each as long as its position tiles times its heads plus kTreeItemCost.
 struct TreeCursor {
   TreeSeq s;
   int64_t rem;
-  int B, b, g, rt, t, t_end, nt;
+  int B, b, g, hsh, rt, t, t_end, nt;
   bool live;
 
+  __device__ __forceinline__ int heads(const TreeAttnArgs &a) const {
+    return min(1 << hsh, a.Hkv - g);
+  }
   // From the sequence b0, `off` behind its start; cost 0: nothing.
   __device__ __forceinline__ void init(const TreeAttnArgs &a, int G, int num, int b0, int64_t off,
                                        int64_t cost) {
     B = num;
     rem = cost;
     b = b0;
-    g = rt = t = t_end = 0;
+    g = rt = t = t_end = hsh = 0;
     live = cost > 0;
     if (!live) return;
     s = tree_seq(a, b, false);
-    const int64_t per_g = tree_group_cost(a, s, G);
-    while (off >= per_g) {
-      off -= per_g;
-      ++g;
-    }
-    int tiles;
-    while (off >= (tiles = tree_tiles(a, s, G, rt) + kTreeItemCost)) {
-      off -= tiles;
+    hsh = tree_heads(a, s, G);
+    // the group of heads and the item that hold the offset
+    int64_t per = 0;
+#pragma unroll 1
+    for (int i = tree_row_tiles(s.n, G) - 1; i >= 0; --i)
+      per += static_cast<int64_t>(tree_tiles(a, s, G, i) << hsh) + kTreeItemCost;
+    for (; off >= per && g + (1 << hsh) < a.Hkv; g += 1 << hsh) off -= per;
+    int c;
+    while (off >= (c = tree_tiles(a, s, G, rt) * heads(a) + kTreeItemCost)) {
+      off -= c;
       ++rt;
     }
     --rt;
@@ -168,7 +183,8 @@ struct TreeCursor {
       }
       if (++rt == tree_row_tiles(s.n, G)) {
         rt = 0;
-        if (++g == a.Hkv) {
+        g += 1 << hsh;
+        if (g >= a.Hkv) {
           g = 0;
           do {
             if (++b >= B) {
@@ -177,12 +193,14 @@ struct TreeCursor {
             }
             s = tree_seq(a, b, false);
           } while (s.n == 0);
+          hsh = tree_heads(a, s, G);
         }
       }
       nt = tree_tiles(a, s, G, rt);
-      const int64_t take = min(static_cast<int64_t>(nt + kTreeItemCost - off), rem);
-      t = max(0, off - kTreeItemCost);
-      t_end = max(0, off + static_cast<int>(take) - kTreeItemCost);
+      const int w = heads(a);                                    // nt * w < 2^28
+      const int take = static_cast<int>(min(static_cast<int64_t>(nt * w + kTreeItemCost - off), rem));
+      t = max(0, off - kTreeItemCost) / w;
+      t_end = max(0, off + take - kTreeItemCost) / w;
       rem -= take;
       off = 0;
     } while (t >= t_end);
@@ -276,19 +294,21 @@ __device__ __forceinline__ void tree_st(uint32_t taddr, const uint32_t (&r)[N]) 
 
 // What the CTA's roles share.
 constexpr int kTreePieces = 4;   // descriptors in the ring
-struct TreeTile {                // for the copies of V
+struct TreeTile {                // a position tile, for the copies of V
   alignas(16) int32_t row[kTreeN];   // first cache row of each copy, or each position's row
-  int32_t g, piece;              // kv head (-1: no more tiles), 1 + index of the piece
+  int32_t g, hc, piece;          // first kv head (-1: no more tiles), heads, 1 + index of the piece
 };
+template <bool M>
 struct TreeShared {
-  uint64_t k_full[kTreeStages], k_free[kTreeStages], t_full[kTreeStages], t_free[kTreeStages];
+  uint64_t k_full[M ? 4 : 3], k_free[M ? 4 : 3], t_full[kTreeStages], t_free[kTreeStages];
   uint64_t v8_full[kTreeStages], v8_free[kTreeStages];
   uint64_t piece_full[kTreePieces], piece_free[kTreePieces];
-  uint64_t q_full, q_free, v_full[2], s_full[2], p_full[2], pv_done[2], drain;
+  uint64_t q_full, q_free, v_full[2], s_full[2], p_full[2], pv_done[2], o_done[2], drain;
   uint64_t valid[8];             // per tile (mod 8): the positions that exist, one bit each
   TreePiece piece[kTreePieces];
   TreeTile tile[kTreeStages];
   int32_t v8_piece[kTreeStages]; // 1 + index of the stage's piece, -1: no more tiles
+  uint32_t v8_tile[kTreeStages]; // index of its position tile
   int start_b;
   int64_t start_off;
   int64_t warp_sum[kTreeThreads / 32];
@@ -296,11 +316,12 @@ struct TreeShared {
   int abort;
   int nan_piece;                 // 1 + index of the last piece with a NaN code in V
   float ml[4][32][2];
-  float4 o[4][32][5];            // 16 columns, rows 80 bytes apart
+  float4 o[4][M ? 1 : 32][5];    // 16 columns, rows 80 bytes apart
 };
 
 // The next piece of the ring for the calling warp; false where there is none.
-__device__ __forceinline__ bool tree_take(TreeShared &sh, uint32_t ip, TreePiece &pc) {
+template <bool M>
+__device__ __forceinline__ bool tree_take(TreeShared<M> &sh, uint32_t ip, TreePiece &pc) {
   const uint32_t i = ip % kTreePieces;
   pc.t = pc.t_end = 0;
   if (!tree_wait<true>(sh.piece_full[i], ip / kTreePieces, &sh.abort)) return false;
@@ -312,7 +333,7 @@ __device__ __forceinline__ bool tree_take(TreeShared &sh, uint32_t ip, TreePiece
 // The dims of kv head g that are NaN in a value row seen by row (node i) among the positions of
 // [t, t_end) whose column within its tile lies in [c0, c0 + nc).  Runs only where V holds NaN codes.
 template <int D>
-__device__ __noinline__ uint4 tree_nan_dims(const TreeAttnArgs &a, TreePiece c, int i, int c0,
+__device__ __noinline__ uint4 tree_nan_dims(const TreeAttnArgs &a, TreePiece c, int g, int i, int c0,
                                             int nc) {
   uint32_t dims[4] = {};
   const int words = (a.max_nodes + 63) / 64;
@@ -325,7 +346,7 @@ __device__ __noinline__ uint4 tree_nan_dims(const TreeAttnArgs &a, TreePiece c, 
       const int32_t blk = a.block_table[c.b * a.max_blocks + a.by_block(pos)];
       if (blk < 0 || blk >= a.num_blocks) continue;
       const int64_t slot = static_cast<int64_t>(blk) * a.block_size + pos % a.block_size;
-      const uint32_t *v = reinterpret_cast<const uint32_t *>(a.v_cache + (slot * a.Hkv + c.g) * D);
+      const uint32_t *v = reinterpret_cast<const uint32_t *>(a.v_cache + (slot * a.Hkv + g) * D);
       for (int w = 0; w < D / 32; ++w)
 #pragma unroll 1
         for (int x = 0; x < 8; ++x) {
@@ -361,11 +382,11 @@ __device__ __forceinline__ void tree_scores(uint32_t taddr, bool all, uint64_t s
 // chunk's scores stay in registers between the maximum and the weights, the others are read again.
 // Loops over short bodies: the roles' code together has to stay in the instruction caches.  j0: the
 // tile's first position, counted from node 0.
-template <int D>
-__device__ __forceinline__ bool tree_tile(TreeShared &sh, uint32_t tmem, uint32_t col0, int chunks,
+template <int D, bool M>
+__device__ __forceinline__ bool tree_tile(TreeShared<M> &sh, uint32_t tmem, uint32_t col0, int chunks,
                                           uint32_t it, bool first, const int64_t *mrow, int words,
                                           int node, int j0, float c2, TreeRow &st) {
-  using L = TreeLayout<D>;
+  using L = TreeLayout<D, M>;
   if (!tree_wait<true>(sh.s_full[it & 1u], it >> 1, &sh.abort)) return false;
   tc_fence_after();
   const uint32_t buf = tmem + L::kColS + 64 * (it & 1u);
@@ -395,7 +416,7 @@ __device__ __forceinline__ bool tree_tile(TreeShared &sh, uint32_t tmem, uint32_
     st.ref = up ? top : st.ref;
     st.l *= f;
     if (!first && __any_sync(0xffffffffu, held)) {
-      if (!tree_wait<true>(sh.pv_done[(it - 1) & 1u], (it - 1) >> 1, &sh.abort)) return false;
+      if (!tree_wait<true>(sh.o_done[(it - 1) & 1u], (it - 1) >> 1, &sh.abort)) return false;
       tc_fence_after();
 #pragma unroll 1
       for (int d = 0; d < D; d += 16) {
@@ -452,22 +473,25 @@ __device__ __forceinline__ bool tree_any4(bool v) {
   return r != 0;
 }
 
-template <int D>
+template <int D, bool M>
 __global__ void __launch_bounds__(kTreeThreads, 2)
     k_tree_attn(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                 const __grid_constant__ TreeAttnArgs a) {
-  using L = TreeLayout<D>;
+  using L = TreeLayout<D, M>;
+  constexpr int kKStages = L::kKStages;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ TreeShared sh;
+  __shared__ TreeShared<M> sh;
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.Hq / a.Hkv;
 
   if (tid == 0) {
-    for (int i = 0; i < kTreeStages; ++i) {
+    for (int i = 0; i < kKStages; ++i) {
       mbar_init(smem_u32(&sh.k_full[i]), 1);
       mbar_init(smem_u32(&sh.k_free[i]), 1);
+    }
+    for (int i = 0; i < kTreeStages; ++i) {
       mbar_init(smem_u32(&sh.t_full[i]), 1);
       mbar_init(smem_u32(&sh.t_free[i]), 1);
       mbar_init(smem_u32(&sh.v8_full[i]), 1);
@@ -484,6 +508,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       mbar_init(smem_u32(&sh.p_full[i]), 4);
       mbar_init(smem_u32(&sh.pv_done[i]), 1);
       mbar_init(smem_u32(&sh.s_full[i]), 1);
+      mbar_init(smem_u32(&sh.o_done[i]), 1);
     }
     mbar_init(smem_u32(&sh.drain), 1);
     sh.abort = 0;
@@ -505,7 +530,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     bool falls = false;
     for (int b = tid * per; b < min(B, (tid + 1) * per); ++b) {
       falls |= a.cu[b + 1] < a.cu[b];
-      mine += tree_group_cost(a, tree_seq(a, b, blockIdx.x == 0), G) * a.Hkv;
+      mine += tree_seq_cost(a, tree_seq(a, b, blockIdx.x == 0), G);
     }
     upto = mine;
 #pragma unroll
@@ -542,7 +567,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     int64_t off = lo - (upto - mine);
     int b = tid * per;
     for (;; ++b) {
-      const int64_t c = tree_group_cost(a, tree_seq(a, b, false), G) * a.Hkv;
+      const int64_t c = tree_seq_cost(a, tree_seq(a, b, false), G);
       if (off < c) break;
       off -= c;
     }
@@ -588,7 +613,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       const uint32_t i = ip % kTreePieces;
       if (!tree_wait<true>(sh.piece_free[i], (ip / kTreePieces) ^ 1u, &sh.abort)) return false;
       if (lane == 0)
-        sh.piece[i] = TreePiece{pre.s.first, pre.b, pre.s.n, pre.s.ctx, pre.g, pre.rt * kTreeM,
+        sh.piece[i] = TreePiece{pre.s.first, pre.b, pre.s.n, pre.s.ctx, pre.g, pre.heads(a), pre.hsh,
+                                pre.rt * kTreeM,
                                 min(kTreeM, pre.s.n * G - pre.rt * kTreeM), pre.t,
                                 pre.live ? pre.t_end : 0, pre.nt};
       tree_arrive(sh.piece_full[i]);
@@ -596,15 +622,14 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       return true;
     };
     look_up();
-    uint32_t it = 0, st = 0, ph = 1u;
-    bool fresh = true;
-    for (;; ++it) {
+    // position tiles (it; ts, tph: stage and phase of their rows), tiles of single heads (kt; st, ph)
+    uint32_t it = 0, ts = 0, tph = 1u, kt = 0, st = 0, ph = 1u;
+    bool fresh = true, going = true;
+    for (; going; ++it) {
       if (fresh && !publish()) break;
       if (!pre.live) break;
       // the stage first: the block ids are on their way meanwhile
-      if (!tree_wait<true>(sh.k_free[st], ph, &sh.abort) ||
-          !tree_wait<true>(sh.t_free[st], ph, &sh.abort))
-        break;
+      if (!tree_wait<true>(sh.t_free[ts], tph, &sh.abort)) break;
       bool ok;
       int32_t slot[2] = {slot_of(0, &ok), 0};
       uint64_t there;
@@ -623,83 +648,101 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           if (left < 64) there &= (1ull << left) - 1;
         }
       }
-      const uint32_t bar = smem_u32(&sh.k_full[st]);
+      const int hc = M ? pre.heads(a) : 1;
       if (lane == 0) {
         sh.valid[it & 7u] = there;
-        sh.tile[st].g = pre.g;
-        sh.tile[st].piece = static_cast<int>(ip);
-        mbar_arrive_expect_tx(bar, L::kTile);
+        sh.tile[ts].g = pre.g;
+        sh.tile[ts].hc = hc;
+        sh.tile[ts].piece = static_cast<int>(ip);
       }
-      __syncwarp();
-      const uint32_t dst = sbase + L::kK + st * L::kTile;
+      sh.tile[ts].row[lane] = slot[0];
+      sh.tile[ts].row[32 + lane] = slot[1];
+      tree_arrive(sh.t_full[ts]);
+      int32_t rows[4];
       if (gather) {
-        int32_t rows[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int32_t v0 = __shfl_sync(0xffffffffu, slot[0], (4 * lane + r) & 31);
           const int32_t v1 = __shfl_sync(0xffffffffu, slot[1], (4 * lane + r) & 31);
           rows[r] = lane & 8 ? v1 : v0;
         }
-        if (lane < 16) tma_gather4(dst + 4 * D * lane, &tm_k, pre.g * D, rows, bar);
-      } else if (lane < chunks) {
-        tma_load_2d(dst + lane * a.box * D, &tm_k, pre.g * D, slot[0], bar);
       }
-      sh.tile[st].row[lane] = slot[0];
-      sh.tile[st].row[32 + lane] = slot[1];
-      tree_arrive(sh.t_full[st]);
-      if (++st == kTreeStages) {
-        st = 0;
-        ph ^= 1u;
+#pragma unroll 1
+      for (int j = 0; j < hc; ++j, ++kt) {
+        if (!(going = tree_wait<true>(sh.k_free[st], ph, &sh.abort))) break;
+        const uint32_t bar = smem_u32(&sh.k_full[st]), dst = sbase + L::kK + st * L::kTile;
+        const int x = (pre.g + j) * D;
+        if (lane == 0) mbar_arrive_expect_tx(bar, L::kTile);
+        __syncwarp();
+        if (gather) {
+          if (lane < 16) tma_gather4(dst + 4 * D * lane, &tm_k, x, rows, bar);
+        } else if (lane < chunks) {
+          tma_load_2d(dst + lane * a.box * D, &tm_k, x, slot[0], bar);
+        }
+        if (++st == kKStages) {
+          st = 0;
+          ph ^= 1u;
+        }
+      }
+      if (++ts == kTreeStages) {
+        ts = 0;
+        tph ^= 1u;
       }
       fresh = ++pre.t >= pre.t_end;
       if (fresh) pre.next(a, G, 0);
       look_up();
     }
-    if (tree_wait<true>(sh.t_free[st], ph, &sh.abort)) {         // the end
-      if (lane == 0) sh.tile[st].g = -1;
-      tree_arrive(sh.t_full[st]);
+    if (tree_wait<true>(sh.t_free[ts], tph, &sh.abort)) {        // the end
+      if (lane == 0) sh.tile[ts].g = -1;
+      tree_arrive(sh.t_full[ts]);
     }
     // after a wait that gave up: no copy in flight at exit
-    for (uint32_t i = it < kTreeStages ? 0 : it - kTreeStages; i < it; ++i)
-      wait_drain(smem_u32(&sh.k_full[i % kTreeStages]), (i / kTreeStages) & 1u);
+    for (uint32_t i = kt < kKStages ? 0 : kt - kKStages; i < kt; ++i)
+      wait_drain(smem_u32(&sh.k_full[i % kKStages]), (i / kKStages) & 1u);
   } else if (warp == 11) {
     // ---------------------------------------------------------------- copies of V
     const bool gather = a.box < 4;
     const int n = gather ? 4 : a.box;                            // rows per copy
-    uint32_t it = 0, st = 0, ph = 0;
-    for (int left = 0;; ++it) {
-      if (left == 0) {
-        if (!tree_wait<true>(sh.t_full[st], ph, &sh.abort)) break;
-        if (sh.tile[st].g < 0) left = 2;                         // the end, for both pairs of V warps
-      } else if (--left == 0) {
-        break;
-      }
-      const int32_t g = sh.tile[st].g, piece = sh.tile[st].piece;
-      const int4 r4 = *reinterpret_cast<const int4 *>(&sh.tile[st].row[4 * (lane & 15)]);
+    uint32_t vt = 0, st = 0, ph = 1u, ts = 0, tph = 0;
+    bool going = true;
+    for (uint32_t it = 0; going; ++it) {
+      if (!tree_wait<true>(sh.t_full[ts], tph, &sh.abort)) break;
+      const int32_t g = sh.tile[ts].g, piece = sh.tile[ts].piece;
+      const int hc = g < 0 ? 2 : sh.tile[ts].hc;                 // the end, for both pairs of V warps
+      const int4 r4 = *reinterpret_cast<const int4 *>(&sh.tile[ts].row[4 * (lane & 15)]);
       const int32_t rows[4] = {r4.x, r4.y, r4.z, r4.w};
-      const int32_t row = sh.tile[st].row[lane];
-      if (!tree_wait<true>(sh.v8_free[st], ph ^ 1u, &sh.abort)) break;
-      const uint32_t bar = smem_u32(&sh.v8_full[st]);
-      if (lane == 0) sh.v8_piece[st] = left > 0 ? -1 : piece;
-      if (left > 0) {
-        tree_arrive(sh.v8_full[st]);
-      } else {
-        tree_arrive(sh.t_free[st]);
-        if (lane == 0) mbar_arrive_expect_tx(bar, L::kTile);
+      const int32_t row = sh.tile[ts].row[lane];
+      tree_arrive(sh.t_free[ts]);
+      if (++ts == kTreeStages) {
+        ts = 0;
+        tph ^= 1u;
+      }
+#pragma unroll 1
+      for (int j = 0; j < hc; ++j, ++vt) {
+        if (!(going = tree_wait<true>(sh.v8_free[st], ph, &sh.abort))) break;
+        const uint32_t bar = smem_u32(&sh.v8_full[st]);
+        if (lane == 0) {
+          sh.v8_piece[st] = g < 0 ? -1 : piece;
+          sh.v8_tile[st] = it;
+          if (g < 0) mbar_arrive(bar);
+          else mbar_arrive_expect_tx(bar, L::kTile);
+        }
         __syncwarp();
         const uint32_t dst = sbase + L::kV8 + st * L::kTile + lane * n * D;
-        if (gather) {
-          if (lane < 16) tma_gather4(dst, &tm_v, g * D, rows, bar);
+        if (g < 0) {
+        } else if (gather) {
+          if (lane < 16) tma_gather4(dst, &tm_v, (g + j) * D, rows, bar);
         } else if (lane < kTreeN / n) {
-          tma_load_2d(dst, &tm_v, g * D, row, bar);
+          tma_load_2d(dst, &tm_v, (g + j) * D, row, bar);
+        }
+        if (++st == kTreeStages) {
+          st = 0;
+          ph ^= 1u;
         }
       }
-      if (++st == kTreeStages) {
-        st = 0;
-        ph ^= 1u;
-      }
+      if (g < 0) break;
     }
-    for (uint32_t i = it < kTreeStages ? 0 : it - kTreeStages; i < it; ++i)
+    for (uint32_t i = vt < kTreeStages ? 0 : vt - kTreeStages; i < vt; ++i)
       wait_drain(smem_u32(&sh.v8_full[i % kTreeStages]), (i / kTreeStages) & 1u);
   } else if (warp == 10) {
     // ---------------------------------------------------------------- queries
@@ -708,19 +751,21 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     const uint32_t qflip = c < 0.0f ? 0x80808080u : 0u;          // a negative scale negates Q
     TreePiece pc;
     bool ok = true;
-    for (uint32_t ip = 0; ok && tree_take(sh, ip, pc); ++ip) {
-      // row r is head g G + r % G of node r / G; up to 32 (64) rows are repeated 4 (2) times down the
-      // tile.  The loads are on their way while the scores of the piece before complete.
-      const int step = pc.rows <= 32 ? 32 : (pc.rows <= 64 ? 64 : 128);
+    for (uint32_t ip = 0; ok && tree_take<M>(sh, ip, pc); ++ip) {
+      // A head's row r is query head g G + r % G of node r / G; the heads stand 32 or 64 rows apart, and
+      // what is left of the tile repeats them.  The loads are on their way while the scores of the
+      // piece before complete.
+      const int shift = tree_shift(pc.rows), span = kTreeM >> shift, step = M ? kTreeM : span;
 #pragma unroll 1
       for (int i0 = 0; i0 < step * LPR; i0 += 256) {
         uint4 v[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const int i = i0 + 32 * k + lane, r = i / LPR;
+          const int i = i0 + 32 * k + lane, vr = i / LPR, j = vr >> (7 - shift), r = vr & (span - 1);
           v[k] = make_uint4(0, 0, 0, 0);
-          if (r < pc.rows) {
-            const int idx = pc.row0 + r, node = a.by_group(idx), h = pc.g * G + (idx - node * G);
+          if (r < pc.rows && (!M || j < pc.hc)) {
+            const int idx = pc.row0 + r, node = a.by_group(idx);
+            const int h = (pc.g + j) * G + (idx - node * G);
             v[k] = *reinterpret_cast<const uint4 *>(a.q + (pc.first + node) * a.ldq + h * D +
                                                     i % LPR * 16);
           }
@@ -728,10 +773,10 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         if (i0 == 0 && !(ok = tree_wait<true>(sh.q_free, ip ^ 1u, &sh.abort))) break;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const int i = i0 + 32 * k + lane, r = i / LPR;
+          const int i = i0 + 32 * k + lane, vr = i / LPR;
           v[k].x ^= qflip; v[k].y ^= qflip; v[k].z ^= qflip; v[k].w ^= qflip;
-          for (int rr = r; r < step && rr < kTreeM; rr += step)
-            *reinterpret_cast<uint4 *>(smem + L::kQ + rr * 128 + ((i % LPR ^ (r & 7)) << 4)) = v[k];
+          for (int rr = vr; vr < step && rr < kTreeM; rr += step)
+            *reinterpret_cast<uint4 *>(smem + L::kQ + rr * 128 + ((i % LPR ^ (vr & 7)) << 4)) = v[k];
         }
       }
       fence_proxy_async_shared();
@@ -790,7 +835,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
               any |= n7;
               *x[q] &= ~((n7 >> 7) * 0xFFu);
             }
-            if (any && ((sh.valid[it & 7u] >> ((j + k) * RPS + r0)) & 1u))
+            if (any && ((sh.valid[sh.v8_tile[st] & 7u] >> ((j + k) * RPS + r0)) & 1u))
               atomicMax(&sh.nan_piece, piece);
           }
         }
@@ -819,7 +864,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       const bool leader = elect_one();
       const uint64_t qd = tree_sdesc_k<128>(sbase + L::kQ);
       uint32_t ip = 0;
-      int left = 0, same = 0, same_before = 0;                   // log2 of the K steps a lane group takes
+      // the piece's heads and the log2 of the heads or repeats in a row tile; those of the tile before
+      int left = 0, hc = 0, shift = 0, hc1 = 0, shift1 = 0;
       bool fresh = false, before = false;
       auto next = [&]() {                                        // the next tile, if there is one
         fresh = left == 0;
@@ -827,13 +873,14 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           const uint32_t i = ip % kTreePieces;
           if (!tree_wait<true>(sh.piece_full[i], ip / kTreePieces, &sh.abort)) return false;
           left = sh.piece[i].t_end - (sh.piece[i].t_end > 0 ? sh.piece[i].t : 0);
-          same = sh.piece[i].rows <= 32 ? 0 : (sh.piece[i].rows <= 64 ? 1 : 2);
+          hc = sh.piece[i].hc;
+          shift = tree_shift(sh.piece[i].rows);
           tree_arrive(sh.piece_free[i]);
           ++ip;
         }
         return left-- > 0;
       };
-      uint32_t st = 0, ph = 0;
+      uint32_t st = 0, ph = 0, vt = 0;
       bool live = next();
       // the scores of tile it, then the values of tile it - 1
 #pragma unroll 1
@@ -845,60 +892,74 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         for (int k = 0; k < 2 && ok; ++k) {
           if (fresh == (k == 1)) {
             if (!live) continue;
-            if ((fresh && !tree_wait<true>(sh.q_full, ip - 1, &sh.abort)) ||
-                !tree_wait<true>(sh.k_full[st], ph, &sh.abort)) {
-              ok = false;
-              continue;
-            }
-            tc_fence_after();
-            const uint64_t kd = tree_sdesc_k<D>(sbase + L::kK + st * L::kTile);
-            if (leader) {
+            if (fresh) ok = tree_wait<true>(sh.q_full, ip - 1, &sh.abort);
+#pragma unroll 1
+            for (int j = 0; j < (M ? hc : 1) && ok; ++j) {
+              if (!(ok = tree_wait<true>(sh.k_full[st], ph, &sh.abort))) break;
+              tc_fence_after();
+              const uint64_t kd = tree_sdesc_k<D>(sbase + L::kK + st * L::kTile);
+              uint32_t off[4];                                   // a head has its own lane groups
 #pragma unroll
-              for (int kk = 0; kk < D / 32; ++kk)
-                mma_f8f6f4(tmem + L::kColS + 64 * (it & 1u), qd + 2 * kk, kd + 2 * kk, L::kIdescQK,
-                           kk > 0 ? 1u : 0u);
-              mma_commit(smem_u32(&sh.s_full[it & 1u]));
-              mma_commit(smem_u32(&sh.k_free[st]));
-              if (left == 0) mma_commit(smem_u32(&sh.q_free));   // the piece's last scores
-            }
-            __syncwarp();
-            if (++st == kTreeStages) {
-              st = 0;
-              ph ^= 1u;
+              for (int q = 0; q < 4; ++q) off[q] = q >> (2 - shift) == j ? 0u : ~0u;
+              if (leader) {
+#pragma unroll
+                for (int kk = 0; kk < D / 32; ++kk) {
+                  const uint32_t at = tmem + L::kColS + 64 * (it & 1u), acc = kk > 0 ? 1u : 0u;
+                  if constexpr (M) mma_f8f6f4_lanes(at, qd + 2 * kk, kd + 2 * kk, L::kIdescQK, off, acc);
+                  else mma_f8f6f4(at, qd + 2 * kk, kd + 2 * kk, L::kIdescQK, acc);
+                }
+                mma_commit(smem_u32(&sh.k_free[st]));
+                if (!M || j + 1 == hc) {
+                  mma_commit(smem_u32(&sh.s_full[it & 1u]));
+                  if (left == 0) mma_commit(smem_u32(&sh.q_free));  // the piece's last scores
+                }
+              }
+              __syncwarp();
+              if (++st == kKStages) {
+                st = 0;
+                ph ^= 1u;
+              }
             }
           } else if (it > 0) {
-            const uint32_t i = (it - 1) & 1u, pp = (it - 1) >> 1;
-            if (!tree_wait<true>(sh.p_full[i], pp, &sh.abort) ||
-                !tree_wait<true>(sh.v_full[i], pp, &sh.abort)) {
-              ok = false;
-              continue;
-            }
-            tc_fence_after();
-            const uint64_t vd = tree_sdesc_v(sbase + L::kV16 + i * L::kV16Bytes);
-            // A lane group (32 rows) that holds a repeat has weights at its own positions only: the
-            // other K steps leave its values alone, and its first one writes them in a new piece.
-            const uint32_t pair = same_before > 0 ? 0u : ~0u, rest = same_before > 1 ? 0u : ~0u;
-            const uint32_t acc[4] = {before ? 0u : 1u, before && same_before == 0 ? 0u : 1u,
-                                     before && same_before < 2 ? 0u : 1u,
-                                     before && same_before == 0 ? 0u : 1u};
-            if (leader) {
+            const uint32_t buf = (it - 1) & 1u;
+            ok = tree_wait<true>(sh.p_full[buf], (it - 1) >> 1, &sh.abort);
+            // A lane group that holds a repeat has weights at its own positions only: the other K
+            // steps leave its values alone, and its first one writes them in a new piece.
+            const uint32_t pair = M || shift1 < 2 ? 0u : ~0u, rest = M || shift1 < 1 ? 0u : ~0u;
+            const uint32_t one = before ? 0u : 1u;
+            const uint32_t acc[4] = {one, M || shift1 < 2 ? 1u : one, M || shift1 < 1 ? 1u : one,
+                                     M || shift1 < 2 ? 1u : one};
+#pragma unroll 1
+            for (int j = 0; j < (M ? hc1 : 1) && ok; ++j, ++vt) {
+              const uint32_t i = vt & 1u;
+              if (!(ok = tree_wait<true>(sh.v_full[i], vt >> 1, &sh.abort))) break;
+              tc_fence_after();
+              const uint64_t vd = tree_sdesc_v(sbase + L::kV16 + i * L::kV16Bytes);
+              uint32_t other[4];
 #pragma unroll
-              for (int kk = 0; kk < kTreeN / 16; ++kk) {
-                uint32_t off[4];
+              for (int q = 0; q < 4; ++q) other[q] = !M || q >> (2 - shift1) == j ? 0u : ~0u;
+              if (leader) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) off[q] = q == kk ? 0u : (q / 2 == kk / 2 ? pair : rest);
-                mma_f16_ts(tmem + L::kColO, tmem + L::kColS + 64 * i + 8 * kk, vd + 128 * kk,
-                           L::kIdescPV, off, acc[kk]);
+                for (int kk = 0; kk < kTreeN / 16; ++kk) {
+                  uint32_t off[4];
+#pragma unroll
+                  for (int q = 0; q < 4; ++q)
+                    off[q] = q == kk ? other[q] : other[q] | (q / 2 == kk / 2 ? pair : rest);
+                  mma_f16_ts(tmem + L::kColO, tmem + L::kColS + 64 * buf + 8 * kk, vd + 128 * kk,
+                             L::kIdescPV, off, acc[kk]);
+                }
+                mma_commit(smem_u32(&sh.pv_done[i]));
+                if (!M || j + 1 == hc1) mma_commit(smem_u32(&sh.o_done[buf]));
               }
-              mma_commit(smem_u32(&sh.pv_done[i]));
+              __syncwarp();
             }
-            __syncwarp();
           }
         }
         if (!ok) break;
         if (!live) break;
         before = fresh;
-        same_before = same;
+        hc1 = hc;
+        shift1 = shift;
         live = next();
       }
       if (leader) {
@@ -917,26 +978,30 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     uint32_t it = 0;
     TreePiece pc;
     for (uint32_t ip = 0;; ++ip) {
-      bool ok = tree_take(sh, ip, pc);
-      const int shift = pc.rows <= 32 ? 2 : (pc.rows <= 64 ? 1 : 0), rep = 1 << shift;
-      const int w0 = warp & ((4 >> shift) - 1), r = 32 * w0 + lane, nc = kTreeN >> shift;
-      const uint32_t col0 = nc * (warp >> (2 - shift));
-      const bool live = r < pc.rows;
+      bool ok = tree_take<M>(sh, ip, pc);
+      // This thread's row of the tile: row r of head pc.g + j, with the columns from col0 on where the
+      // other lane groups of the row (rep > 1) hold the others.
+      const int span = 7 - tree_shift(pc.rows), csh = M ? 0 : 7 - span, rep = 1 << csh;
+      const int w0 = warp & ((4 >> csh) - 1), vr = 32 * w0 + lane, nc = kTreeN >> csh;
+      const uint32_t col0 = nc * (warp >> (2 - csh));
+      const int j = M ? vr >> span : 0, r = M ? vr & ((1 << span) - 1) : vr;
+      const bool live = r < pc.rows && (!M || j < pc.hc);
       const int node = a.by_group(pc.row0 + r);
       const int64_t *mrow = a.mask && live ? a.mask + (pc.first + node) * a.ldm : nullptr;
+      const float c2r = !M || live ? c2 : 0.0f;                  // rows without a head hold no scores
       TreeRow st{-INFINITY, 0.0f};
       for (int t = pc.t; t < pc.t_end && ok; ++t, ++it) {
-        ok = tree_tile<D>(sh, tw, col0, 4 >> shift, it, t == pc.t, mrow, words, live ? node : -1,
-                          t * kTreeN - pc.ctx, c2, st);
+        ok = tree_tile<D, M>(sh, tw, col0, 4 >> csh, it, t == pc.t, mrow, words, live ? node : -1,
+                          t * kTreeN - pc.ctx, c2r, st);
       }
-      ok = ok && tree_wait<true>(sh.pv_done[(it - 1) & 1u], (it - 1) >> 1, &sh.abort);
+      ok = ok && tree_wait<true>(sh.o_done[(it - 1) & 1u], (it - 1) >> 1, &sh.abort);
       sh.ml[warp][lane][0] = st.ref;
       sh.ml[warp][lane][1] = st.l;
       if (tree_any4(!ok)) break;                                 // no more pieces, or given up
       tc_fence_after();
       uint4 nan = make_uint4(0, 0, 0, 0);
       const bool any_nan = *reinterpret_cast<volatile int *>(&sh.nan_piece) > static_cast<int>(ip);
-      if (any_nan && live) nan = tree_nan_dims<D>(a, pc, node, col0, nc);
+      if (any_nan && live) nan = tree_nan_dims<D>(a, pc, pc.g + j, node, col0, nc);
       const bool whole = pc.t == 0 && pc.t_end == pc.nt;
       const int slot = pc.t > 0 ? 0 : 1;
       float *part = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * a.row_cap * (D + 2);
@@ -948,27 +1013,31 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           meta[3] = pc.row0;
           meta[4] = pc.rows;
           meta[5] = pc.g;
+          meta[6] = pc.hc;
+          meta[7] = span;
         }
       }
       // Repeats of a row hold different positions: their states are merged, then summed by rows, `rep`
       // threads per row and 16 / rep columns each.
       auto merged = [&](int w, int ln, float &l) {
-        float M = -INFINITY;
-        for (int i = w; i < 4; i += 4 >> shift) M = fmaxf(M, sh.ml[i][ln][0]);
+        float top = -INFINITY;
+        for (int i = w; i < 4; i += 4 >> csh) top = fmaxf(top, sh.ml[i][ln][0]);
         l = 0.0f;
-        for (int i = w; i < 4; i += 4 >> shift) {
+        for (int i = w; i < 4; i += 4 >> csh) {
           const float m = sh.ml[i][ln][0];
-          l += sh.ml[i][ln][1] * (m == M ? 1.0f : tree_ex2(m - M));
+          l += sh.ml[i][ln][1] * (m == top ? 1.0f : tree_ex2(m - top));
         }
-        return M;
+        return top;
       };
-      const int tr = tid >> shift, cpt = 16 >> shift, tc = (tid & (rep - 1)) * cpt;
+      const int tr = tid >> csh, cpt = 16 >> csh, tc = (tid & (rep - 1)) * cpt;
       float l;
-      const float mine_M = merged(w0, lane, l);
-      const float f = st.l == 0.0f ? 0.0f : (st.ref == mine_M ? 1.0f : tree_ex2(st.ref - mine_M));
-      const float M = merged(tr >> 5, tr & 31, l);
+      const float own = merged(w0, lane, l);                     // of the row whose values this lane holds
+      const float f = st.l == 0.0f ? 0.0f : (st.ref == own ? 1.0f : tree_ex2(st.ref - own));
+      const float ref = merged(tr >> 5, tr & 31, l);             // of the row that this thread writes
       const float scale = whole ? (l == 0.0f ? 0.0f : sv / l) : 1.0f;
-      const int idx = pc.row0 + tr, nd = a.by_group(idx), h = pc.g * G + (idx - nd * G);
+      const int tj = M ? j : 0, idx = pc.row0 + (M ? r : tr), nd = a.by_group(idx);
+      const bool there = M ? live : tr < pc.rows;
+      const int h = (pc.g + tj) * G + (idx - nd * G);
       uint16_t *out = a.out + (pc.first + nd) * a.ldo + h * D + tc;
       float *po = part + tr * D + tc;
       auto store4 = [&](int c, float4 v) {
@@ -1002,7 +1071,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
             if ((w >> (4 * j)) & 8u) v[j].w = NAN;
           }
         }
-        if (rep == 1) {
+        if (M || rep == 1) {
           if (live) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) store4(c + 4 * j, v[j]);
@@ -1012,7 +1081,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
 #pragma unroll
         for (int j = 0; j < 4; ++j) sh.o[warp][lane][j] = v[j];
         tree_sync4();
-        if (tr < pc.rows) {
+        if (there) {
           // four reads: four warps' columns, or two warps' twice as many
           float4 x[4];
 #pragma unroll
@@ -1032,9 +1101,9 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         }
         tree_sync4();
       }
-      if (!whole && tr < pc.rows && tc == 0) {
+      if (!whole && there && tc == 0) {
         float *ml = part + static_cast<int64_t>(a.row_cap) * D;
-        ml[2 * tr] = M;
+        ml[2 * tr] = ref;
         ml[2 * tr + 1] = l;
       }
       tc_fence_before();
@@ -1060,9 +1129,10 @@ __global__ void __launch_bounds__(256) k_tree_attn_combine(const TreeAttnArgs a)
   const int32_t *meta = a.meta + i * kTreeMetaInts;
   if (meta[1] == 0) return;
   const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (r >= meta[4]) return;
-  const int G = a.Hq / a.Hkv, idx = meta[3] + r, node = a.by_group(idx);
-  const int h = meta[5] * G + (idx - node * G);
+  const int head = r >> meta[7], row = r & ((1 << meta[7]) - 1);
+  if (row >= meta[4] || head >= meta[6]) return;
+  const int G = a.Hq / a.Hkv, idx = meta[3] + row, node = a.by_group(idx);
+  const int h = (meta[5] + head) * G + (idx - node * G);
   const int64_t slot = static_cast<int64_t>(a.row_cap) * (D + 2);
   const float *base = a.part + r * D + V * lane;
   const int64_t ml = static_cast<int64_t>(a.row_cap) * D + 2 * r;

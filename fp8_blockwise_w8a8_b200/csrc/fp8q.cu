@@ -424,7 +424,7 @@ bool tree_attn_heads(int64_t Hq, int64_t Hkv, int64_t max_nodes) {
 int64_t tree_attn_row_cap(int64_t Hq, int64_t Hkv, int64_t max_nodes) {
   const int64_t rows = max_nodes * (Hq / Hkv);
   if (rows > fp8q::kTreeM / 2 || tree_attn_heads(Hq, Hkv, max_nodes)) return fp8q::kTreeM;
-  return (rows + 1) / 2 * 2;  // even: 16-byte aligned slots
+  return (rows + 3) / 4 * 4;  // 16-byte aligned slots, whole groups of rows in the merge
 }
 
 // Per CTA: what its pieces are, and two partial states of row_cap rows.
@@ -1245,7 +1245,8 @@ int fp8q_attention_tree(const void *q_e4m3, int64_t ldq, const void *k_cache, co
   if ((rc = launch_status()) != FP8Q_OK) return rc;
   // the merge as a programmatic dependent launch: scheduled while the first kernel drains
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, static_cast<unsigned>((a.row_cap + 7) / 8));
+  constexpr int merge_rows = 8 * fp8q::kTreeMergeRows;
+  cfg.gridDim = dim3(grid, static_cast<unsigned>((a.row_cap + merge_rows - 1) / merge_rows));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];

@@ -1118,75 +1118,101 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   }
 }
 
-// The items that several CTAs shared: block (i, y) takes the rows 8 y .. 8 y + 7 of the item whose
-// first part is CTA i's last piece, and adds the parts in CTA order, each a running maximum's state.
+// The items that several CTAs shared: block (i, y) takes eight warps' rows of the item whose
+// first part is CTA i's last piece, and adds the parts in CTA order, each a
+// running maximum's state.
+constexpr int kTreeMergeRows = 1;  // 2 or 4 rows per warp: within 1 % on batches, 2 % slower on a long context
 template <int D>
 __global__ void __launch_bounds__(256) k_tree_attn_combine(const TreeAttnArgs a) {
-  constexpr int V = D / 32;
+  constexpr int V = D / 32, R = kTreeMergeRows;
   static_assert(V == 2 || V == 4, "vector loads of the parts");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int i = blockIdx.x;
+  const int i = blockIdx.x, lane = threadIdx.x & 31;
   const int32_t *meta = a.meta + i * kTreeMetaInts;
-  if (meta[1] == 0) return;
-  const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int head = r >> meta[7], row = r & ((1 << meta[7]) - 1);
-  if (row >= meta[4] || head >= meta[6]) return;
-  const int G = a.Hq / a.Hkv, idx = meta[3] + row, node = a.by_group(idx);
-  const int h = (meta[5] + head) * G + (idx - node * G);
+  const int4 m0 = *reinterpret_cast<const int4 *>(meta), m1 = *reinterpret_cast<const int4 *>(meta + 4);
+  if (m0.y == 0) return;
+  const int rows = m1.x, heads = m1.z, span = m1.w;
+  const int r0 = (blockIdx.y * 8 + (threadIdx.x >> 5)) * R;
   const int64_t slot = static_cast<int64_t>(a.row_cap) * (D + 2);
-  const float *base = a.part + r * D + V * lane;
-  const int64_t ml = static_cast<int64_t>(a.row_cap) * D + 2 * r;
-  float M = -INFINITY, l = 0.0f, o[V] = {};
-  auto add = [&](const float *p, float wk) {
-    alignas(16) float v[V];
-    if constexpr (V == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(p);
-    else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(p);
+  const float *base = a.part + r0 * D + V * lane;
+  const int64_t ml = static_cast<int64_t>(a.row_cap) * D + 2 * r0;
+  bool on[R], any = false;
 #pragma unroll
-    for (int k = 0; k < V; ++k) o[k] += v[k] * wk;
-  };
+  for (int q = 0; q < R; ++q) {
+    on[q] = ((r0 + q) & ((1 << span) - 1)) < rows && (r0 + q) >> span < heads;
+    any |= on[q];
+  }
+  if (!any) return;
+  float top[R], l[R], o[R][V];
+#pragma unroll
+  for (int q = 0; q < R; ++q) {
+    top[q] = -INFINITY;
+    l[q] = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) o[q][v] = 0.0f;
+  }
   // 32 parts at a time: their maxima and sums by lanes, then the values one after the other
   for (int j0 = i;; j0 += 32) {
     const int j = j0 + lane;
     const bool in = j < static_cast<int>(gridDim.x);
     const int kind = j == i ? 1 : (in ? a.meta[j * kTreeMetaInts] : 2);
     const uint32_t ends = __ballot_sync(0xffffffffu, kind != 1);
-    const int last = ends ? __ffs(ends) - 1 : 31, num = last + (in ? 1 : 0);
-    const int n = __shfl_sync(0xffffffffu, num, last);           // behind the grid: not a part
-    float m = -INFINITY, lj = 0.0f;
-    if (lane < n) {
-      const float *p = a.part + (2 * static_cast<int64_t>(j) + (j == i ? 1 : 0)) * slot + ml;
-      m = p[0];
-      lj = p[1];
-      if (lj == 0.0f) m = -INFINITY;
+    const int last = ends ? __ffs(ends) - 1 : 31;
+    const int n = __shfl_sync(0xffffffffu, last + (in ? 1 : 0), last);  // behind the grid: not a part
+    const float *p = a.part + (2 * static_cast<int64_t>(j) + (j == i ? 1 : 0)) * slot + ml;
+    float w[R];
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      float2 e = make_float2(-INFINITY, 0.0f);                   // maximum, sum
+      if (lane < n && on[q]) e = *reinterpret_cast<const float2 *>(p + 2 * q);
+      if (e.y == 0.0f) e.x = -INFINITY;
+      float m = e.x;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      m = fmaxf(m, top[q]);
+      // a part without weight has l = 0; a NaN sum stays one
+      w[q] = e.y == 0.0f ? 0.0f : (e.x == m ? 1.0f : tree_ex2(e.x - m));
+      const float keep = l[q] == 0.0f ? 0.0f : (top[q] == m ? 1.0f : tree_ex2(top[q] - m));
+      float sum = e.y * w[q];
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      l[q] = l[q] * keep + sum;
+      top[q] = m;
+#pragma unroll
+      for (int v = 0; v < V; ++v) o[q][v] *= keep;
     }
-    float top = m;
+#pragma unroll 2
+    for (int k = 0; k < n; ++k) {
+      const float *part = base + (2 * static_cast<int64_t>(j0 + k) + (j0 + k == i ? 1 : 0)) * slot;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    top = fmaxf(top, M);
-    // a part without weight has l = 0; a NaN sum stays one
-    const float w = lj == 0.0f ? 0.0f : (m == top ? 1.0f : tree_ex2(m - top));
-    const float keep = l == 0.0f ? 0.0f : (M == top ? 1.0f : tree_ex2(M - top));
-    float sum = lj * w;
+      for (int q = 0; q < R; ++q) {
+        const float wk = __shfl_sync(0xffffffffu, w[q], k);
+        if (!on[q]) continue;
+        alignas(16) float v[V];
+        if constexpr (V == 4)
+          *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(part + q * D);
+        else
+          *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(part + q * D);
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    l = l * keep + sum;
-#pragma unroll
-    for (int v = 0; v < V; ++v) o[v] *= keep;
-    M = top;
-    const int k0 = j0 == i ? 1 : 0;                              // part i is the CTA's second slot
-    if (k0) add(base + (2 * static_cast<int64_t>(i) + 1) * slot, __shfl_sync(0xffffffffu, w, 0));
-    const float *p = base + 2 * static_cast<int64_t>(j0 + k0) * slot;
-#pragma unroll 8
-    for (int k = k0; k < n; ++k, p += 2 * slot) add(p, __shfl_sync(0xffffffffu, w, k));
+        for (int x = 0; x < V; ++x) o[q][x] += v[x] * wk;
+      }
+    }
     if (ends) break;
   }
-  const float f = l == 0.0f ? 0.0f : a.scale3[2] / l;
-  uint16_t *out = a.out + (static_cast<int64_t>(meta[2]) + node) * a.ldo + h * D + V * lane;
+  const int G = a.Hq / a.Hkv;
 #pragma unroll
-  for (int v = 0; v < V; v += 2) {
-    const __nv_bfloat162 b2 = __floats2bfloat162_rn(l == 0.0f ? 0.0f : o[v] * f,
-                                                    l == 0.0f ? 0.0f : o[v + 1] * f);
-    *reinterpret_cast<uint32_t *>(out + v) = *reinterpret_cast<const uint32_t *>(&b2);
+  for (int q = 0; q < R; ++q) {
+    if (!on[q]) continue;
+    const int idx = m0.w + ((r0 + q) & ((1 << span) - 1)), node = a.by_group(idx);
+    const int h = (m1.y + ((r0 + q) >> span)) * G + (idx - node * G);
+    const float f = l[q] == 0.0f ? 0.0f : a.scale3[2] / l[q];
+    uint16_t *out = a.out + (static_cast<int64_t>(m0.z) + node) * a.ldo + h * D + V * lane;
+#pragma unroll
+    for (int v = 0; v < V; v += 2) {
+      const __nv_bfloat162 b2 = __floats2bfloat162_rn(l[q] == 0.0f ? 0.0f : o[q][v] * f,
+                                                      l[q] == 0.0f ? 0.0f : o[q][v + 1] * f);
+      *reinterpret_cast<uint32_t *>(out + v) = *reinterpret_cast<const uint32_t *>(&b2);
+    }
   }
 }
 

@@ -68,6 +68,12 @@ def test_tree_mask(L):
     _no_device(lambda: call(ctx=None, pos=None))
 
 
+def test_tree_mask_batch_limit(L):
+    call = lambda B: L.fp8q_tree_mask(FAKE, FAKE, None, B, 100, 64, FAKE, 1, None, None)
+    assert call(65536) == SHAPE
+    _no_device(lambda: call(65535))
+
+
 def test_attention_tree(L):
     q = L.fp8q_attention_tree_workspace_bytes
     b = ctypes.c_int64(-1)

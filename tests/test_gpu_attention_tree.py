@@ -232,6 +232,114 @@ def test_nan_codes_that_are_not_seen(Hq, Hkv, n):
     np.testing.assert_array_equal(got[~bad], same[~bad])
 
 
+# Small drafts over three or more kv heads: several heads share a row tile of the products.
+SHARED = [(3, 3, 20), (4, 4, 64), (10, 5, 16), (32, 8, 16), (32, 8, 7), (12, 4, 21), (40, 5, 8),
+          (7, 7, 1), (24, 3, 4)]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv,most", SHARED)
+def test_heads_that_share_a_row_tile(Hq, Hkv, most, D):
+    """Drafts from none to as many rows as half a tile holds, contexts from none to several tiles, long
+    enough in one sequence that its tiles are split between CTAs."""
+    nodes = [1, most, 0, max(1, most // 2), max(1, most - 1), min(3, most), 1]
+    d = _case(Hq, Hkv, D, nodes, [0, 1, 40, 63, 64, 3000, 200], 16, seed=70 + Hq + most)
+    o = fq.attention_tree(*_args(d))
+    assert fq.check_device_error() == 0
+    _check(o, d)
+
+
+@pytest.mark.parametrize("Hq,Hkv,n", [(8, 4, 9), (4, 4, 40), (6, 3, 30)])
+def test_shared_row_tiles_masks_nan_and_growing_scores(Hq, Hkv, n):
+    """The same with arbitrary masks and rows that see nothing, with NaN in places that only some rows
+    of some heads see, and with scores that grow along the positions."""
+    D, G = 128, Hq // Hkv
+    d = _case(Hq, Hkv, D, [n, 5], [0, 150], 16, seed=71 + n, kind="random")
+    d["sees"][0][n // 2] = False
+    o = fq.attention_tree(*_args(d))
+    assert fq.check_device_error() == 0
+    _check(o, d)
+    assert not host_bf16_f64(o)[n // 2].any()
+
+    d = _case(Hq, Hkv, D, [n, 5], [150, 0], 16, seed=72 + n)
+    d["sees"] = [np.eye(n, dtype=bool), np.eye(5, dtype=bool)]
+    slot = lambda b, p: d["table"][b, p // 16] * 16 + p % 16
+    held = {slot(0, p) for p in range(150 + n)} | {slot(1, p) for p in range(5)}
+    for s in set(range(len(d["k"]))) - held:
+        d["k"][s] = d["v"][s] = 0x7F
+    clean = dict(d, k=d["k"].copy(), v=d["v"].copy())
+    d["v"][slot(0, 152), (Hkv - 1) * D + 7] = 0xFF      # node 2: one dim of the last kv head
+    d["k"][slot(0, 154), D + 3] = 0x7F                  # node 4: key of kv head 1
+    got = host_bf16_f64(fq.attention_tree(*_args(d))).reshape(n + 5, Hq, D)
+    bad = np.zeros((n + 5, Hq, D), bool)
+    bad[2, (Hkv - 1) * G:, 7] = True
+    bad[4, G:2 * G] = True
+    np.testing.assert_array_equal(np.isnan(got), bad)
+    same = fq.attention_tree(*_args(clean))
+    _check(same, clean)
+    np.testing.assert_array_equal(got[~bad], host_bf16_f64(same).reshape(n + 5, Hq, D)[~bad])
+    assert fq.check_device_error() == 0
+
+    d = _case(Hq, Hkv, D, [n], [900], 16, seed=73 + n)
+    rng = np.random.default_rng(74)
+    L = 900 + n
+    ramp = np.linspace(0.02, 60.0, L)[:, None] * rng.uniform(0.5, 1.5, (L, Hkv * D))
+    enc = lambda x: (torch.from_numpy(x.astype(np.float32)).to(torch.float8_e4m3fn)
+                     .view(torch.uint8).numpy())
+    d["k"][d["table"][0][np.arange(L) // 16] * 16 + np.arange(L) % 16] = enc(ramp)
+    d["q"][0] = enc(rng.uniform(20, 60, (n, Hq * D)))
+    o = fq.attention_tree(*_args(d))
+    assert fq.check_device_error() == 0
+    _check(o, d)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(2, 1), (8, 4)])
+def test_cache_smaller_than_a_block(Hq, Hkv):
+    """No whole block: every id is out of range, nothing is seen, the results are 0."""
+    d = _case(Hq, Hkv, 64, [3, 1], [20, 0], 16, seed=75)
+    a = _args(d)
+    a[1], a[2] = a[1][:9].contiguous(), a[2][:9].contiguous()
+    o = fq.attention_tree(*a)
+    assert fq.check_device_error() == RANGE
+    assert not o.any()
+
+
+def test_offsets_that_fall_end_the_batch():
+    """The sequence whose offsets fall and all behind it have no rows, also where a later one would
+    name rows of an earlier one; a sequence with more nodes than max_seq_len has none either."""
+    d = _case(8, 2, 128, [4, 5, 6, 3], [100, 90, 80, 10], 16, seed=76)
+    for cu, whole in (([0, 4, 2, 3, 6], 1), ([0, 4, 9, 5, 15], 2), ([5, 4, 9, 15, 18], 0)):
+        a = _args(d)
+        a[6] = i32(cu)
+        out = torch.full((18, 8 * 128), 3.0, dtype=torch.bfloat16, device="cuda")
+        fq.attention_tree(*a, out=out)
+        assert fq.check_device_error() == RANGE
+        _check(out, d, seqs=range(whole))
+        assert (out[sum(d["nodes"][:whole]):] == 3.0).all()
+    a = _args(d)
+    a[12] = 5                                           # max_seq_len
+    out = torch.full((18, 8 * 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    fq.attention_tree(*a, out=out)
+    assert fq.check_device_error() == RANGE
+    assert (out[9:15] == 3.0).all() and not (out[:9] == 3.0).all(dim=1).any()
+
+
+def test_bound_on_nodes_above_the_drafts():
+    """One graph's bounds over small drafts: the same results to the tolerance as with tight bounds, for
+    a bound that takes the single-head form."""
+    d = _case(32, 8, 128, [3, 16, 1], [700, 20, 64], 16, seed=77)
+    a = _args(d)
+    tight = fq.attention_tree(*a)
+    d["max_nodes"], d["max_len"] = 200, 1 << 20
+    wide = np.full((3, (1 << 20) // 16), -1, np.int32)
+    wide[:, :d["table"].shape[1]] = d["table"]
+    b = _args(dict(d, table=wide))
+    o = fq.attention_tree(*b)
+    assert fq.check_device_error() == 0
+    _check(o, d)
+    _check(tight, d)
+
+
 def test_strided_and_padded_rows():
     """Leading dimensions wider than the rows, and a capacity beyond the last sequence: what lies
     outside the rows is neither read nor written."""

@@ -205,6 +205,59 @@ def test_mask_bad_parents_and_offsets():
     assert host(out)[:, 0].tolist() == [1, 3, -7, -7, -7, -7]
 
 
+def test_mask_offsets_that_fall_end_the_batch():
+    """Later sequences would name rows of an earlier one: nothing of theirs is written."""
+    par = [-1, 0, 1, 2, -1, 0, 0, -1, 0]
+    for cu, rows in (([0, 4, 2, 3, 6], 4), ([0, 3, 5, 4, 9], 5), ([4, 2, 9, 9, 9], 0)):
+        out = torch.full((9, 1), -7, dtype=torch.int64, device="cuda")
+        pos = torch.full((9,), -7, dtype=torch.int64, device="cuda")
+        fq.tree_mask(i32(par), i32(cu), 8, out_mask=out, out_positions=pos)
+        assert fq.check_device_error() == RANGE
+        assert (host(out)[rows:] == -7).all() and (host(pos)[rows:] == -7).all()
+        assert (host(out)[:rows] != -7).all()
+
+
+def test_mask_depths_of_long_trees():
+    """Positions of trees whose nodes' chains cross several words of the mask."""
+    rng = np.random.default_rng(9)
+    par = np.concatenate([np.arange(-1, 699), [rng.integers(max(0, i - 3), i) for i in range(700, 1024)]])
+    mask, pos = fq.tree_mask(i32(par), i32([0, 1024]), 1024, ctx_lens=i32([50]))
+    sees = spec.tree_sees(par)
+    np.testing.assert_array_equal(host(mask), spec.pack_bits(sees, 16))
+    np.testing.assert_array_equal(host(pos), 50 + sees.sum(1) - 1)
+    assert fq.check_device_error() == 0
+
+
+@pytest.mark.parametrize("cap", [151552, 151553, 400001])
+def test_tables_many_tokens(cap):
+    """Around and above the size from which a thread takes four tokens, with capacities that leave a
+    partial group at the end, an unaligned slot array among them."""
+    rng = np.random.default_rng(cap)
+    B, bs = 37, 24
+    new = rng.multinomial(cap - 5, rng.dirichlet(np.ones(B)))
+    ctx = rng.integers(0, 900, B)
+    ctx[3], new[7] = 0, 0
+    total = int(new.sum())
+    have, want = -(-ctx // bs), -(-(ctx + new) // bs)
+    perm = rng.permutation(int(want.sum())).astype(np.int32)
+    table = np.full((B, int(want.max())), -1, np.int32)
+    at = 0
+    for b in range(B):
+        table[b, :have[b]] = perm[at:at + have[b]]
+        at += have[b]
+    free = perm[at:]
+    ref = spec.batch_tables(ctx, new, table, bs, free, len(free), cap)
+    for skew in (0, 1):
+        slots = torch.empty(cap + skew, dtype=torch.int64, device="cuda")[skew:]
+        pos = torch.empty(cap, dtype=torch.int64, device="cuda")
+        bt = i32(table)
+        out = (i32(np.zeros(B + 1)), i32(np.zeros(B)), slots, pos, i32([0]))
+        fq.paged_batch_tables(i32(ctx), i32(new), bt, i32(free), i32([len(free)]), bs, cap, out=out)
+        for got, want_ in zip((bt, *out), ref):
+            np.testing.assert_array_equal(host(got), want_)
+    assert total <= cap and fq.check_device_error() == 0
+
+
 # --- accepted rows --------------------------------------------------------------------------------
 
 def _accept_case(B, bs, row, layers, seed, n_hi=20, path_hi=12):

@@ -7,6 +7,35 @@
 //   z_j = sm_scale s_q s_k sum_d dec(q[i][h][d]) dec(k_j[g][d])
 //   o[i][h][d] = s_v * sum_j softmax(z)_j dec(v_j[g][d])   -> bf16,   g = h / (Hq / Hkv)
 // A node that sees nothing gets zeros.
+//
+// Products on the tensor cores, accumulators in TMEM.  A row tile is 128 query rows (node, head of the
+// group); a position tile is 64 cached positions of one kv head.  Scores: kind::f8f6f4 on the codes as
+// they are.  Weights: fp16 (at most 2^-11 off, half the bound of bf16 results), written over the scores
+// in TMEM as the next product's A operand; V is converted to fp16, which is exact.  The softmax keeps a
+// reference that lags the running maximum by at most 2^8, so that the accumulators are rescaled rarely.
+//
+// Few rows leave most of a row tile idle.  Where every draft's rows of one kv head fit into half of it
+// and there are three heads or more (M), two or four heads share the tile: each has its own lane
+// groups of 32 or 64 rows, and the products of a head's K and V leave the other lanes alone (the MMAs'
+// lane mask).  Else up to 32 (64) rows are repeated four (two) times, each repeat with its own 16 (32)
+// of a tile's positions, merged at the end.  Measured, 64 sequences of 512 to 4096 positions with up to
+// 16 nodes, heads of 128 in groups of 4: 96 us with shared tiles, 102 with repeats; 40 sequences, 16
+// heads of 64 without groups: 64 against 75.
+//
+// Work is split evenly whatever the lengths: all items (sequence, heads, row tile) stand one behind the
+// other on one axis of position tiles, two CTAs per SM take equal shares of it, and what CTAs share of
+// an item is merged by a second kernel in CTA order, so that results do not depend on timing.
+//
+// Roles of a CTA's twelve warps: 0-3 softmax and output, 4-7 V codes to fp16, 8 MMAs, 9 K by TMA (a
+// copy per run of positions in a block; gathers of four rows for odd block sizes), 10 queries, 11 V by
+// TMA.  Every wait is bounded.
+//
+// Measured (calls back to back, new inputs every time): 64 sequences as above 94 us, 3.4 TB/s of cache
+// and 52 % of the copy rate; one sequence of 131501 positions with 61 nodes 193 us, 681 TFLOP/s; 8 of
+// up to 512 nodes over up to 6000 positions 340 us, 695 TFLOP/s.  What bounds it is the issue of the
+// roles' instructions and the hand-offs between them (0.43 to 0.56 instructions per cycle and
+// scheduler), with the tensor pipe at 27 to 32 %.  The roles' code has to stay small: at 170 KB
+// instruction fetch was the largest stall and everything took twice as long.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>

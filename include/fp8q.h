@@ -406,10 +406,12 @@ int fp8q_tree_mask(const int32_t *parents, const int32_t *cu_nodes, const int32_
  * D is 64 or 128, Hq a multiple of Hkv with Hq / Hkv <= 128, num_slots <= 2^31 - 1, B <= 65535; q and
  * out 16-byte aligned with ldq % 16 == 0, ldo % 8 == 0.  Results within
  * |out - ref| <= ulp_bf16(|ref|)/2 + absref * (2^-11 + 2 (D + 2) 2^-24 zabs + (L + 16) 2^-23)
- * of the fp64 reference, as fp8q_attention_decode (absref, zabs over the positions seen, L their
- * number).  Recorded as FP8Q_ERR_RANGE: offsets as in fp8q_tree_mask; a context that is negative or
- * makes ctx + nodes exceed max_seq_len (clamped); a block id outside [0, num_slots / block_size)
- * (its positions are not seen). */
+ * + L 2^-32 * 448 s_v of the fp64 reference (absref, zabs over the positions seen, L their number): the
+ * bound of fp8q_attention_decode, and half a step of the smallest fp16 weight at each position.
+ * Results do not depend on timing.  Recorded as FP8Q_ERR_RANGE: offsets as in fp8q_tree_mask; a context
+ * that is negative or makes ctx + nodes exceed max_seq_len (clamped; a sequence with more nodes than
+ * max_seq_len has no rows); a block id outside [0, num_slots / block_size) (its positions are not
+ * seen).  Two launches; bounds (max_nodes, max_seq_len) that fit the batch are faster. */
 int fp8q_attention_tree(const void *q_e4m3, int64_t ldq, const void *k_cache, const void *v_cache,
                         int64_t num_slots, const float *scale3, const int32_t *block_table,
                         int64_t max_blocks, const int32_t *ctx_lens, const int32_t *cu_nodes,

@@ -11,6 +11,14 @@ library or a non-sm_100 device raises.
     gemm_w8a8_block(aq, sa, wq, sw, fmt)       -> bf16 [M, N]
     gemm_w8a8_block_splitk(aq, sa, wq, sw, ...) -> bf16 [M, N], K split over CTAs (small M)
     grouped_gemm_w8a8_block(aq, sa, wq, sw, offsets, fmt) -> bf16 [M, N]
+
+A speculative-decoding step over the paged FP8 KV cache, in the order of its calls:
+
+    paged_batch_tables(ctx, new, table, ...)   slots and positions of the drafted tokens
+    tree_mask(parents, cu, max_nodes)          ancestor bits, rotary positions
+    kv_cache_write(qkv, ..., slots, ...)       their K and V into the cache
+    attention_tree(q, k_cache, v_cache, ...)   -> bf16 [total, Hq * D]
+    kv_cache_accept(k_cache, v_cache, ...)     accepted rows up, new context lengths
 """
 import numpy as np
 import torch

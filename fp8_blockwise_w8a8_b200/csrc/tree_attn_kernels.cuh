@@ -393,19 +393,6 @@ struct TreeRow {
   float ref, l;                  // reference of the weights (log2 units), their sum
 };
 
-// Sixteen scores of this thread's row from TMEM; where not all are seen, those that are not (bit 0 on)
-// become -inf.
-__device__ __forceinline__ void tree_scores(uint32_t taddr, bool all, uint64_t seen,
-                                            uint32_t (&sr)[16]) {
-  tree_ld<16>(taddr, sr);
-  if (!all) {
-    const uint32_t bits = static_cast<uint32_t>(seen);
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if (!((bits >> j) & 1)) sr[j] = 0xFF800000u;
-  }
-}
-
 // One position tile: the scores of 16 * chunks columns of this thread's row become weights, in the
 // first half of the score buffer's columns: 8 columns per chunk, behind those already read.  The first
 // chunk's scores stay in registers between the maximum and the weights, the others are read again.
@@ -421,19 +408,28 @@ __device__ __forceinline__ bool tree_tile(TreeShared<M> &sh, uint32_t tmem, uint
   const uint32_t buf = tmem + L::kColS + 64 * (it & 1u);
   uint32_t sr[16];
   uint64_t seen = sh.valid[it & 7u];
-  const bool all = j0 <= -kTreeN && seen == ~0ull;               // within the context, all there
-  if (!all) {
-    // a row that does not exist counts as seeing all (its results are unused)
+  if (j0 > -kTreeN || seen != ~0ull) {                           // not within the context, or not whole
+    // what is not seen becomes -inf in TMEM; a row that does not exist counts as seeing all
     if (node >= 0) seen &= tree_bits(mrow, words, node, j0);
     seen >>= col0;
-    __syncwarp();                                                // whole warps at the TMEM loads
+#pragma unroll 1
+    for (int c = 0; c < 16 * chunks; c += 16, seen >>= 16) {
+      __syncwarp();                                              // whole warps at the TMEM loads
+      tree_ld<16>(buf + col0 + c, sr);
+      const uint32_t bits = static_cast<uint32_t>(seen);
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (!((bits >> j) & 1)) sr[j] = 0xFF800000u;
+      tree_st<16>(buf + col0 + c, sr);
+    }
+    tmem_st_wait();
   }
   float mx[2] = {-INFINITY, -INFINITY};
   int c = chunks;
 #pragma unroll 1
   do {
     --c;
-    tree_scores(buf + col0 + 16 * c, all, seen >> (16 * c), sr);
+    tree_ld<16>(buf + col0 + 16 * c, sr);
 #pragma unroll
     for (int j = 0; j < 16; ++j) mx[j & 1] = fmaxf(mx[j & 1], __uint_as_float(sr[j]));
   } while (c > 0);
@@ -473,7 +469,7 @@ __device__ __forceinline__ bool tree_tile(TreeShared<M> &sh, uint32_t tmem, uint
     }
     tree_st<8>(buf + col0 / 2 + 8 * c, pk);
     if (++c >= chunks) break;
-    tree_scores(buf + col0 + 16 * c, all, seen >> (16 * c), sr);
+    tree_ld<16>(buf + col0 + 16 * c, sr);
   }
   st.l += sum.x + sum.y;
   tmem_st_wait();

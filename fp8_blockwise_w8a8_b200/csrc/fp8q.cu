@@ -41,12 +41,6 @@ std::mutex g_mu;
 DeviceState g_dev[kMaxDevices];
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
-template <int D, bool M>
-bool tree_attn_attr() {
-  return cudaFuncSetAttribute(fp8q::k_tree_attn<D, M>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              fp8q::TreeLayout<D, M>::kSmem) == cudaSuccess;
-}
-
 int device_state(DeviceState **out) {
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FP8Q_ERR_ARCH;
@@ -127,8 +121,10 @@ int device_state(DeviceState **out) {
                              kTablesMaxSmem) != cudaSuccess ||
         cudaFuncSetAttribute(fp8q::k_paged_tables<4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kTablesMaxSmem) != cudaSuccess ||
-        !tree_attn_attr<128, false>() || !tree_attn_attr<128, true>() ||
-        !tree_attn_attr<64, false>() || !tree_attn_attr<64, true>())
+        cudaFuncSetAttribute(fp8q::k_tree_attn<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             fp8q::TreeLayout<128>::kSmem) != cudaSuccess ||
+        cudaFuncSetAttribute(fp8q::k_tree_attn<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             fp8q::TreeLayout<64>::kSmem) != cudaSuccess)
       return FP8Q_ERR_LAUNCH;
     st.attrs_set = true;
   }
@@ -414,17 +410,10 @@ int64_t tree_attn_ctas(int64_t B, int64_t Hq, int64_t Hkv, int64_t max_nodes,
   return most < fp8q::kTreeMaxCtas ? most : fp8q::kTreeMaxCtas;
 }
 
-// Whether several kv heads share a row tile: where every sequence's rows of one head fit into half of
-// it, and there are heads to fill it.
-bool tree_attn_heads(int64_t Hq, int64_t Hkv, int64_t max_nodes) {
-  return Hkv > 2 && max_nodes * (Hq / Hkv) <= fp8q::kTreeM / 2;
-}
-
-// Rows of a partial state: a row tile, or the rows that repeat in it.
+// Rows of a partial state.
 int64_t tree_attn_row_cap(int64_t Hq, int64_t Hkv, int64_t max_nodes) {
   const int64_t rows = max_nodes * (Hq / Hkv);
-  if (rows > fp8q::kTreeM / 2 || tree_attn_heads(Hq, Hkv, max_nodes)) return fp8q::kTreeM;
-  return (rows + 3) / 4 * 4;  // 16-byte aligned slots, whole groups of rows in the merge
+  return rows < fp8q::kTreeM ? (rows + 3) / 4 * 4 : fp8q::kTreeM;  // 16-byte aligned slots
 }
 
 // Per CTA: what its pieces are, and two partial states of row_cap rows.
@@ -435,13 +424,6 @@ int64_t tree_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
          (4 * fp8q::kTreeMetaInts + 8 * tree_attn_row_cap(Hq, Hkv, max_nodes) * (D + 2));
 }
 
-
-template <int D, bool M>
-void tree_attn_launch(unsigned grid, cudaStream_t stream, const CUtensorMap &tm_k,
-                      const CUtensorMap &tm_v, const fp8q::TreeAttnArgs &a) {
-  fp8q::k_tree_attn<D, M><<<grid, fp8q::kTreeThreads, fp8q::TreeLayout<D, M>::kSmem, stream>>>(
-      tm_k, tm_v, a);
-}
 
 int attn_shape_status(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t block_size,
                       int64_t max_seq_len) {
@@ -1222,31 +1204,25 @@ int fp8q_attention_tree(const void *q_e4m3, int64_t ldq, const void *k_cache, co
   const int64_t pow2 = block_size & -block_size;
   a.box = static_cast<int>(pow2 > 64 ? 64 : pow2);
   const uint32_t box = a.box < 4 ? 1 : static_cast<uint32_t>(a.box);
-  const bool heads = tree_attn_heads(Hq, Hkv, max_nodes);
-  a.log_hkv = 0;
-  while (heads && (int64_t{1} << a.log_hkv) < Hkv) ++a.log_hkv;
   a.by_block = tree_div(block_size);
   a.by_group = tree_div(Hq / Hkv);
   // a cache without slots: every position is out of range and loads row 0, here of q
-  const void *k_rows = num_slots > 0 ? k_cache : q_e4m3, *v_rows = num_slots > 0 ? v_cache : q_e4m3;
-  const int64_t map_rows = num_slots > 0 ? num_slots : 1;
-  CUtensorMap tm_k, tm_v;
+  CUtensorMap tm_k;
   if ((rc = get_encoder()) != FP8Q_OK ||
-      (rc = make_u8_row_map(&tm_k, k_rows, map_rows, Hkv * D, box, static_cast<uint32_t>(D),
+      (rc = make_u8_row_map(&tm_k, num_slots > 0 ? k_cache : q_e4m3, num_slots > 0 ? num_slots : 1,
+                            Hkv * D, box, static_cast<uint32_t>(D),
                             D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B)) !=
-          FP8Q_OK ||
-      (rc = make_u8_row_map(&tm_v, v_rows, map_rows, Hkv * D, box, static_cast<uint32_t>(D),
-                            CU_TENSOR_MAP_SWIZZLE_NONE)) != FP8Q_OK)
+          FP8Q_OK)
     return rc;
-  if (D == 128 && heads) tree_attn_launch<128, true>(grid, stream, tm_k, tm_v, a);
-  else if (D == 128) tree_attn_launch<128, false>(grid, stream, tm_k, tm_v, a);
-  else if (heads) tree_attn_launch<64, true>(grid, stream, tm_k, tm_v, a);
-  else tree_attn_launch<64, false>(grid, stream, tm_k, tm_v, a);
+  if (D == 128)
+    fp8q::k_tree_attn<128><<<grid, fp8q::kTreeThreads, fp8q::TreeLayout<128>::kSmem, stream>>>(tm_k,
+                                                                                               a);
+  else
+    fp8q::k_tree_attn<64><<<grid, fp8q::kTreeThreads, fp8q::TreeLayout<64>::kSmem, stream>>>(tm_k, a);
   if ((rc = launch_status()) != FP8Q_OK) return rc;
   // the merge as a programmatic dependent launch: scheduled while the first kernel drains
   cudaLaunchConfig_t cfg = {};
-  constexpr int merge_rows = 8 * fp8q::kTreeMergeRows;
-  cfg.gridDim = dim3(grid, static_cast<unsigned>((a.row_cap + merge_rows - 1) / merge_rows));
+  cfg.gridDim = dim3(grid, static_cast<unsigned>((a.row_cap + 7) / 8));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];

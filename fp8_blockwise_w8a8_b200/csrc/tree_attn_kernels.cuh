@@ -7,35 +7,6 @@
 //   z_j = sm_scale s_q s_k sum_d dec(q[i][h][d]) dec(k_j[g][d])
 //   o[i][h][d] = s_v * sum_j softmax(z)_j dec(v_j[g][d])   -> bf16,   g = h / (Hq / Hkv)
 // A node that sees nothing gets zeros.
-//
-// Products on the tensor cores, accumulators in TMEM.  A row tile is 128 query rows (node, head of the
-// group); a position tile is 64 cached positions of one kv head.  Scores: kind::f8f6f4 on the codes as
-// they are.  Weights: fp16 (at most 2^-11 off, half the bound of bf16 results), written over the scores
-// in TMEM as the next product's A operand; V is converted to fp16, which is exact.  The softmax keeps a
-// reference that lags the running maximum by at most 2^8, so that the accumulators are rescaled rarely.
-//
-// Few rows leave most of a row tile idle.  Where every draft's rows of one kv head fit into half of it
-// and there are three heads or more (M), two or four heads share the tile: each has its own lane
-// groups of 32 or 64 rows, and the products of a head's K and V leave the other lanes alone (the MMAs'
-// lane mask).  Else up to 32 (64) rows are repeated four (two) times, each repeat with its own 16 (32)
-// of a tile's positions, merged at the end.  Measured, 64 sequences of 512 to 4096 positions with up to
-// 16 nodes, heads of 128 in groups of 4: 96 us with shared tiles, 102 with repeats; 40 sequences, 16
-// heads of 64 without groups: 64 against 75.
-//
-// Work is split evenly whatever the lengths: all items (sequence, heads, row tile) stand one behind the
-// other on one axis of position tiles, two CTAs per SM take equal shares of it, and what CTAs share of
-// an item is merged by a second kernel in CTA order, so that results do not depend on timing.
-//
-// Roles of a CTA's twelve warps: 0-3 softmax and output, 4-7 V codes to fp16, 8 MMAs, 9 K by TMA (a
-// copy per run of positions in a block; gathers of four rows for odd block sizes), 10 queries, 11 V by
-// TMA.  Every wait is bounded.
-//
-// Measured (calls back to back, new inputs every time): 64 sequences as above 94 us, 3.4 TB/s of cache
-// and 52 % of the copy rate; one sequence of 131501 positions with 61 nodes 193 us, 681 TFLOP/s; 8 of
-// up to 512 nodes over up to 6000 positions 340 us, 695 TFLOP/s.  What bounds it is the issue of the
-// roles' instructions and the hand-offs between them (0.43 to 0.56 instructions per cycle and
-// scheduler), with the tensor pipe at 27 to 32 %.  The roles' code has to stay small: at 170 KB
-// instruction fetch was the largest stall and everything took twice as long.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -71,7 +42,6 @@ struct TreeAttnArgs {
   float sm_scale;
   uint16_t *out;               // [total][ldo] bf16
   int64_t ldo;
-  int log_hkv;                 // ceil(log2(Hkv))
   int box;                     // rows per copy: the power of two in block_size, at most 64; 1: gathers
   uint64_t grid_recip;         // floor((2^64 - 1) / gridDim.x)
   TreeDiv by_block, by_group;  // by block_size and by G = Hq / Hkv
@@ -106,25 +76,24 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeAttnArgs &a, int b, bool r
 // ---------------------------------------------------------------------------------------------
 constexpr int kTreeM = 128;          // query rows (node, head of the group) per row tile: TMEM lanes
 constexpr int kTreeN = 64;           // cached positions per tile
-constexpr int kTreeThreads = 384;    // 4 softmax warps, 4 convert V, one each: MMAs, K, Q, copies of V
+constexpr int kTreeThreads = 352;    // 4 softmax warps, 4 for V, one each for the MMAs, K and Q
 constexpr int kTreeMaxCtas = 296;    // 2 per SM of 148
-constexpr int kTreeStages = 3;       // V tiles (codes) in shared memory, position tiles known ahead
+constexpr int kTreeStages = 4;       // K tiles in shared memory
 constexpr int kTreeItemCost = 4;     // cost of starting a row tile, in position tiles
 constexpr int kTreeMinCost = 4;      // least cost per CTA
 constexpr int kTreeMetaInts = 8;
 constexpr float kTreeLag = 8.0f;     // the reference lags the running maximum by at most 2^8
 constexpr float kTreeBias = 7.0f;    // weights are 2^(z - reference + 7): at most 2^15 in fp16
 
-template <int D, bool M>
+template <int D>
 struct TreeLayout {
-  static constexpr int kKStages = M ? 4 : 3;                     // K tiles (codes) in shared memory
   static constexpr int kQ = 0;                                   // [128][128 B], swizzled
   static constexpr int kK = kQ + kTreeM * 128;                   // [stage][64][D], swizzled
   static constexpr int kTile = kTreeN * D;
-  static constexpr int kV16 = kK + kKStages * kTile;          // [2][D / 64][64][128 B], swizzled
+  static constexpr int kV16 = kK + kTreeStages * kTile;          // [2][D / 64][64][128 B], swizzled
   static constexpr int kV16Bytes = kTreeN * D * 2;
-  static constexpr int kV8 = kV16 + 2 * kV16Bytes;               // [stage][64][D]
-  static constexpr int kSmem = kV8 + kTreeStages * kTile + 1024;
+  static constexpr int kV8 = kV16 + 2 * kV16Bytes;               // [pair of V warps][64][D]
+  static constexpr int kSmem = kV8 + 2 * kTile + 1024;
   // TMEM columns: two score buffers, whose first halves then hold the weights (two fp16 a column),
   // and the values
   static constexpr int kColS = 0, kColO = 128, kCols = 256;
@@ -144,60 +113,47 @@ __device__ __forceinline__ int tree_tiles(const TreeAttnArgs &a, const TreeSeq &
   const int last = a.by_group(min(s.n * G, (rt + 1) * kTreeM) - 1);  // the tile's last node
   return (s.ctx + last) / kTreeN + 1;
 }
-// Log2 of the repeats of up to 32 (64) rows in a row tile of 128.
-__device__ __forceinline__ int tree_shift(int rows) { return rows <= 32 ? 2 : (rows <= 64 ? 1 : 0); }
-// Log2 of the kv heads that share a row tile (log_hkv > 0): as many as fit, 32 or 64 rows each.
-__device__ __forceinline__ int tree_heads(const TreeAttnArgs &a, const TreeSeq &s, int G) {
-  return min(tree_shift(s.n * G), a.log_hkv);
-}
-// Position tiles of all heads, and kTreeItemCost for each item (row tile of a group of heads).
-__device__ __forceinline__ int64_t tree_seq_cost(const TreeAttnArgs &a, const TreeSeq &s, int G) {
-  const int groups = (a.Hkv + (1 << tree_heads(a, s, G)) - 1) >> tree_heads(a, s, G);
+__device__ __forceinline__ int64_t tree_group_cost(const TreeAttnArgs &a, const TreeSeq &s, int G) {
   int64_t c = 0;
 #pragma unroll 1
   for (int rt = tree_row_tiles(s.n, G) - 1; rt >= 0; --rt)
-    c += static_cast<int64_t>(tree_tiles(a, s, G, rt)) * a.Hkv + groups * kTreeItemCost;
+    c += tree_tiles(a, s, G, rt) + kTreeItemCost;
   return c;
 }
 
-// A share of one item (sequence, heads g .. g + hc - 1, row tile): its position tiles [t, t_end) of
-// nt.  The load warp hands the pieces of a CTA to the other roles, the last one with t_end = 0.
+// A share of one item (sequence, kv head, row tile): its position tiles [t, t_end) of nt.  The load
+// warp hands the pieces of a CTA to the other roles, the last one with t_end = 0.
 struct TreePiece {
   int64_t first;                 // row of the sequence's node 0
-  int b, n, ctx, g, hc, hsh, row0, rows, t, t_end, nt;
+  int b, n, ctx, g, row0, rows, t, t_end, nt;
 };
 
 // The pieces of work of one CTA: a range of the cost axis on which the items stand one behind the
-// other, each as long as its position tiles times its heads plus kTreeItemCost.
+// other, each as long as its position tiles plus kTreeItemCost.
 struct TreeCursor {
   TreeSeq s;
   int64_t rem;
-  int B, b, g, hsh, rt, t, t_end, nt;
+  int B, b, g, rt, t, t_end, nt;
   bool live;
 
-  __device__ __forceinline__ int heads(const TreeAttnArgs &a) const {
-    return min(1 << hsh, a.Hkv - g);
-  }
   // From the sequence b0, `off` behind its start; cost 0: nothing.
   __device__ __forceinline__ void init(const TreeAttnArgs &a, int G, int num, int b0, int64_t off,
                                        int64_t cost) {
     B = num;
     rem = cost;
     b = b0;
-    g = rt = t = t_end = hsh = 0;
+    g = rt = t = t_end = 0;
     live = cost > 0;
     if (!live) return;
     s = tree_seq(a, b, false);
-    hsh = tree_heads(a, s, G);
-    // the group of heads and the item that hold the offset
-    int64_t per = 0;
-#pragma unroll 1
-    for (int i = tree_row_tiles(s.n, G) - 1; i >= 0; --i)
-      per += static_cast<int64_t>(tree_tiles(a, s, G, i) << hsh) + kTreeItemCost;
-    for (; off >= per && g + (1 << hsh) < a.Hkv; g += 1 << hsh) off -= per;
-    int c;
-    while (off >= (c = tree_tiles(a, s, G, rt) * heads(a) + kTreeItemCost)) {
-      off -= c;
+    const int64_t per_g = tree_group_cost(a, s, G);
+    while (off >= per_g) {
+      off -= per_g;
+      ++g;
+    }
+    int tiles;
+    while (off >= (tiles = tree_tiles(a, s, G, rt) + kTreeItemCost)) {
+      off -= tiles;
       ++rt;
     }
     --rt;
@@ -212,8 +168,7 @@ struct TreeCursor {
       }
       if (++rt == tree_row_tiles(s.n, G)) {
         rt = 0;
-        g += 1 << hsh;
-        if (g >= a.Hkv) {
+        if (++g == a.Hkv) {
           g = 0;
           do {
             if (++b >= B) {
@@ -222,14 +177,12 @@ struct TreeCursor {
             }
             s = tree_seq(a, b, false);
           } while (s.n == 0);
-          hsh = tree_heads(a, s, G);
         }
       }
       nt = tree_tiles(a, s, G, rt);
-      const int w = heads(a);                                    // nt * w < 2^28
-      const int take = static_cast<int>(min(static_cast<int64_t>(nt * w + kTreeItemCost - off), rem));
-      t = max(0, off - kTreeItemCost) / w;
-      t_end = max(0, off + take - kTreeItemCost) / w;
+      const int64_t take = min(static_cast<int64_t>(nt + kTreeItemCost - off), rem);
+      t = max(0, off - kTreeItemCost);
+      t_end = max(0, off + static_cast<int>(take) - kTreeItemCost);
       rem -= take;
       off = 0;
     } while (t >= t_end);
@@ -277,28 +230,32 @@ __device__ __forceinline__ uint64_t tree_sdesc_k(uint32_t saddr) {
          (static_cast<uint64_t>(B == 128 ? 2 : 4) << 61);
 }
 
-// Bounded waits by a warp and by one thread, short in code: 2^20 polls of a microsecond at most, then
-// the CTA's abort flag is raised (it becomes the recorded timeout at the end) and the role gives up;
-// those that wait for it do the same in their turn.
-template <bool WARP>
-__device__ __forceinline__ bool tree_wait(const uint64_t &barrier, uint32_t parity, int *abort_flag) {
+// Bounded waits by a warp and by one thread, short in code: about 2^20 polls of a microsecond at most,
+// then the timeout is recorded and the CTA's roles give up.
+__device__ __forceinline__ bool tree_poll(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-      "mov.u32 n, 0;\n"
-      "TREE_POLL_%=:\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
-      "@p bra TREE_DONE_%=;\n\t"
-      "add.u32 n, n, 1;\n\t"
-      "setp.lt.u32 q, n, 1048576;\n\t"
-      "@q bra TREE_POLL_%=;\n"
-      "TREE_DONE_%=:\n\t"
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(smem_u32(&barrier)), "r"(parity & 1u)
+      : "r"(bar), "r"(parity), "r"(1000u)
       : "memory");
-  if (WARP ? __all_sync(0xffffffffu, ok) : ok) return true;
-  *const_cast<volatile int *>(abort_flag) = 1;
+  return ok != 0;
+}
+constexpr uint32_t kTreePolls = 1u << 20;
+template <bool WARP>
+__device__ __forceinline__ bool tree_wait(const uint64_t &barrier, uint32_t parity,
+                                          volatile int *abort_flag) {
+  const uint32_t bar = smem_u32(&barrier);
+#pragma unroll 1
+  for (uint32_t n = 0;; ++n) {
+    const bool ok = tree_poll(bar, parity & 1u);
+    if (WARP ? __all_sync(0xffffffffu, ok) : ok) return true;
+    const bool stop = *abort_flag != 0 || n >= kTreePolls;
+    if (WARP ? __any_sync(0xffffffffu, stop) : stop) break;
+  }
+  if (atomicExch(const_cast<int *>(abort_flag), 1) == 0) record_error(6 /* FP8Q_ERR_TIMEOUT */);
   return false;
 }
 // The calling warp's share of an arrival.
@@ -323,21 +280,17 @@ __device__ __forceinline__ void tree_st(uint32_t taddr, const uint32_t (&r)[N]) 
 
 // What the CTA's roles share.
 constexpr int kTreePieces = 4;   // descriptors in the ring
-struct TreeTile {                // a position tile, for the copies of V
-  alignas(16) int32_t row[kTreeN];   // first cache row of each copy, or each position's row
-  int32_t g, hc, piece;          // first kv head (-1: no more tiles), heads, 1 + index of the piece
+struct TreeTile {                // for the V warps
+  int32_t slot[kTreeN];          // cache rows of the tile's positions, -1 where there is none
+  int32_t g, piece;              // kv head (-1: no more tiles), 1 + index of the piece
 };
-template <bool M>
 struct TreeShared {
-  uint64_t k_full[M ? 4 : 3], k_free[M ? 4 : 3], t_full[kTreeStages], t_free[kTreeStages];
-  uint64_t v8_full[kTreeStages], v8_free[kTreeStages];
+  uint64_t k_full[kTreeStages], k_free[kTreeStages], t_full[kTreeStages], t_free[kTreeStages];
   uint64_t piece_full[kTreePieces], piece_free[kTreePieces];
-  uint64_t q_full, q_free, v_full[2], s_full[2], p_full[2], pv_done[2], o_done[2], drain;
+  uint64_t q_full, q_free, v_full[2], s_full[2], p_full[2], pv_done[2], drain;
   uint64_t valid[8];             // per tile (mod 8): the positions that exist, one bit each
   TreePiece piece[kTreePieces];
   TreeTile tile[kTreeStages];
-  int32_t v8_piece[kTreeStages]; // 1 + index of the stage's piece, -1: no more tiles
-  uint32_t v8_tile[kTreeStages]; // index of its position tile
   int start_b;
   int64_t start_off;
   int64_t warp_sum[kTreeThreads / 32];
@@ -345,12 +298,11 @@ struct TreeShared {
   int abort;
   int nan_piece;                 // 1 + index of the last piece with a NaN code in V
   float ml[4][32][2];
-  float4 o[4][M ? 1 : 32][5];    // 16 columns, rows 80 bytes apart
+  float4 o[4][32][5];            // 16 columns, rows 80 bytes apart
 };
 
 // The next piece of the ring for the calling warp; false where there is none.
-template <bool M>
-__device__ __forceinline__ bool tree_take(TreeShared<M> &sh, uint32_t ip, TreePiece &pc) {
+__device__ __forceinline__ bool tree_take(TreeShared &sh, uint32_t ip, TreePiece &pc) {
   const uint32_t i = ip % kTreePieces;
   pc.t = pc.t_end = 0;
   if (!tree_wait<true>(sh.piece_full[i], ip / kTreePieces, &sh.abort)) return false;
@@ -362,7 +314,7 @@ __device__ __forceinline__ bool tree_take(TreeShared<M> &sh, uint32_t ip, TreePi
 // The dims of kv head g that are NaN in a value row seen by row (node i) among the positions of
 // [t, t_end) whose column within its tile lies in [c0, c0 + nc).  Runs only where V holds NaN codes.
 template <int D>
-__device__ __noinline__ uint4 tree_nan_dims(const TreeAttnArgs &a, TreePiece c, int g, int i, int c0,
+__device__ __noinline__ uint4 tree_nan_dims(const TreeAttnArgs &a, TreePiece c, int i, int c0,
                                             int nc) {
   uint32_t dims[4] = {};
   const int words = (a.max_nodes + 63) / 64;
@@ -375,7 +327,7 @@ __device__ __noinline__ uint4 tree_nan_dims(const TreeAttnArgs &a, TreePiece c, 
       const int32_t blk = a.block_table[c.b * a.max_blocks + a.by_block(pos)];
       if (blk < 0 || blk >= a.num_blocks) continue;
       const int64_t slot = static_cast<int64_t>(blk) * a.block_size + pos % a.block_size;
-      const uint32_t *v = reinterpret_cast<const uint32_t *>(a.v_cache + (slot * a.Hkv + g) * D);
+      const uint32_t *v = reinterpret_cast<const uint32_t *>(a.v_cache + (slot * a.Hkv + c.g) * D);
       for (int w = 0; w < D / 32; ++w)
 #pragma unroll 1
         for (int x = 0; x < 8; ++x) {
@@ -393,43 +345,37 @@ struct TreeRow {
   float ref, l;                  // reference of the weights (log2 units), their sum
 };
 
+// Sixteen scores of this thread's row from TMEM; what is not seen (bit 0 on) becomes -inf.
+__device__ __forceinline__ void tree_scores(uint32_t taddr, uint64_t seen, uint32_t (&sr)[16]) {
+  tree_ld<16>(taddr, sr);
+  const uint32_t bits = static_cast<uint32_t>(seen) & 0xFFFFu;
+  if (!__all_sync(0xffffffffu, bits == 0xFFFFu)) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (!((bits >> j) & 1)) sr[j] = 0xFF800000u;
+  }
+}
+
 // One position tile: the scores of 16 * chunks columns of this thread's row become weights, in the
 // first half of the score buffer's columns: 8 columns per chunk, behind those already read.  The first
 // chunk's scores stay in registers between the maximum and the weights, the others are read again.
-// Loops over short bodies: the roles' code together has to stay in the instruction caches.  j0: the
-// tile's first position, counted from node 0.
-template <int D, bool M>
-__device__ __forceinline__ bool tree_tile(TreeShared<M> &sh, uint32_t tmem, uint32_t col0, int chunks,
-                                          uint32_t it, bool first, const int64_t *mrow, int words,
-                                          int node, int j0, float c2, TreeRow &st) {
-  using L = TreeLayout<D, M>;
+// Loops over short bodies: the roles' code together has to stay in the instruction caches.
+template <int D>
+__device__ __forceinline__ bool tree_tile(TreeShared &sh, uint32_t tmem, uint32_t col0, int chunks,
+                                          uint32_t it, bool first, uint64_t seen, float c2,
+                                          TreeRow &st) {
+  using L = TreeLayout<D>;
   if (!tree_wait<true>(sh.s_full[it & 1u], it >> 1, &sh.abort)) return false;
   tc_fence_after();
   const uint32_t buf = tmem + L::kColS + 64 * (it & 1u);
   uint32_t sr[16];
-  uint64_t seen = sh.valid[it & 7u];
-  if (j0 > -kTreeN || seen != ~0ull) {                           // not within the context, or not whole
-    // what is not seen becomes -inf in TMEM; a row that does not exist counts as seeing all
-    if (node >= 0) seen &= tree_bits(mrow, words, node, j0);
-    seen >>= col0;
-#pragma unroll 1
-    for (int c = 0; c < 16 * chunks; c += 16, seen >>= 16) {
-      __syncwarp();                                              // whole warps at the TMEM loads
-      tree_ld<16>(buf + col0 + c, sr);
-      const uint32_t bits = static_cast<uint32_t>(seen);
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (!((bits >> j) & 1)) sr[j] = 0xFF800000u;
-      tree_st<16>(buf + col0 + c, sr);
-    }
-    tmem_st_wait();
-  }
+  seen = (seen & sh.valid[it & 7u]) >> col0;
   float mx[2] = {-INFINITY, -INFINITY};
   int c = chunks;
 #pragma unroll 1
   do {
     --c;
-    tree_ld<16>(buf + col0 + 16 * c, sr);
+    tree_scores(buf + col0 + 16 * c, seen >> (16 * c), sr);
 #pragma unroll
     for (int j = 0; j < 16; ++j) mx[j & 1] = fmaxf(mx[j & 1], __uint_as_float(sr[j]));
   } while (c > 0);
@@ -441,7 +387,7 @@ __device__ __forceinline__ bool tree_tile(TreeShared<M> &sh, uint32_t tmem, uint
     st.ref = up ? top : st.ref;
     st.l *= f;
     if (!first && __any_sync(0xffffffffu, held)) {
-      if (!tree_wait<true>(sh.o_done[(it - 1) & 1u], (it - 1) >> 1, &sh.abort)) return false;
+      if (!tree_wait<true>(sh.pv_done[(it - 1) & 1u], (it - 1) >> 1, &sh.abort)) return false;
       tc_fence_after();
 #pragma unroll 1
       for (int d = 0; d < D; d += 16) {
@@ -469,7 +415,13 @@ __device__ __forceinline__ bool tree_tile(TreeShared<M> &sh, uint32_t tmem, uint
     }
     tree_st<8>(buf + col0 / 2 + 8 * c, pk);
     if (++c >= chunks) break;
-    tree_ld<16>(buf + col0 + 16 * c, sr);
+    tree_scores(buf + col0 + 16 * c, seen >> (16 * c), sr);
+  }
+  // a repeat of a row has no weight at the other repeats' positions
+#pragma unroll 1
+  for (int i = 8 * chunks; i < 32; i += 8) {
+    const uint32_t z[8] = {};
+    tree_st<8>(buf + ((col0 / 2 + i) & 31u), z);
   }
   st.l += sum.x + sum.y;
   tmem_st_wait();
@@ -498,29 +450,24 @@ __device__ __forceinline__ bool tree_any4(bool v) {
   return r != 0;
 }
 
-template <int D, bool M>
+template <int D>
 __global__ void __launch_bounds__(kTreeThreads, 2)
-    k_tree_attn(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+    k_tree_attn(const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ TreeAttnArgs a) {
-  using L = TreeLayout<D, M>;
-  constexpr int kKStages = L::kKStages;
+  using L = TreeLayout<D>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ TreeShared<M> sh;
+  __shared__ TreeShared sh;
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.Hq / a.Hkv;
 
   if (tid == 0) {
-    for (int i = 0; i < kKStages; ++i) {
+    for (int i = 0; i < kTreeStages; ++i) {
       mbar_init(smem_u32(&sh.k_full[i]), 1);
       mbar_init(smem_u32(&sh.k_free[i]), 1);
-    }
-    for (int i = 0; i < kTreeStages; ++i) {
       mbar_init(smem_u32(&sh.t_full[i]), 1);
-      mbar_init(smem_u32(&sh.t_free[i]), 1);
-      mbar_init(smem_u32(&sh.v8_full[i]), 1);
-      mbar_init(smem_u32(&sh.v8_free[i]), 2);
+      mbar_init(smem_u32(&sh.t_free[i]), 2);
     }
     for (int i = 0; i < kTreePieces; ++i) {
       mbar_init(smem_u32(&sh.piece_full[i]), 1);
@@ -533,18 +480,12 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       mbar_init(smem_u32(&sh.p_full[i]), 4);
       mbar_init(smem_u32(&sh.pv_done[i]), 1);
       mbar_init(smem_u32(&sh.s_full[i]), 1);
-      mbar_init(smem_u32(&sh.o_done[i]), 1);
     }
     mbar_init(smem_u32(&sh.drain), 1);
     sh.abort = 0;
     sh.nan_piece = 0;
     fence_barrier_init();
   }
-  if (warp == 8) {
-    tmem_alloc(smem_u32(&sh.tmem), L::kCols);
-    tmem_relinquish();
-  }
-
   // This CTA's range of the cost axis: every CTA adds up all sequences' costs itself.  Offsets that
   // decrease end the batch before that sequence, so that no two sequences write the same rows.
   const int per = (a.B + kTreeThreads - 1) / kTreeThreads;
@@ -555,7 +496,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     bool falls = false;
     for (int b = tid * per; b < min(B, (tid + 1) * per); ++b) {
       falls |= a.cu[b + 1] < a.cu[b];
-      mine += tree_seq_cost(a, tree_seq(a, b, blockIdx.x == 0), G);
+      mine += tree_group_cost(a, tree_seq(a, b, blockIdx.x == 0), G) * a.Hkv;
     }
     upto = mine;
 #pragma unroll
@@ -564,6 +505,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       if (lane >= d) upto += y;
     }
     if (lane == 31) sh.warp_sum[warp] = upto;
+    __syncwarp();                                                // whole warps at every barrier
     if (!__syncthreads_or(falls) || again) break;
     if (tid == 0) sh.start_b = a.B;
     __syncthreads();
@@ -572,6 +514,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         atomicMin(&sh.start_b, b);
         break;
       }
+    __syncwarp();
     __syncthreads();
     B = sh.start_b;
     __syncthreads();
@@ -592,12 +535,18 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     int64_t off = lo - (upto - mine);
     int b = tid * per;
     for (;; ++b) {
-      const int64_t c = tree_seq_cost(a, tree_seq(a, b, false), G);
+      const int64_t c = tree_group_cost(a, tree_seq(a, b, false), G) * a.Hkv;
       if (off < c) break;
       off -= c;
     }
     sh.start_b = b;
     sh.start_off = off;
+  }
+  __syncwarp();
+  // only now that every warp of the CTA has started
+  if (warp == 8) {
+    tmem_alloc(smem_u32(&sh.tmem), L::kCols);
+    tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
@@ -612,7 +561,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     TreeCursor pre;
     pre.init(a, G, B, sh.start_b, sh.start_off, hi - lo);
     const bool gather = a.box < 4;
-    const int chunks = kTreeN / a.box;
+    const int chunks = kTreeN / a.box, log_box = __ffs(a.box) - 1;
     const int first = gather ? lane : min(lane, chunks - 1) * a.box;
     int blk[2], off[2];
     auto look_up = [&]() {                                       // block ids of the cursor's tile
@@ -638,8 +587,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       const uint32_t i = ip % kTreePieces;
       if (!tree_wait<true>(sh.piece_free[i], (ip / kTreePieces) ^ 1u, &sh.abort)) return false;
       if (lane == 0)
-        sh.piece[i] = TreePiece{pre.s.first, pre.b, pre.s.n, pre.s.ctx, pre.g, pre.heads(a), pre.hsh,
-                                pre.rt * kTreeM,
+        sh.piece[i] = TreePiece{pre.s.first, pre.b, pre.s.n, pre.s.ctx, pre.g, pre.rt * kTreeM,
                                 min(kTreeM, pre.s.n * G - pre.rt * kTreeM), pre.t,
                                 pre.live ? pre.t_end : 0, pre.nt};
       tree_arrive(sh.piece_full[i]);
@@ -647,14 +595,15 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       return true;
     };
     look_up();
-    // position tiles (it; ts, tph: stage and phase of their rows), tiles of single heads (kt; st, ph)
-    uint32_t it = 0, ts = 0, tph = 1u, kt = 0, st = 0, ph = 1u;
-    bool fresh = true, going = true;
-    for (; going; ++it) {
+    uint32_t it = 0, st = 0, ph = 1u;
+    bool fresh = true;
+    for (;; ++it) {
       if (fresh && !publish()) break;
       if (!pre.live) break;
       // the stage first: the block ids are on their way meanwhile
-      if (!tree_wait<true>(sh.t_free[ts], tph, &sh.abort)) break;
+      if (!tree_wait<true>(sh.k_free[st], ph, &sh.abort) ||
+          !tree_wait<true>(sh.t_free[st], ph, &sh.abort))
+        break;
       bool ok;
       int32_t slot[2] = {slot_of(0, &ok), 0};
       uint64_t there;
@@ -663,112 +612,65 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         slot[1] = slot_of(1, &ok);
         there |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, ok)) << 32;
       } else {
+        const uint64_t bits = ok ? (a.box == 64 ? ~0ull : ((1ull << a.box) - 1) << first) : 0ull;
+        there = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(bits));
+        there |= static_cast<uint64_t>(
+                     __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(bits >> 32))) << 32;
         const int left = pre.s.ctx + pre.s.n - pre.t * kTreeN;   // positions that exist
-        there = ~0ull;
-        if (left < 64 || !__all_sync(0xffffffffu, ok)) {
-          const uint64_t bits = ok ? (a.box == 64 ? ~0ull : ((1ull << a.box) - 1) << first) : 0ull;
-          there = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(bits));
-          there |= static_cast<uint64_t>(
-                       __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(bits >> 32))) << 32;
-          if (left < 64) there &= (1ull << left) - 1;
-        }
+        if (left < 64) there &= (1ull << left) - 1;
       }
-      const int hc = M ? pre.heads(a) : 1;
+      const uint32_t bar = smem_u32(&sh.k_full[st]);
       if (lane == 0) {
         sh.valid[it & 7u] = there;
-        sh.tile[ts].g = pre.g;
-        sh.tile[ts].hc = hc;
-        sh.tile[ts].piece = static_cast<int>(ip);
+        sh.tile[st].g = pre.g;
+        sh.tile[st].piece = static_cast<int>(ip);
+        mbar_arrive_expect_tx(bar, L::kTile);
       }
-      sh.tile[ts].row[lane] = slot[0];
-      sh.tile[ts].row[32 + lane] = slot[1];
-      tree_arrive(sh.t_full[ts]);
-      int32_t rows[4];
+      __syncwarp();
+      const uint32_t dst = sbase + L::kK + st * L::kTile;
       if (gather) {
+        int32_t rows[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int32_t v0 = __shfl_sync(0xffffffffu, slot[0], (4 * lane + r) & 31);
           const int32_t v1 = __shfl_sync(0xffffffffu, slot[1], (4 * lane + r) & 31);
           rows[r] = lane & 8 ? v1 : v0;
         }
-      }
-#pragma unroll 1
-      for (int j = 0; j < hc; ++j, ++kt) {
-        if (!(going = tree_wait<true>(sh.k_free[st], ph, &sh.abort))) break;
-        const uint32_t bar = smem_u32(&sh.k_full[st]), dst = sbase + L::kK + st * L::kTile;
-        const int x = (pre.g + j) * D;
-        if (lane == 0) mbar_arrive_expect_tx(bar, L::kTile);
-        __syncwarp();
-        if (gather) {
-          if (lane < 16) tma_gather4(dst + 4 * D * lane, &tm_k, x, rows, bar);
-        } else if (lane < chunks) {
-          tma_load_2d(dst + lane * a.box * D, &tm_k, x, slot[0], bar);
-        }
-        if (++st == kKStages) {
-          st = 0;
-          ph ^= 1u;
+        if (lane < 16) tma_gather4(dst + 4 * D * lane, &tm_k, pre.g * D, rows, bar);
+      } else {
+        if (lane < chunks) tma_load_2d(dst + lane * a.box * D, &tm_k, pre.g * D, slot[0], bar);
+        const int32_t row = slot[0];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int p = 32 * j + lane;
+          slot[j] = __shfl_sync(0xffffffffu, row, p >> log_box) + (p & (a.box - 1));
         }
       }
-      if (++ts == kTreeStages) {
-        ts = 0;
-        tph ^= 1u;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        sh.tile[st].slot[32 * j + lane] = (there >> (32 * j + lane)) & 1u ? slot[j] : -1;
+      tree_arrive(sh.t_full[st]);
+      if (++st == kTreeStages) {
+        st = 0;
+        ph ^= 1u;
       }
       fresh = ++pre.t >= pre.t_end;
       if (fresh) pre.next(a, G, 0);
       look_up();
     }
-    if (tree_wait<true>(sh.t_free[ts], tph, &sh.abort)) {        // the end
-      if (lane == 0) sh.tile[ts].g = -1;
-      tree_arrive(sh.t_full[ts]);
+    // the end, for both pairs of V warps
+    for (int i = 0; i < 2; ++i) {
+      if (!tree_wait<true>(sh.t_free[st], ph, &sh.abort)) break;
+      if (lane == 0) sh.tile[st].g = -1;
+      tree_arrive(sh.t_full[st]);
+      if (++st == kTreeStages) {
+        st = 0;
+        ph ^= 1u;
+      }
     }
     // after a wait that gave up: no copy in flight at exit
-    for (uint32_t i = kt < kKStages ? 0 : kt - kKStages; i < kt; ++i)
-      wait_drain(smem_u32(&sh.k_full[i % kKStages]), (i / kKStages) & 1u);
-  } else if (warp == 11) {
-    // ---------------------------------------------------------------- copies of V
-    const bool gather = a.box < 4;
-    const int n = gather ? 4 : a.box;                            // rows per copy
-    uint32_t vt = 0, st = 0, ph = 1u, ts = 0, tph = 0;
-    bool going = true;
-    for (uint32_t it = 0; going; ++it) {
-      if (!tree_wait<true>(sh.t_full[ts], tph, &sh.abort)) break;
-      const int32_t g = sh.tile[ts].g, piece = sh.tile[ts].piece;
-      const int hc = g < 0 ? 2 : sh.tile[ts].hc;                 // the end, for both pairs of V warps
-      const int4 r4 = *reinterpret_cast<const int4 *>(&sh.tile[ts].row[4 * (lane & 15)]);
-      const int32_t rows[4] = {r4.x, r4.y, r4.z, r4.w};
-      const int32_t row = sh.tile[ts].row[lane];
-      tree_arrive(sh.t_free[ts]);
-      if (++ts == kTreeStages) {
-        ts = 0;
-        tph ^= 1u;
-      }
-#pragma unroll 1
-      for (int j = 0; j < hc; ++j, ++vt) {
-        if (!(going = tree_wait<true>(sh.v8_free[st], ph, &sh.abort))) break;
-        const uint32_t bar = smem_u32(&sh.v8_full[st]);
-        if (lane == 0) {
-          sh.v8_piece[st] = g < 0 ? -1 : piece;
-          sh.v8_tile[st] = it;
-          if (g < 0) mbar_arrive(bar);
-          else mbar_arrive_expect_tx(bar, L::kTile);
-        }
-        __syncwarp();
-        const uint32_t dst = sbase + L::kV8 + st * L::kTile + lane * n * D;
-        if (g < 0) {
-        } else if (gather) {
-          if (lane < 16) tma_gather4(dst, &tm_v, (g + j) * D, rows, bar);
-        } else if (lane < kTreeN / n) {
-          tma_load_2d(dst, &tm_v, (g + j) * D, row, bar);
-        }
-        if (++st == kTreeStages) {
-          st = 0;
-          ph ^= 1u;
-        }
-      }
-      if (g < 0) break;
-    }
-    for (uint32_t i = vt < kTreeStages ? 0 : vt - kTreeStages; i < vt; ++i)
-      wait_drain(smem_u32(&sh.v8_full[i % kTreeStages]), (i / kTreeStages) & 1u);
+    for (uint32_t i = it < kTreeStages ? 0 : it - kTreeStages; i < it; ++i)
+      tree_wait<true>(sh.k_full[i % kTreeStages], i / kTreeStages, &sh.abort);
   } else if (warp == 10) {
     // ---------------------------------------------------------------- queries
     constexpr int LPR = D / 16;                                  // 16-byte chunks per row
@@ -776,21 +678,19 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     const uint32_t qflip = c < 0.0f ? 0x80808080u : 0u;          // a negative scale negates Q
     TreePiece pc;
     bool ok = true;
-    for (uint32_t ip = 0; ok && tree_take<M>(sh, ip, pc); ++ip) {
-      // A head's row r is query head g G + r % G of node r / G; the heads stand 32 or 64 rows apart, and
-      // what is left of the tile repeats them.  The loads are on their way while the scores of the
-      // piece before complete.
-      const int shift = tree_shift(pc.rows), span = kTreeM >> shift, step = M ? kTreeM : span;
+    for (uint32_t ip = 0; ok && tree_take(sh, ip, pc); ++ip) {
+      // row r is head g G + r % G of node r / G; up to 32 (64) rows are repeated 4 (2) times down the
+      // tile.  The loads are on their way while the scores of the piece before complete.
+      const int step = pc.rows <= 32 ? 32 : (pc.rows <= 64 ? 64 : 128);
 #pragma unroll 1
       for (int i0 = 0; i0 < step * LPR; i0 += 256) {
         uint4 v[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const int i = i0 + 32 * k + lane, vr = i / LPR, j = vr >> (7 - shift), r = vr & (span - 1);
+          const int i = i0 + 32 * k + lane, r = i / LPR;
           v[k] = make_uint4(0, 0, 0, 0);
-          if (r < pc.rows && (!M || j < pc.hc)) {
-            const int idx = pc.row0 + r, node = a.by_group(idx);
-            const int h = (pc.g + j) * G + (idx - node * G);
+          if (r < pc.rows) {
+            const int idx = pc.row0 + r, node = a.by_group(idx), h = pc.g * G + (idx - node * G);
             v[k] = *reinterpret_cast<const uint4 *>(a.q + (pc.first + node) * a.ldq + h * D +
                                                     i % LPR * 16);
           }
@@ -798,10 +698,10 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         if (i0 == 0 && !(ok = tree_wait<true>(sh.q_free, ip ^ 1u, &sh.abort))) break;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const int i = i0 + 32 * k + lane, vr = i / LPR;
+          const int i = i0 + 32 * k + lane, r = i / LPR;
           v[k].x ^= qflip; v[k].y ^= qflip; v[k].z ^= qflip; v[k].w ^= qflip;
-          for (int rr = vr; vr < step && rr < kTreeM; rr += step)
-            *reinterpret_cast<uint4 *>(smem + L::kQ + rr * 128 + ((i % LPR ^ (vr & 7)) << 4)) = v[k];
+          for (int rr = r; r < step && rr < kTreeM; rr += step)
+            *reinterpret_cast<uint4 *>(smem + L::kQ + rr * 128 + ((i % LPR ^ (r & 7)) << 4)) = v[k];
         }
       }
       fence_proxy_async_shared();
@@ -817,95 +717,75 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     const int pair = (warp - 4) >> 1, gt = tid - 128 - 64 * pair;
     const int ch = D == 128 ? (gt & 3) | (gt >> 1 & 4) : gt & 3;
     const int r0 = D == 128 ? (gt >> 2 & 1) | (gt >> 4 << 1) : gt >> 2;
-    uint32_t st = pair, ph = 0;
+    const int64_t row = static_cast<int64_t>(a.Hkv) * D;
+    const uint32_t stage = sbase + L::kV8 + pair * L::kTile + gt * 16;
     for (uint32_t it = pair;; it += 2) {
-      if (!tree_wait<true>(sh.v8_full[st], ph, &sh.abort)) break;
-      const int32_t piece = sh.v8_piece[st];
-      if (piece < 0) break;
+      const uint32_t st = it % kTreeStages;
+      if (!tree_wait<true>(sh.t_full[st], it / kTreeStages, &sh.abort)) break;
+      const TreeTile &tile = sh.tile[st];
+      const int32_t g = tile.g, piece = tile.piece;
+      if (g < 0) break;
+      // each thread copies and converts 16 codes of every step's row
+      const uint8_t *col = a.v_cache + g * D + ch * 16;
+#pragma unroll 2
+      for (int j = 0; j < NR; ++j) {
+        const int32_t slot = tile.slot[j * RPS + r0];
+        cp_async16(stage + j * 1024, col + static_cast<int64_t>(max(slot, 0)) * row,
+                   slot >= 0 ? 16u : 0u);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      tree_arrive(sh.t_free[st]);
       if (it >= 2 && !tree_wait<true>(sh.pv_done[pair], (it - 2) >> 1, &sh.abort)) break;
-      const uint8_t *src = smem + L::kV8 + st * L::kTile + r0 * D + ch * 16;
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
       uint8_t *dst = smem + L::kV16 + pair * L::kV16Bytes + (ch >> 2) * 8192 + r0 * 128;
       const int at0 = ((ch & 3) * 2 ^ (r0 & 7)) << 4;            // RPS is a multiple of 8
 #pragma unroll 1
-      for (int j = 0; j < NR; j += 2) {
-        uint4 v8[2];
-        uint32_t h[16];
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          v8[k] = *reinterpret_cast<const uint4 *>(src + (j + k) * RPS * D);
+      for (int j = 0; j < NR; ++j) {
+        uint4 v8 = *reinterpret_cast<const uint4 *>(smem + (stage - sbase) + j * 1024);
+        uint32_t h[8];
         while (true) {
-          const uint32_t w[8] = {v8[0].x, v8[0].y, v8[0].z, v8[0].w,
-                                 v8[1].x, v8[1].y, v8[1].z, v8[1].w};
-          __half2 m[8];
+          const uint32_t w[4] = {v8.x, v8.y, v8.z, v8.w};
+          __half2 acc = __half2half2(__ushort_as_half(0));
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            h[2 * k] = e4m3x2_to_f16x2(w[k] & 0xFFFFu);
-            h[2 * k + 1] = e4m3x2_to_f16x2(w[k] >> 16);
-            m[k] = __hmax2_nan(*reinterpret_cast<const __half2 *>(&h[2 * k]),
-                               *reinterpret_cast<const __half2 *>(&h[2 * k + 1]));
+            h[k] = e4m3x2_to_f16x2(k & 1 ? w[k / 2] >> 16 : w[k / 2] & 0xFFFFu);
+            acc = __hmax2_nan(acc, *reinterpret_cast<const __half2 *>(&h[k]));
           }
-#pragma unroll
-          for (int d = 4; d > 0; d /= 2)
-#pragma unroll
-            for (int k = 0; k < d; ++k) m[k] = __hmax2_nan(m[k], m[k + d]);
-          if (!__hisnan(__low2half(m[0])) && !__hisnan(__high2half(m[0]))) break;
+          if (!__hisnan(__low2half(acc)) && !__hisnan(__high2half(acc))) break;
           // A NaN code becomes 0; it is put back into the results of the rows that see it.
+          uint32_t *x[4] = {&v8.x, &v8.y, &v8.z, &v8.w};
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint32_t *x[4] = {&v8[k].x, &v8[k].y, &v8[k].z, &v8[k].w};
-            uint32_t any = 0;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t n7 = ((*x[q] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-              any |= n7;
-              *x[q] &= ~((n7 >> 7) * 0xFFu);
-            }
-            if (any && ((sh.valid[sh.v8_tile[st] & 7u] >> ((j + k) * RPS + r0)) & 1u))
-              atomicMax(&sh.nan_piece, piece);
-          }
+          for (int k = 0; k < 4; ++k)
+            *x[k] &= ~(((((*x[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xFFu);
+          atomicMax(&sh.nan_piece, piece);
         }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint8_t *d = dst + (j + k) * RPS * 128;
-          *reinterpret_cast<uint4 *>(d + at0) =
-              make_uint4(h[8 * k], h[8 * k + 1], h[8 * k + 2], h[8 * k + 3]);
-          *reinterpret_cast<uint4 *>(d + (at0 ^ 16)) =
-              make_uint4(h[8 * k + 4], h[8 * k + 5], h[8 * k + 6], h[8 * k + 7]);
-        }
+        uint8_t *d = dst + j * RPS * 128;
+        *reinterpret_cast<uint4 *>(d + at0) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4 *>(d + (at0 ^ 16)) = make_uint4(h[4], h[5], h[6], h[7]);
       }
       fence_proxy_async_shared();
-      tree_arrive(sh.v8_free[st]);
       tree_arrive(sh.v_full[pair]);
-      st += 2;
-      if (st >= kTreeStages) {
-        st -= kTreeStages;
-        ph ^= 1u;
-      }
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");         // none in flight at exit
   } else if (warp == 8) {
     // ---------------------------------------------------------------- MMA issue
-    // The whole warp runs the loop, so that addresses stay in uniform registers; one lane issues.
-    {
-      const bool leader = elect_one();
+    if (lane == 0) {
       const uint64_t qd = tree_sdesc_k<128>(sbase + L::kQ);
       uint32_t ip = 0;
-      // the piece's heads and the log2 of the heads or repeats in a row tile; those of the tile before
-      int left = 0, hc = 0, shift = 0, hc1 = 0, shift1 = 0;
+      int left = 0;
       bool fresh = false, before = false;
       auto next = [&]() {                                        // the next tile, if there is one
         fresh = left == 0;
         if (fresh) {
           const uint32_t i = ip % kTreePieces;
-          if (!tree_wait<true>(sh.piece_full[i], ip / kTreePieces, &sh.abort)) return false;
+          if (!tree_wait<false>(sh.piece_full[i], ip / kTreePieces, &sh.abort)) return false;
           left = sh.piece[i].t_end - (sh.piece[i].t_end > 0 ? sh.piece[i].t : 0);
-          hc = sh.piece[i].hc;
-          shift = tree_shift(sh.piece[i].rows);
-          tree_arrive(sh.piece_free[i]);
+          mbar_arrive(smem_u32(&sh.piece_free[i]));
           ++ip;
         }
         return left-- > 0;
       };
-      uint32_t st = 0, ph = 0, vt = 0;
+      uint32_t st = 0, ph = 0;
       bool live = next();
       // the scores of tile it, then the values of tile it - 1
 #pragma unroll 1
@@ -917,80 +797,47 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         for (int k = 0; k < 2 && ok; ++k) {
           if (fresh == (k == 1)) {
             if (!live) continue;
-            if (fresh) ok = tree_wait<true>(sh.q_full, ip - 1, &sh.abort);
-#pragma unroll 1
-            for (int j = 0; j < (M ? hc : 1) && ok; ++j) {
-              if (!(ok = tree_wait<true>(sh.k_full[st], ph, &sh.abort))) break;
-              tc_fence_after();
-              const uint64_t kd = tree_sdesc_k<D>(sbase + L::kK + st * L::kTile);
-              uint32_t off[4];                                   // a head has its own lane groups
+            if ((fresh && !tree_wait<false>(sh.q_full, ip - 1, &sh.abort)) ||
+                !tree_wait<false>(sh.k_full[st], ph, &sh.abort)) {
+              ok = false;
+              continue;
+            }
+            tc_fence_after();
+            const uint64_t kd = tree_sdesc_k<D>(sbase + L::kK + st * L::kTile);
 #pragma unroll
-              for (int q = 0; q < 4; ++q) off[q] = q >> (2 - shift) == j ? 0u : ~0u;
-              if (leader) {
-#pragma unroll
-                for (int kk = 0; kk < D / 32; ++kk) {
-                  const uint32_t at = tmem + L::kColS + 64 * (it & 1u), acc = kk > 0 ? 1u : 0u;
-                  if constexpr (M) mma_f8f6f4_lanes(at, qd + 2 * kk, kd + 2 * kk, L::kIdescQK, off, acc);
-                  else mma_f8f6f4(at, qd + 2 * kk, kd + 2 * kk, L::kIdescQK, acc);
-                }
-                mma_commit(smem_u32(&sh.k_free[st]));
-                if (!M || j + 1 == hc) {
-                  mma_commit(smem_u32(&sh.s_full[it & 1u]));
-                  if (left == 0) mma_commit(smem_u32(&sh.q_free));  // the piece's last scores
-                }
-              }
-              __syncwarp();
-              if (++st == kKStages) {
-                st = 0;
-                ph ^= 1u;
-              }
+            for (int kk = 0; kk < D / 32; ++kk)
+              mma_f8f6f4(tmem + L::kColS + 64 * (it & 1u), qd + 2 * kk, kd + 2 * kk, L::kIdescQK,
+                         kk > 0 ? 1u : 0u);
+            mma_commit(smem_u32(&sh.s_full[it & 1u]));
+            mma_commit(smem_u32(&sh.k_free[st]));
+            if (left == 0) mma_commit(smem_u32(&sh.q_free));     // the piece's last scores
+            if (++st == kTreeStages) {
+              st = 0;
+              ph ^= 1u;
             }
           } else if (it > 0) {
-            const uint32_t buf = (it - 1) & 1u;
-            ok = tree_wait<true>(sh.p_full[buf], (it - 1) >> 1, &sh.abort);
-            // A lane group that holds a repeat has weights at its own positions only: the other K
-            // steps leave its values alone, and its first one writes them in a new piece.
-            const uint32_t pair = M || shift1 < 2 ? 0u : ~0u, rest = M || shift1 < 1 ? 0u : ~0u;
-            const uint32_t one = before ? 0u : 1u;
-            const uint32_t acc[4] = {one, M || shift1 < 2 ? 1u : one, M || shift1 < 1 ? 1u : one,
-                                     M || shift1 < 2 ? 1u : one};
-#pragma unroll 1
-            for (int j = 0; j < (M ? hc1 : 1) && ok; ++j, ++vt) {
-              const uint32_t i = vt & 1u;
-              if (!(ok = tree_wait<true>(sh.v_full[i], vt >> 1, &sh.abort))) break;
-              tc_fence_after();
-              const uint64_t vd = tree_sdesc_v(sbase + L::kV16 + i * L::kV16Bytes);
-              uint32_t other[4];
-#pragma unroll
-              for (int q = 0; q < 4; ++q) other[q] = !M || q >> (2 - shift1) == j ? 0u : ~0u;
-              if (leader) {
-#pragma unroll
-                for (int kk = 0; kk < kTreeN / 16; ++kk) {
-                  uint32_t off[4];
-#pragma unroll
-                  for (int q = 0; q < 4; ++q)
-                    off[q] = q == kk ? other[q] : other[q] | (q / 2 == kk / 2 ? pair : rest);
-                  mma_f16_ts(tmem + L::kColO, tmem + L::kColS + 64 * buf + 8 * kk, vd + 128 * kk,
-                             L::kIdescPV, off, acc[kk]);
-                }
-                mma_commit(smem_u32(&sh.pv_done[i]));
-                if (!M || j + 1 == hc1) mma_commit(smem_u32(&sh.o_done[buf]));
-              }
-              __syncwarp();
+            const uint32_t i = (it - 1) & 1u, pp = (it - 1) >> 1;
+            if (!tree_wait<false>(sh.p_full[i], pp, &sh.abort) ||
+                !tree_wait<false>(sh.v_full[i], pp, &sh.abort)) {
+              ok = false;
+              continue;
             }
+            tc_fence_after();
+            const uint64_t vd = tree_sdesc_v(sbase + L::kV16 + i * L::kV16Bytes);
+#pragma unroll
+            for (int kk = 0; kk < kTreeN / 16; ++kk)
+              mma_f16_ts(tmem + L::kColO, tmem + L::kColS + 64 * i + 8 * kk, vd + 128 * kk,
+                         L::kIdescPV, before && kk == 0 ? 0u : 1u);
+            mma_commit(smem_u32(&sh.pv_done[i]));
           }
         }
         if (!ok) break;
         if (!live) break;
         before = fresh;
-        hc1 = hc;
-        shift1 = shift;
         live = next();
       }
-      if (leader) {
-        mma_commit(smem_u32(&sh.drain));                         // all MMAs done before dealloc
-        wait_drain(smem_u32(&sh.drain), 0);
-      }
+      mma_commit(smem_u32(&sh.drain));                           // all MMAs done before dealloc
+      wait_drain(smem_u32(&sh.drain), 0);
     }
     __syncwarp();
   } else {
@@ -1003,30 +850,28 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     uint32_t it = 0;
     TreePiece pc;
     for (uint32_t ip = 0;; ++ip) {
-      bool ok = tree_take<M>(sh, ip, pc);
-      // This thread's row of the tile: row r of head pc.g + j, with the columns from col0 on where the
-      // other lane groups of the row (rep > 1) hold the others.
-      const int span = 7 - tree_shift(pc.rows), csh = M ? 0 : 7 - span, rep = 1 << csh;
-      const int w0 = warp & ((4 >> csh) - 1), vr = 32 * w0 + lane, nc = kTreeN >> csh;
-      const uint32_t col0 = nc * (warp >> (2 - csh));
-      const int j = M ? vr >> span : 0, r = M ? vr & ((1 << span) - 1) : vr;
-      const bool live = r < pc.rows && (!M || j < pc.hc);
+      bool ok = tree_take(sh, ip, pc);
+      const int shift = pc.rows <= 32 ? 2 : (pc.rows <= 64 ? 1 : 0), rep = 1 << shift;
+      const int w0 = warp & ((4 >> shift) - 1), r = 32 * w0 + lane, nc = kTreeN >> shift;
+      const uint32_t col0 = nc * (warp >> (2 - shift));
+      const bool live = r < pc.rows;
       const int node = a.by_group(pc.row0 + r);
       const int64_t *mrow = a.mask && live ? a.mask + (pc.first + node) * a.ldm : nullptr;
-      const float c2r = !M || live ? c2 : 0.0f;                  // rows without a head hold no scores
       TreeRow st{-INFINITY, 0.0f};
       for (int t = pc.t; t < pc.t_end && ok; ++t, ++it) {
-        ok = tree_tile<D, M>(sh, tw, col0, 4 >> csh, it, t == pc.t, mrow, words, live ? node : -1,
-                          t * kTreeN - pc.ctx, c2r, st);
+        // a row that does not exist counts as seeing all (its scores are 0, its results unused)
+        const uint64_t seen = live ? tree_bits(mrow, words, node, t * kTreeN - pc.ctx) : ~0ull;
+        const bool first = t == pc.t;
+        ok = tree_tile<D>(sh, tw, col0, 4 >> shift, it, first, seen, c2, st);
       }
-      ok = ok && tree_wait<true>(sh.o_done[(it - 1) & 1u], (it - 1) >> 1, &sh.abort);
+      ok = ok && tree_wait<true>(sh.pv_done[(it - 1) & 1u], (it - 1) >> 1, &sh.abort);
       sh.ml[warp][lane][0] = st.ref;
       sh.ml[warp][lane][1] = st.l;
       if (tree_any4(!ok)) break;                                 // no more pieces, or given up
       tc_fence_after();
       uint4 nan = make_uint4(0, 0, 0, 0);
       const bool any_nan = *reinterpret_cast<volatile int *>(&sh.nan_piece) > static_cast<int>(ip);
-      if (any_nan && live) nan = tree_nan_dims<D>(a, pc, pc.g + j, node, col0, nc);
+      if (any_nan && live) nan = tree_nan_dims<D>(a, pc, node, col0, nc);
       const bool whole = pc.t == 0 && pc.t_end == pc.nt;
       const int slot = pc.t > 0 ? 0 : 1;
       float *part = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * a.row_cap * (D + 2);
@@ -1038,31 +883,27 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           meta[3] = pc.row0;
           meta[4] = pc.rows;
           meta[5] = pc.g;
-          meta[6] = pc.hc;
-          meta[7] = span;
         }
       }
       // Repeats of a row hold different positions: their states are merged, then summed by rows, `rep`
       // threads per row and 16 / rep columns each.
       auto merged = [&](int w, int ln, float &l) {
-        float top = -INFINITY;
-        for (int i = w; i < 4; i += 4 >> csh) top = fmaxf(top, sh.ml[i][ln][0]);
+        float M = -INFINITY;
+        for (int i = w; i < 4; i += 4 >> shift) M = fmaxf(M, sh.ml[i][ln][0]);
         l = 0.0f;
-        for (int i = w; i < 4; i += 4 >> csh) {
+        for (int i = w; i < 4; i += 4 >> shift) {
           const float m = sh.ml[i][ln][0];
-          l += sh.ml[i][ln][1] * (m == top ? 1.0f : tree_ex2(m - top));
+          l += sh.ml[i][ln][1] * (m == M ? 1.0f : tree_ex2(m - M));
         }
-        return top;
+        return M;
       };
-      const int tr = tid >> csh, cpt = 16 >> csh, tc = (tid & (rep - 1)) * cpt;
+      const int tr = tid >> shift, cpt = 16 >> shift, tc = (tid & (rep - 1)) * cpt;
       float l;
-      const float own = merged(w0, lane, l);                     // of the row whose values this lane holds
-      const float f = st.l == 0.0f ? 0.0f : (st.ref == own ? 1.0f : tree_ex2(st.ref - own));
-      const float ref = merged(tr >> 5, tr & 31, l);             // of the row that this thread writes
+      const float mine_M = merged(w0, lane, l);
+      const float f = st.l == 0.0f ? 0.0f : (st.ref == mine_M ? 1.0f : tree_ex2(st.ref - mine_M));
+      const float M = merged(tr >> 5, tr & 31, l);
       const float scale = whole ? (l == 0.0f ? 0.0f : sv / l) : 1.0f;
-      const int tj = M ? j : 0, idx = pc.row0 + (M ? r : tr), nd = a.by_group(idx);
-      const bool there = M ? live : tr < pc.rows;
-      const int h = (pc.g + tj) * G + (idx - nd * G);
+      const int idx = pc.row0 + tr, nd = a.by_group(idx), h = pc.g * G + (idx - nd * G);
       uint16_t *out = a.out + (pc.first + nd) * a.ldo + h * D + tc;
       float *po = part + tr * D + tc;
       auto store4 = [&](int c, float4 v) {
@@ -1096,7 +937,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
             if ((w >> (4 * j)) & 8u) v[j].w = NAN;
           }
         }
-        if (M || rep == 1) {
+        if (rep == 1) {
           if (live) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) store4(c + 4 * j, v[j]);
@@ -1106,7 +947,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
 #pragma unroll
         for (int j = 0; j < 4; ++j) sh.o[warp][lane][j] = v[j];
         tree_sync4();
-        if (there) {
+        if (tr < pc.rows) {
           // four reads: four warps' columns, or two warps' twice as many
           float4 x[4];
 #pragma unroll
@@ -1126,56 +967,42 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         }
         tree_sync4();
       }
-      if (!whole && there && tc == 0) {
+      if (!whole && tr < pc.rows && tc == 0) {
         float *ml = part + static_cast<int64_t>(a.row_cap) * D;
-        ml[2 * tr] = ref;
+        ml[2 * tr] = M;
         ml[2 * tr + 1] = l;
       }
       tc_fence_before();
     }
   }
 
+  __syncwarp();
   __syncthreads();
-  if (tid == 0 && sh.abort) record_error(6 /* FP8Q_ERR_TIMEOUT */);
   if (warp == 8) {
     tc_fence_after();
+    __syncwarp();
     tmem_dealloc(tmem, L::kCols);
   }
 }
 
-// The items that several CTAs shared: block (i, y) takes eight warps' rows of the item whose
-// first part is CTA i's last piece, and adds the parts in CTA order, each a
-// running maximum's state.
-constexpr int kTreeMergeRows = 1;  // 2 or 4 rows per warp: within 1 % on batches, 2 % slower on a long context
+// The items that several CTAs shared: block (i, y) takes the rows 8 y .. 8 y + 7 of the item whose
+// first part is CTA i's last piece, a warp per row, and adds the parts in CTA order, each a running
+// maximum's state.
 template <int D>
 __global__ void __launch_bounds__(256) k_tree_attn_combine(const TreeAttnArgs a) {
-  constexpr int V = D / 32, R = kTreeMergeRows;
+  constexpr int V = D / 32;
   static_assert(V == 2 || V == 4, "vector loads of the parts");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int i = blockIdx.x, lane = threadIdx.x & 31;
   const int32_t *meta = a.meta + i * kTreeMetaInts;
-  const int4 m0 = *reinterpret_cast<const int4 *>(meta), m1 = *reinterpret_cast<const int4 *>(meta + 4);
-  if (m0.y == 0) return;
-  const int rows = m1.x, heads = m1.z, span = m1.w;
-  const int r0 = (blockIdx.y * 8 + (threadIdx.x >> 5)) * R;
+  const int4 m0 = *reinterpret_cast<const int4 *>(meta);         // part, first part, row of node 0, row0
+  const int2 m1 = *reinterpret_cast<const int2 *>(meta + 4);     // rows, kv head
+  const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  if (m0.y == 0 || r >= m1.x) return;
   const int64_t slot = static_cast<int64_t>(a.row_cap) * (D + 2);
-  const float *base = a.part + r0 * D + V * lane;
-  const int64_t ml = static_cast<int64_t>(a.row_cap) * D + 2 * r0;
-  bool on[R], any = false;
-#pragma unroll
-  for (int q = 0; q < R; ++q) {
-    on[q] = ((r0 + q) & ((1 << span) - 1)) < rows && (r0 + q) >> span < heads;
-    any |= on[q];
-  }
-  if (!any) return;
-  float top[R], l[R], o[R][V];
-#pragma unroll
-  for (int q = 0; q < R; ++q) {
-    top[q] = -INFINITY;
-    l[q] = 0.0f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) o[q][v] = 0.0f;
-  }
+  const float *base = a.part + r * D + V * lane;
+  const int64_t ml = static_cast<int64_t>(a.row_cap) * D + 2 * r;
+  float top = -INFINITY, l = 0.0f, o[V] = {};
   // 32 parts at a time: their maxima and sums by lanes, then the values one after the other
   for (int j0 = i;; j0 += 32) {
     const int j = j0 + lane;
@@ -1184,60 +1011,46 @@ __global__ void __launch_bounds__(256) k_tree_attn_combine(const TreeAttnArgs a)
     const uint32_t ends = __ballot_sync(0xffffffffu, kind != 1);
     const int last = ends ? __ffs(ends) - 1 : 31;
     const int n = __shfl_sync(0xffffffffu, last + (in ? 1 : 0), last);  // behind the grid: not a part
-    const float *p = a.part + (2 * static_cast<int64_t>(j) + (j == i ? 1 : 0)) * slot + ml;
-    float w[R];
+    float2 e = make_float2(-INFINITY, 0.0f);                     // maximum, sum
+    if (lane < n)
+      e = *reinterpret_cast<const float2 *>(
+          a.part + (2 * static_cast<int64_t>(j) + (j == i ? 1 : 0)) * slot + ml);
+    if (e.y == 0.0f) e.x = -INFINITY;
+    float m = e.x;
 #pragma unroll
-    for (int q = 0; q < R; ++q) {
-      float2 e = make_float2(-INFINITY, 0.0f);                   // maximum, sum
-      if (lane < n && on[q]) e = *reinterpret_cast<const float2 *>(p + 2 * q);
-      if (e.y == 0.0f) e.x = -INFINITY;
-      float m = e.x;
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    m = fmaxf(m, top);
+    // a part without weight has l = 0; a NaN sum stays one
+    const float w = e.y == 0.0f ? 0.0f : (e.x == m ? 1.0f : tree_ex2(e.x - m));
+    const float keep = l == 0.0f ? 0.0f : (top == m ? 1.0f : tree_ex2(top - m));
+    float sum = e.y * w;
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-      m = fmaxf(m, top[q]);
-      // a part without weight has l = 0; a NaN sum stays one
-      w[q] = e.y == 0.0f ? 0.0f : (e.x == m ? 1.0f : tree_ex2(e.x - m));
-      const float keep = l[q] == 0.0f ? 0.0f : (top[q] == m ? 1.0f : tree_ex2(top[q] - m));
-      float sum = e.y * w[q];
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    l = l * keep + sum;
+    top = m;
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      l[q] = l[q] * keep + sum;
-      top[q] = m;
-#pragma unroll
-      for (int v = 0; v < V; ++v) o[q][v] *= keep;
-    }
+    for (int v = 0; v < V; ++v) o[v] *= keep;
 #pragma unroll 2
     for (int k = 0; k < n; ++k) {
-      const float *part = base + (2 * static_cast<int64_t>(j0 + k) + (j0 + k == i ? 1 : 0)) * slot;
+      const float *p = base + (2 * static_cast<int64_t>(j0 + k) + (j0 + k == i ? 1 : 0)) * slot;
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+      alignas(16) float v[V];
+      if constexpr (V == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(p);
+      else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(p);
 #pragma unroll
-      for (int q = 0; q < R; ++q) {
-        const float wk = __shfl_sync(0xffffffffu, w[q], k);
-        if (!on[q]) continue;
-        alignas(16) float v[V];
-        if constexpr (V == 4)
-          *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(part + q * D);
-        else
-          *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(part + q * D);
-#pragma unroll
-        for (int x = 0; x < V; ++x) o[q][x] += v[x] * wk;
-      }
+      for (int x = 0; x < V; ++x) o[x] += v[x] * wk;
     }
     if (ends) break;
   }
-  const int G = a.Hq / a.Hkv;
+  const int G = a.Hq / a.Hkv, idx = m0.w + r, node = a.by_group(idx);
+  const int h = m1.y * G + (idx - node * G);
+  const float f = l == 0.0f ? 0.0f : a.scale3[2] / l;
+  uint16_t *out = a.out + (static_cast<int64_t>(m0.z) + node) * a.ldo + h * D + V * lane;
 #pragma unroll
-  for (int q = 0; q < R; ++q) {
-    if (!on[q]) continue;
-    const int idx = m0.w + ((r0 + q) & ((1 << span) - 1)), node = a.by_group(idx);
-    const int h = (m1.y + ((r0 + q) >> span)) * G + (idx - node * G);
-    const float f = l[q] == 0.0f ? 0.0f : a.scale3[2] / l[q];
-    uint16_t *out = a.out + (static_cast<int64_t>(m0.z) + node) * a.ldo + h * D + V * lane;
-#pragma unroll
-    for (int v = 0; v < V; v += 2) {
-      const __nv_bfloat162 b2 = __floats2bfloat162_rn(l[q] == 0.0f ? 0.0f : o[q][v] * f,
-                                                      l[q] == 0.0f ? 0.0f : o[q][v + 1] * f);
-      *reinterpret_cast<uint32_t *>(out + v) = *reinterpret_cast<const uint32_t *>(&b2);
-    }
+  for (int v = 0; v < V; v += 2) {
+    const __nv_bfloat162 b2 = __floats2bfloat162_rn(l == 0.0f ? 0.0f : o[v] * f,
+                                                    l == 0.0f ? 0.0f : o[v + 1] * f);
+    *reinterpret_cast<uint32_t *>(out + v) = *reinterpret_cast<const uint32_t *>(&b2);
   }
 }
 

@@ -218,6 +218,17 @@ __device__ __forceinline__ void mma_mxf8f6f4(uint32_t tmem_d, uint64_t adesc, ui
       : "memory");
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // D[tmem] (+)= A[tmem] x B[smem desc], kind::f16 (A packed two fp16 per 32-bit column, one row per
 // lane).
 __device__ __forceinline__ void mma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,

@@ -345,37 +345,44 @@ struct TreeRow {
   float ref, l;                  // reference of the weights (log2 units), their sum
 };
 
-// Sixteen scores of this thread's row from TMEM; what is not seen (bit 0 on) becomes -inf.
-__device__ __forceinline__ void tree_scores(uint32_t taddr, uint64_t seen, uint32_t (&sr)[16]) {
-  tree_ld<16>(taddr, sr);
-  const uint32_t bits = static_cast<uint32_t>(seen) & 0xFFFFu;
-  if (!__all_sync(0xffffffffu, bits == 0xFFFFu)) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if (!((bits >> j) & 1)) sr[j] = 0xFF800000u;
-  }
-}
-
 // One position tile: the scores of 16 * chunks columns of this thread's row become weights, in the
 // first half of the score buffer's columns: 8 columns per chunk, behind those already read.  The first
 // chunk's scores stay in registers between the maximum and the weights, the others are read again.
-// Loops over short bodies: the roles' code together has to stay in the instruction caches.
+// Loops over short bodies: the roles' code together has to stay in the instruction caches.  j0: the
+// tile's first position, counted from node 0.
 template <int D>
 __device__ __forceinline__ bool tree_tile(TreeShared &sh, uint32_t tmem, uint32_t col0, int chunks,
-                                          uint32_t it, bool first, uint64_t seen, float c2,
-                                          TreeRow &st) {
+                                          uint32_t it, bool first, const int64_t *mrow, int words,
+                                          int node, int j0, float c2, TreeRow &st) {
   using L = TreeLayout<D>;
   if (!tree_wait<true>(sh.s_full[it & 1u], it >> 1, &sh.abort)) return false;
   tc_fence_after();
   const uint32_t buf = tmem + L::kColS + 64 * (it & 1u);
   uint32_t sr[16];
-  seen = (seen & sh.valid[it & 7u]) >> col0;
+  uint64_t seen = sh.valid[it & 7u];
+  if (j0 > -kTreeN || seen != ~0ull) {                           // not within the context, or not whole
+    // what is not seen becomes -inf in TMEM; a row that does not exist counts as seeing all
+    if (node >= 0) seen &= tree_bits(mrow, words, node, j0);
+    seen >>= col0;
+#pragma unroll 1
+    for (int c = 0; c < 16 * chunks; c += 16, seen >>= 16) {
+      __syncwarp();                                              // whole warps at the TMEM loads
+      tree_ld<16>(buf + col0 + c, sr);
+      const uint32_t bits = static_cast<uint32_t>(seen);
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (!((bits >> j) & 1)) sr[j] = 0xFF800000u;
+      __syncwarp();
+      tree_st<16>(buf + col0 + c, sr);
+    }
+    tmem_st_wait();
+  }
   float mx[2] = {-INFINITY, -INFINITY};
   int c = chunks;
 #pragma unroll 1
   do {
     --c;
-    tree_scores(buf + col0 + 16 * c, seen >> (16 * c), sr);
+    tree_ld<16>(buf + col0 + 16 * c, sr);
 #pragma unroll
     for (int j = 0; j < 16; ++j) mx[j & 1] = fmaxf(mx[j & 1], __uint_as_float(sr[j]));
   } while (c > 0);
@@ -415,7 +422,7 @@ __device__ __forceinline__ bool tree_tile(TreeShared &sh, uint32_t tmem, uint32_
     }
     tree_st<8>(buf + col0 / 2 + 8 * c, pk);
     if (++c >= chunks) break;
-    tree_scores(buf + col0 + 16 * c, seen >> (16 * c), sr);
+    tree_ld<16>(buf + col0 + 16 * c, sr);
   }
   // a repeat of a row has no weight at the other repeats' positions
 #pragma unroll 1
@@ -612,12 +619,15 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         slot[1] = slot_of(1, &ok);
         there |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, ok)) << 32;
       } else {
-        const uint64_t bits = ok ? (a.box == 64 ? ~0ull : ((1ull << a.box) - 1) << first) : 0ull;
-        there = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(bits));
-        there |= static_cast<uint64_t>(
-                     __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(bits >> 32))) << 32;
         const int left = pre.s.ctx + pre.s.n - pre.t * kTreeN;   // positions that exist
-        if (left < 64) there &= (1ull << left) - 1;
+        there = ~0ull;
+        if (left < 64 || !__all_sync(0xffffffffu, ok)) {
+          const uint64_t bits = ok ? (a.box == 64 ? ~0ull : ((1ull << a.box) - 1) << first) : 0ull;
+          there = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(bits));
+          there |= static_cast<uint64_t>(
+                       __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(bits >> 32))) << 32;
+          if (left < 64) there &= (1ull << left) - 1;
+        }
       }
       const uint32_t bar = smem_u32(&sh.k_full[st]);
       if (lane == 0) {
@@ -740,28 +750,46 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       uint8_t *dst = smem + L::kV16 + pair * L::kV16Bytes + (ch >> 2) * 8192 + r0 * 128;
       const int at0 = ((ch & 3) * 2 ^ (r0 & 7)) << 4;            // RPS is a multiple of 8
 #pragma unroll 1
-      for (int j = 0; j < NR; ++j) {
-        uint4 v8 = *reinterpret_cast<const uint4 *>(smem + (stage - sbase) + j * 1024);
-        uint32_t h[8];
+      for (int j = 0; j < NR; j += 2) {
+        uint4 v8[2];
+        uint32_t h[16];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          v8[k] = *reinterpret_cast<const uint4 *>(smem + (stage - sbase) + (j + k) * 1024);
         while (true) {
-          const uint32_t w[4] = {v8.x, v8.y, v8.z, v8.w};
-          __half2 acc = __half2half2(__ushort_as_half(0));
+          const uint32_t w[8] = {v8[0].x, v8[0].y, v8[0].z, v8[0].w,
+                                 v8[1].x, v8[1].y, v8[1].z, v8[1].w};
+          __half2 m[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            h[k] = e4m3x2_to_f16x2(k & 1 ? w[k / 2] >> 16 : w[k / 2] & 0xFFFFu);
-            acc = __hmax2_nan(acc, *reinterpret_cast<const __half2 *>(&h[k]));
+            h[2 * k] = e4m3x2_to_f16x2(w[k] & 0xFFFFu);
+            h[2 * k + 1] = e4m3x2_to_f16x2(w[k] >> 16);
+            m[k] = __hmax2_nan(*reinterpret_cast<const __half2 *>(&h[2 * k]),
+                               *reinterpret_cast<const __half2 *>(&h[2 * k + 1]));
           }
-          if (!__hisnan(__low2half(acc)) && !__hisnan(__high2half(acc))) break;
-          // A NaN code becomes 0; it is put back into the results of the rows that see it.
-          uint32_t *x[4] = {&v8.x, &v8.y, &v8.z, &v8.w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            *x[k] &= ~(((((*x[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xFFu);
+          for (int d = 4; d > 0; d /= 2)
+#pragma unroll
+            for (int k = 0; k < d; ++k) m[k] = __hmax2_nan(m[k], m[k + d]);
+          if (!__hisnan(__low2half(m[0])) && !__hisnan(__high2half(m[0]))) break;
+          // A NaN code becomes 0; it is put back into the results of the rows that see it.
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t *x[4] = {&v8[k].x, &v8[k].y, &v8[k].z, &v8[k].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              *x[q] &= ~(((((*x[q] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xFFu);
+          }
           atomicMax(&sh.nan_piece, piece);
         }
-        uint8_t *d = dst + j * RPS * 128;
-        *reinterpret_cast<uint4 *>(d + at0) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4 *>(d + (at0 ^ 16)) = make_uint4(h[4], h[5], h[6], h[7]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint8_t *d = dst + (j + k) * RPS * 128;
+          *reinterpret_cast<uint4 *>(d + at0) =
+              make_uint4(h[8 * k], h[8 * k + 1], h[8 * k + 2], h[8 * k + 3]);
+          *reinterpret_cast<uint4 *>(d + (at0 ^ 16)) =
+              make_uint4(h[8 * k + 4], h[8 * k + 5], h[8 * k + 6], h[8 * k + 7]);
+        }
       }
       fence_proxy_async_shared();
       tree_arrive(sh.v_full[pair]);
@@ -769,7 +797,9 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     asm volatile("cp.async.wait_group 0;" ::: "memory");         // none in flight at exit
   } else if (warp == 8) {
     // ---------------------------------------------------------------- MMA issue
-    if (lane == 0) {
+    // The whole warp runs the loop, so that addresses stay in uniform registers; one lane issues.
+    {
+      const bool leader = elect_one();
       const uint64_t qd = tree_sdesc_k<128>(sbase + L::kQ);
       uint32_t ip = 0;
       int left = 0;
@@ -778,9 +808,9 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         fresh = left == 0;
         if (fresh) {
           const uint32_t i = ip % kTreePieces;
-          if (!tree_wait<false>(sh.piece_full[i], ip / kTreePieces, &sh.abort)) return false;
+          if (!tree_wait<true>(sh.piece_full[i], ip / kTreePieces, &sh.abort)) return false;
           left = sh.piece[i].t_end - (sh.piece[i].t_end > 0 ? sh.piece[i].t : 0);
-          mbar_arrive(smem_u32(&sh.piece_free[i]));
+          tree_arrive(sh.piece_free[i]);
           ++ip;
         }
         return left-- > 0;
@@ -797,38 +827,44 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         for (int k = 0; k < 2 && ok; ++k) {
           if (fresh == (k == 1)) {
             if (!live) continue;
-            if ((fresh && !tree_wait<false>(sh.q_full, ip - 1, &sh.abort)) ||
-                !tree_wait<false>(sh.k_full[st], ph, &sh.abort)) {
+            if ((fresh && !tree_wait<true>(sh.q_full, ip - 1, &sh.abort)) ||
+                !tree_wait<true>(sh.k_full[st], ph, &sh.abort)) {
               ok = false;
               continue;
             }
             tc_fence_after();
             const uint64_t kd = tree_sdesc_k<D>(sbase + L::kK + st * L::kTile);
+            if (leader) {
 #pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk)
-              mma_f8f6f4(tmem + L::kColS + 64 * (it & 1u), qd + 2 * kk, kd + 2 * kk, L::kIdescQK,
-                         kk > 0 ? 1u : 0u);
-            mma_commit(smem_u32(&sh.s_full[it & 1u]));
-            mma_commit(smem_u32(&sh.k_free[st]));
-            if (left == 0) mma_commit(smem_u32(&sh.q_free));     // the piece's last scores
+              for (int kk = 0; kk < D / 32; ++kk)
+                mma_f8f6f4(tmem + L::kColS + 64 * (it & 1u), qd + 2 * kk, kd + 2 * kk, L::kIdescQK,
+                           kk > 0 ? 1u : 0u);
+              mma_commit(smem_u32(&sh.s_full[it & 1u]));
+              mma_commit(smem_u32(&sh.k_free[st]));
+              if (left == 0) mma_commit(smem_u32(&sh.q_free));   // the piece's last scores
+            }
+            __syncwarp();
             if (++st == kTreeStages) {
               st = 0;
               ph ^= 1u;
             }
           } else if (it > 0) {
             const uint32_t i = (it - 1) & 1u, pp = (it - 1) >> 1;
-            if (!tree_wait<false>(sh.p_full[i], pp, &sh.abort) ||
-                !tree_wait<false>(sh.v_full[i], pp, &sh.abort)) {
+            if (!tree_wait<true>(sh.p_full[i], pp, &sh.abort) ||
+                !tree_wait<true>(sh.v_full[i], pp, &sh.abort)) {
               ok = false;
               continue;
             }
             tc_fence_after();
             const uint64_t vd = tree_sdesc_v(sbase + L::kV16 + i * L::kV16Bytes);
+            if (leader) {
 #pragma unroll
-            for (int kk = 0; kk < kTreeN / 16; ++kk)
-              mma_f16_ts(tmem + L::kColO, tmem + L::kColS + 64 * i + 8 * kk, vd + 128 * kk,
-                         L::kIdescPV, before && kk == 0 ? 0u : 1u);
-            mma_commit(smem_u32(&sh.pv_done[i]));
+              for (int kk = 0; kk < kTreeN / 16; ++kk)
+                mma_f16_ts(tmem + L::kColO, tmem + L::kColS + 64 * i + 8 * kk, vd + 128 * kk,
+                           L::kIdescPV, before && kk == 0 ? 0u : 1u);
+              mma_commit(smem_u32(&sh.pv_done[i]));
+            }
+            __syncwarp();
           }
         }
         if (!ok) break;
@@ -836,7 +872,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         before = fresh;
         live = next();
       }
-      mma_commit(smem_u32(&sh.drain));                           // all MMAs done before dealloc
+      if (leader) mma_commit(smem_u32(&sh.drain));               // all MMAs done before dealloc
+      __syncwarp();
       wait_drain(smem_u32(&sh.drain), 0);
     }
     __syncwarp();
@@ -859,10 +896,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       const int64_t *mrow = a.mask && live ? a.mask + (pc.first + node) * a.ldm : nullptr;
       TreeRow st{-INFINITY, 0.0f};
       for (int t = pc.t; t < pc.t_end && ok; ++t, ++it) {
-        // a row that does not exist counts as seeing all (its scores are 0, its results unused)
-        const uint64_t seen = live ? tree_bits(mrow, words, node, t * kTreeN - pc.ctx) : ~0ull;
-        const bool first = t == pc.t;
-        ok = tree_tile<D>(sh, tw, col0, 4 >> shift, it, first, seen, c2, st);
+        ok = tree_tile<D>(sh, tw, col0, 4 >> shift, it, t == pc.t, mrow, words, live ? node : -1,
+                          t * kTreeN - pc.ctx, c2, st);
       }
       ok = ok && tree_wait<true>(sh.pv_done[(it - 1) & 1u], (it - 1) >> 1, &sh.abort);
       sh.ml[warp][lane][0] = st.ref;

@@ -689,29 +689,47 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     TreePiece pc;
     bool ok = true;
     for (uint32_t ip = 0; ok && tree_take(sh, ip, pc); ++ip) {
-      // row r is head g G + r % G of node r / G; up to 32 (64) rows are repeated 4 (2) times down the
-      // tile.  The loads are on their way while the scores of the piece before complete.
+      // Row r is head g G + r % G of node r / G; up to 32 (64) rows are repeated 4 (2) times down the
+      // tile.  The first 256 chunks are on their way while the scores of the piece before complete,
+      // the others all at once behind them.
       const int step = pc.rows <= 32 ? 32 : (pc.rows <= 64 ? 64 : 128);
+      auto source = [&](int r) {
+        const int idx = pc.row0 + r, node = a.by_group(idx), h = pc.g * G + (idx - node * G);
+        return a.q + (pc.first + node) * a.ldq + h * D;
+      };
+      uint4 v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = 32 * k + lane, r = i / LPR;
+        v[k] = make_uint4(0, 0, 0, 0);
+        if (r < min(pc.rows, step))
+          v[k] = *reinterpret_cast<const uint4 *>(source(r) + i % LPR * 16);
+      }
+      if (!(ok = tree_wait<true>(sh.q_free, ip ^ 1u, &sh.abort))) break;
 #pragma unroll 1
-      for (int i0 = 0; i0 < step * LPR; i0 += 256) {
-        uint4 v[8];
+      for (int i = 256 + lane; i < step * LPR; i += 32) {
+        const int r = i / LPR, x = (i % LPR ^ (r & 7)) << 4;
+        const uint8_t *src = source(min(r, pc.rows - 1)) + i % LPR * 16;
+        for (int rr = r; rr < kTreeM; rr += step)
+          cp_async16(sbase + L::kQ + rr * 128 + x, src, r < pc.rows ? 16u : 0u);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int i = i0 + 32 * k + lane, r = i / LPR;
-          v[k] = make_uint4(0, 0, 0, 0);
-          if (r < pc.rows) {
-            const int idx = pc.row0 + r, node = a.by_group(idx), h = pc.g * G + (idx - node * G);
-            v[k] = *reinterpret_cast<const uint4 *>(a.q + (pc.first + node) * a.ldq + h * D +
-                                                    i % LPR * 16);
+      for (int k = 0; k < 8; ++k) {
+        const int i = 32 * k + lane, r = i / LPR;
+        v[k].x ^= qflip; v[k].y ^= qflip; v[k].z ^= qflip; v[k].w ^= qflip;
+        for (int rr = r; r < step && rr < kTreeM; rr += step)
+          *reinterpret_cast<uint4 *>(smem + L::kQ + rr * 128 + ((i % LPR ^ (r & 7)) << 4)) = v[k];
+      }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      if (qflip != 0) {
+#pragma unroll 1
+        for (int i = 256 + lane; i < step * LPR; i += 32) {
+          const int r = i / LPR, x = (i % LPR ^ (r & 7)) << 4;
+          for (int rr = r; rr < kTreeM; rr += step) {
+            uint4 *q = reinterpret_cast<uint4 *>(smem + L::kQ + rr * 128 + x);
+            *q = make_uint4(q->x ^ qflip, q->y ^ qflip, q->z ^ qflip, q->w ^ qflip);
           }
-        }
-        if (i0 == 0 && !(ok = tree_wait<true>(sh.q_free, ip ^ 1u, &sh.abort))) break;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int i = i0 + 32 * k + lane, r = i / LPR;
-          v[k].x ^= qflip; v[k].y ^= qflip; v[k].z ^= qflip; v[k].w ^= qflip;
-          for (int rr = r; r < step && rr < kTreeM; rr += step)
-            *reinterpret_cast<uint4 *>(smem + L::kQ + rr * 128 + ((i % LPR ^ (r & 7)) << 4)) = v[k];
         }
       }
       fence_proxy_async_shared();

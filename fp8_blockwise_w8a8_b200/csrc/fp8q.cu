@@ -1200,7 +1200,7 @@ int fp8q_attention_tree(const void *q_e4m3, int64_t ldq, const void *k_cache, co
   a.part = reinterpret_cast<float *>(a.meta + ctas * fp8q::kTreeMetaInts);
   const unsigned grid = static_cast<unsigned>(ctas < 2 * st->sms ? ctas : 2 * st->sms);
   a.grid_recip = ~uint64_t{0} / grid;
-  // rows per copy; blocks without a power of two of 4 or more go by gathers (box of one row)
+  // rows per TMA copy; blocks without a power of two of 4 or more go row by row, without TMA
   const int64_t pow2 = block_size & -block_size;
   a.box = static_cast<int>(pow2 > 64 ? 64 : pow2);
   const uint32_t box = a.box < 4 ? 1 : static_cast<uint32_t>(a.box);

@@ -42,7 +42,7 @@ struct TreeAttnArgs {
   float sm_scale;
   uint16_t *out;               // [total][ldo] bf16
   int64_t ldo;
-  int box;                     // rows per copy: the power of two in block_size, at most 64; 1: gathers
+  int box;                     // rows per TMA copy: the power of two in block_size, at most 64; 1: row by row
   uint64_t grid_recip;         // floor((2^64 - 1) / gridDim.x)
   TreeDiv by_block, by_group;  // by block_size and by G = Hq / Hkv
   int row_cap;                 // rows of a partial slot: min(128, max_nodes * Hq / Hkv)
@@ -264,6 +264,12 @@ __device__ __forceinline__ void tree_arrive(const uint64_t &barrier) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&barrier));
 }
 
+// An arrival of every thread, once its cp.async copies so far are there.
+__device__ __forceinline__ void tree_arrive_copies(const uint64_t &barrier) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&barrier))
+               : "memory");
+}
+
 template <int N>
 __device__ __forceinline__ void tree_ld(uint32_t taddr, uint32_t (&r)[N]) {
   if constexpr (N == 64) tmem_ld_32x32b_x64(taddr, r);
@@ -471,7 +477,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
 
   if (tid == 0) {
     for (int i = 0; i < kTreeStages; ++i) {
-      mbar_init(smem_u32(&sh.k_full[i]), 1);
+      mbar_init(smem_u32(&sh.k_full[i]), a.box < 4 ? 33 : 1);     // the load warp's lanes and lane 0
       mbar_init(smem_u32(&sh.k_free[i]), 1);
       mbar_init(smem_u32(&sh.t_full[i]), 1);
       mbar_init(smem_u32(&sh.t_free[i]), 2);
@@ -563,19 +569,20 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   if (warp == 9) {
     // ---------------------------------------------------------------- load
     // A copy brings `box` consecutive positions of one block; lane i holds the slot of the i-th copy's
-    // first.  Blocks of odd size or 2 mod 4 go by gathers of four rows instead; then lane i holds the
-    // slots of the positions i and i + 32.
+    // first.  Blocks of odd size or 2 mod 4 go by cp.async instead, row by row; then lane i holds the
+    // slots of the positions i and i + 32.  (TMA gathers of four rows were slower there: 16 a tile held
+    // the load warp for 80 % of the time.)
     TreeCursor pre;
     pre.init(a, G, B, sh.start_b, sh.start_off, hi - lo);
-    const bool gather = a.box < 4;
+    const bool by_row = a.box < 4;
     const int chunks = kTreeN / a.box, log_box = __ffs(a.box) - 1;
-    const int first = gather ? lane : min(lane, chunks - 1) * a.box;
+    const int first = by_row ? lane : min(lane, chunks - 1) * a.box;
     int blk[2], off[2];
     auto look_up = [&]() {                                       // block ids of the cursor's tile
       if (!pre.live) return;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        if (j == 1 && !gather) break;
+        if (j == 1 && !by_row) break;
         const int pos = pre.t * kTreeN + 32 * j + first;
         const int q = a.by_block(pos);
         off[j] = pos - q * a.block_size;
@@ -614,7 +621,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       bool ok;
       int32_t slot[2] = {slot_of(0, &ok), 0};
       uint64_t there;
-      if (gather) {
+      if (by_row) {
         there = __ballot_sync(0xffffffffu, ok);
         slot[1] = slot_of(1, &ok);
         there |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, ok)) << 32;
@@ -634,19 +641,26 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         sh.valid[it & 7u] = there;
         sh.tile[st].g = pre.g;
         sh.tile[st].piece = static_cast<int>(ip);
-        mbar_arrive_expect_tx(bar, L::kTile);
+        if (by_row) mbar_arrive(bar);
+        else mbar_arrive_expect_tx(bar, L::kTile);
       }
       __syncwarp();
       const uint32_t dst = sbase + L::kK + st * L::kTile;
-      if (gather) {
-        int32_t rows[4];
+      if (by_row) {
+        constexpr int LPR = D / 16, RPS = 32 / LPR;              // lanes per row, rows per step
+        const int ch = lane % LPR;
+        const uint8_t *src = a.k_cache + pre.g * D + ch * 16;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int32_t v0 = __shfl_sync(0xffffffffu, slot[0], (4 * lane + r) & 31);
-          const int32_t v1 = __shfl_sync(0xffffffffu, slot[1], (4 * lane + r) & 31);
-          rows[r] = lane & 8 ? v1 : v0;
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll 4
+          for (int r = lane / LPR; r < 32; r += RPS) {
+            const int64_t from = __shfl_sync(0xffffffffu, slot[j], r);
+            const int to = 32 * j + r, x = D == 128 ? to & 7 : to >> 1 & 3;
+            cp_async16(dst + to * D + ((ch ^ x) << 4), src + from * a.Hkv * D,
+                       (there >> to) & 1u ? 16u : 0u);
+          }
         }
-        if (lane < 16) tma_gather4(dst + 4 * D * lane, &tm_k, pre.g * D, rows, bar);
+        tree_arrive_copies(sh.k_full[st]);
       } else {
         if (lane < chunks) tma_load_2d(dst + lane * a.box * D, &tm_k, pre.g * D, slot[0], bar);
         const int32_t row = slot[0];
@@ -850,6 +864,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
               ok = false;
               continue;
             }
+            if (a.box < 4) fence_proxy_async_shared();           // K came by cp.async
             tc_fence_after();
             const uint64_t kd = tree_sdesc_k<D>(sbase + L::kK + st * L::kTile);
             if (leader) {

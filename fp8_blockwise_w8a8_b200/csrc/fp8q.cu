@@ -1200,17 +1200,16 @@ int fp8q_attention_tree(const void *q_e4m3, int64_t ldq, const void *k_cache, co
   a.part = reinterpret_cast<float *>(a.meta + ctas * fp8q::kTreeMetaInts);
   const unsigned grid = static_cast<unsigned>(ctas < 2 * st->sms ? ctas : 2 * st->sms);
   a.grid_recip = ~uint64_t{0} / grid;
-  // rows per TMA copy; blocks without a power of two of 4 or more go row by row, without TMA
+  // rows per TMA copy
   const int64_t pow2 = block_size & -block_size;
   a.box = static_cast<int>(pow2 > 64 ? 64 : pow2);
-  const uint32_t box = a.box < 4 ? 1 : static_cast<uint32_t>(a.box);
   a.by_block = tree_div(block_size);
   a.by_group = tree_div(Hq / Hkv);
   // a cache without slots: every position is out of range and loads row 0, here of q
   CUtensorMap tm_k;
   if ((rc = get_encoder()) != FP8Q_OK ||
       (rc = make_u8_row_map(&tm_k, num_slots > 0 ? k_cache : q_e4m3, num_slots > 0 ? num_slots : 1,
-                            Hkv * D, box, static_cast<uint32_t>(D),
+                            Hkv * D, static_cast<uint32_t>(a.box), static_cast<uint32_t>(D),
                             D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B)) !=
           FP8Q_OK)
     return rc;

@@ -42,7 +42,7 @@ struct TreeAttnArgs {
   float sm_scale;
   uint16_t *out;               // [total][ldo] bf16
   int64_t ldo;
-  int box;                     // rows per TMA copy: the power of two in block_size, at most 64; 1: row by row
+  int box;                     // rows per TMA copy: the power of two in block_size, at most 64
   uint64_t grid_recip;         // floor((2^64 - 1) / gridDim.x)
   TreeDiv by_block, by_group;  // by block_size and by G = Hq / Hkv
   int row_cap;                 // rows of a partial slot: min(128, max_nodes * Hq / Hkv)
@@ -99,6 +99,10 @@ struct TreeLayout {
   static constexpr int kColS = 0, kColO = 128, kCols = 256;
   static constexpr uint32_t kIdescQK = (1u << 4) | (static_cast<uint32_t>(kTreeN >> 3) << 17) |
                                        (static_cast<uint32_t>(kTreeM >> 4) << 24);
+  // K goes row by row by cp.async where a TMA copy has less than 512 bytes.  40 sequences, heads of 64,
+  // blocks of 4: 65.5 us against 76 by TMA, of 8: 65.8 against 66.6; blocks of 7 by TMA gathers of four
+  // rows: 82.  64 sequences, heads of 128, blocks of 4: 130 against 124, of 16: 128 against 106.
+  static constexpr __host__ __device__ bool by_row(int box) { return box * D < 512; }
   // kind::f16, fp16 operands, B with its columns (dims) contiguous (bit 16)
   static constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) |
                                        (static_cast<uint32_t>(D >> 3) << 17) |
@@ -477,7 +481,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
 
   if (tid == 0) {
     for (int i = 0; i < kTreeStages; ++i) {
-      mbar_init(smem_u32(&sh.k_full[i]), a.box < 4 ? 33 : 1);     // the load warp's lanes and lane 0
+      mbar_init(smem_u32(&sh.k_full[i]), L::by_row(a.box) ? 33 : 1);   // its lanes and lane 0
       mbar_init(smem_u32(&sh.k_free[i]), 1);
       mbar_init(smem_u32(&sh.t_full[i]), 1);
       mbar_init(smem_u32(&sh.t_free[i]), 2);
@@ -569,12 +573,11 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   if (warp == 9) {
     // ---------------------------------------------------------------- load
     // A copy brings `box` consecutive positions of one block; lane i holds the slot of the i-th copy's
-    // first.  Blocks of odd size or 2 mod 4 go by cp.async instead, row by row; then lane i holds the
-    // slots of the positions i and i + 32.  (TMA gathers of four rows were slower there: 16 a tile held
-    // the load warp for 80 % of the time.)
+    // first.  Where a copy would be small, rows go by cp.async; then lane i holds the slots of the
+    // positions i and i + 32.
     TreeCursor pre;
     pre.init(a, G, B, sh.start_b, sh.start_off, hi - lo);
-    const bool by_row = a.box < 4;
+    const bool by_row = L::by_row(a.box);
     const int chunks = kTreeN / a.box, log_box = __ffs(a.box) - 1;
     const int first = by_row ? lane : min(lane, chunks - 1) * a.box;
     int blk[2], off[2];
@@ -864,7 +867,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
               ok = false;
               continue;
             }
-            if (a.box < 4) fence_proxy_async_shared();           // K came by cp.async
+            if (L::by_row(a.box)) fence_proxy_async_shared();    // K came by cp.async
             tc_fence_after();
             const uint64_t kd = tree_sdesc_k<D>(sbase + L::kK + st * L::kTile);
             if (leader) {

@@ -7,6 +7,33 @@
 //   z_j = sm_scale s_q s_k sum_d dec(q[i][h][d]) dec(k_j[g][d])
 //   o[i][h][d] = s_v * sum_j softmax(z)_j dec(v_j[g][d])   -> bf16,   g = h / (Hq / Hkv)
 // A node that sees nothing gets zeros.
+//
+// Products on the tensor cores, accumulators in TMEM.  A row tile is 128 query rows (node, head of the
+// group); a position tile is 64 cached positions of one kv head.  Scores: kind::f8f6f4 on the codes as
+// they are.  Weights: fp16 (at most 2^-11 off, half the bound of bf16 results), written over the scores
+// in TMEM as the next product's A operand; V is converted to fp16, which is exact.  The softmax keeps a
+// reference that lags the running maximum by at most 2^8, so that the accumulators are rescaled rarely.
+//
+// Few rows leave most of a row tile idle: up to 32 (64) rows are repeated four (two) times down it, each
+// repeat takes the weights of its own 16 (32) of a tile's positions (the others are written as zeros),
+// and the repeats are merged at the end.  So every softmax warp works, whatever the draft's size.
+//
+// Work is split evenly whatever the lengths: all items (sequence, kv head, row tile) stand one behind
+// the other on one axis of position tiles, two CTAs per SM take equal shares of it, and what CTAs share
+// of an item is merged by a second kernel in CTA order, so that results do not depend on timing.
+//
+// Roles of a CTA's eleven warps: 0-3 softmax and output, 4-7 V (copies by cp.async, conversion to fp16),
+// 8 MMAs, 9 K (by TMA a copy per run of positions in a block, or row by row), 10 queries.  Every wait is
+// bounded, and a warp's lanes leave it together.
+//
+// Measured (calls back to back, new inputs every time): 64 sequences of 512 to 4096 positions with up to
+// 16 nodes, 32/8 heads of 128: 107 us, 3.0 TB/s of cache and 46 % of the copy rate; one sequence of
+// 131501 positions with 61 nodes 192 us, 685 TFLOP/s; 8 of up to 512 nodes over up to 6000 positions
+// 336 us, 704 TFLOP/s; 40 sequences, 16 heads of 64, blocks of 7: 64 us.  What bounds it is the issue of
+// the roles' instructions and the hand-offs between them (0.46 to 0.53 instructions per cycle and
+// scheduler), with the tensor pipe at 27 %.  The MMA warp runs converged, one lane issuing, so that its
+// operands stay in uniform registers: 128 -> 107 us on the first case.  The roles' code has to stay
+// small: at 170 KB instruction fetch was the largest stall and everything took twice as long.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -234,8 +261,8 @@ __device__ __forceinline__ uint64_t tree_sdesc_k(uint32_t saddr) {
          (static_cast<uint64_t>(B == 128 ? 2 : 4) << 61);
 }
 
-// Bounded waits by a warp and by one thread, short in code: about 2^20 polls of a microsecond at most,
-// then the timeout is recorded and the CTA's roles give up.
+// Bounded wait of a warp, short in code: about 2^20 polls of a microsecond at most, then the timeout is
+// recorded and the CTA's roles give up.  The lanes leave it together.
 __device__ __forceinline__ bool tree_poll(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -248,16 +275,15 @@ __device__ __forceinline__ bool tree_poll(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 constexpr uint32_t kTreePolls = 1u << 20;
-template <bool WARP>
 __device__ __forceinline__ bool tree_wait(const uint64_t &barrier, uint32_t parity,
                                           volatile int *abort_flag) {
   const uint32_t bar = smem_u32(&barrier);
 #pragma unroll 1
   for (uint32_t n = 0;; ++n) {
     const bool ok = tree_poll(bar, parity & 1u);
-    if (WARP ? __all_sync(0xffffffffu, ok) : ok) return true;
+    if (__all_sync(0xffffffffu, ok)) return true;
     const bool stop = *abort_flag != 0 || n >= kTreePolls;
-    if (WARP ? __any_sync(0xffffffffu, stop) : stop) break;
+    if (__any_sync(0xffffffffu, stop)) break;
   }
   if (atomicExch(const_cast<int *>(abort_flag), 1) == 0) record_error(6 /* FP8Q_ERR_TIMEOUT */);
   return false;
@@ -315,7 +341,7 @@ struct TreeShared {
 __device__ __forceinline__ bool tree_take(TreeShared &sh, uint32_t ip, TreePiece &pc) {
   const uint32_t i = ip % kTreePieces;
   pc.t = pc.t_end = 0;
-  if (!tree_wait<true>(sh.piece_full[i], ip / kTreePieces, &sh.abort)) return false;
+  if (!tree_wait(sh.piece_full[i], ip / kTreePieces, &sh.abort)) return false;
   pc = sh.piece[i];
   tree_arrive(sh.piece_free[i]);
   return pc.t_end > 0;
@@ -365,7 +391,7 @@ __device__ __forceinline__ bool tree_tile(TreeShared &sh, uint32_t tmem, uint32_
                                           uint32_t it, bool first, const int64_t *mrow, int words,
                                           int node, int j0, float c2, TreeRow &st) {
   using L = TreeLayout<D>;
-  if (!tree_wait<true>(sh.s_full[it & 1u], it >> 1, &sh.abort)) return false;
+  if (!tree_wait(sh.s_full[it & 1u], it >> 1, &sh.abort)) return false;
   tc_fence_after();
   const uint32_t buf = tmem + L::kColS + 64 * (it & 1u);
   uint32_t sr[16];
@@ -404,7 +430,7 @@ __device__ __forceinline__ bool tree_tile(TreeShared &sh, uint32_t tmem, uint32_
     st.ref = up ? top : st.ref;
     st.l *= f;
     if (!first && __any_sync(0xffffffffu, held)) {
-      if (!tree_wait<true>(sh.pv_done[(it - 1) & 1u], (it - 1) >> 1, &sh.abort)) return false;
+      if (!tree_wait(sh.pv_done[(it - 1) & 1u], (it - 1) >> 1, &sh.abort)) return false;
       tc_fence_after();
 #pragma unroll 1
       for (int d = 0; d < D; d += 16) {
@@ -602,7 +628,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     uint32_t ip = 0;
     auto publish = [&]() {                                       // the piece, or the end
       const uint32_t i = ip % kTreePieces;
-      if (!tree_wait<true>(sh.piece_free[i], (ip / kTreePieces) ^ 1u, &sh.abort)) return false;
+      if (!tree_wait(sh.piece_free[i], (ip / kTreePieces) ^ 1u, &sh.abort)) return false;
       if (lane == 0)
         sh.piece[i] = TreePiece{pre.s.first, pre.b, pre.s.n, pre.s.ctx, pre.g, pre.rt * kTreeM,
                                 min(kTreeM, pre.s.n * G - pre.rt * kTreeM), pre.t,
@@ -618,8 +644,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       if (fresh && !publish()) break;
       if (!pre.live) break;
       // the stage first: the block ids are on their way meanwhile
-      if (!tree_wait<true>(sh.k_free[st], ph, &sh.abort) ||
-          !tree_wait<true>(sh.t_free[st], ph, &sh.abort))
+      if (!tree_wait(sh.k_free[st], ph, &sh.abort) ||
+          !tree_wait(sh.t_free[st], ph, &sh.abort))
         break;
       bool ok;
       int32_t slot[2] = {slot_of(0, &ok), 0};
@@ -687,7 +713,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     }
     // the end, for both pairs of V warps
     for (int i = 0; i < 2; ++i) {
-      if (!tree_wait<true>(sh.t_free[st], ph, &sh.abort)) break;
+      if (!tree_wait(sh.t_free[st], ph, &sh.abort)) break;
       if (lane == 0) sh.tile[st].g = -1;
       tree_arrive(sh.t_full[st]);
       if (++st == kTreeStages) {
@@ -697,7 +723,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     }
     // after a wait that gave up: no copy in flight at exit
     for (uint32_t i = it < kTreeStages ? 0 : it - kTreeStages; i < it; ++i)
-      tree_wait<true>(sh.k_full[i % kTreeStages], i / kTreeStages, &sh.abort);
+      tree_wait(sh.k_full[i % kTreeStages], i / kTreeStages, &sh.abort);
   } else if (warp == 10) {
     // ---------------------------------------------------------------- queries
     constexpr int LPR = D / 16;                                  // 16-byte chunks per row
@@ -722,7 +748,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         if (r < min(pc.rows, step))
           v[k] = *reinterpret_cast<const uint4 *>(source(r) + i % LPR * 16);
       }
-      if (!(ok = tree_wait<true>(sh.q_free, ip ^ 1u, &sh.abort))) break;
+      if (!(ok = tree_wait(sh.q_free, ip ^ 1u, &sh.abort))) break;
 #pragma unroll 1
       for (int i = 256 + lane; i < step * LPR; i += 32) {
         const int r = i / LPR, x = (i % LPR ^ (r & 7)) << 4;
@@ -766,7 +792,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     const uint32_t stage = sbase + L::kV8 + pair * L::kTile + gt * 16;
     for (uint32_t it = pair;; it += 2) {
       const uint32_t st = it % kTreeStages;
-      if (!tree_wait<true>(sh.t_full[st], it / kTreeStages, &sh.abort)) break;
+      if (!tree_wait(sh.t_full[st], it / kTreeStages, &sh.abort)) break;
       const TreeTile &tile = sh.tile[st];
       const int32_t g = tile.g, piece = tile.piece;
       if (g < 0) break;
@@ -780,7 +806,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
       tree_arrive(sh.t_free[st]);
-      if (it >= 2 && !tree_wait<true>(sh.pv_done[pair], (it - 2) >> 1, &sh.abort)) break;
+      if (it >= 2 && !tree_wait(sh.pv_done[pair], (it - 2) >> 1, &sh.abort)) break;
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       uint8_t *dst = smem + L::kV16 + pair * L::kV16Bytes + (ch >> 2) * 8192 + r0 * 128;
       const int at0 = ((ch & 3) * 2 ^ (r0 & 7)) << 4;            // RPS is a multiple of 8
@@ -843,7 +869,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         fresh = left == 0;
         if (fresh) {
           const uint32_t i = ip % kTreePieces;
-          if (!tree_wait<true>(sh.piece_full[i], ip / kTreePieces, &sh.abort)) return false;
+          if (!tree_wait(sh.piece_full[i], ip / kTreePieces, &sh.abort)) return false;
           left = sh.piece[i].t_end - (sh.piece[i].t_end > 0 ? sh.piece[i].t : 0);
           tree_arrive(sh.piece_free[i]);
           ++ip;
@@ -862,8 +888,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         for (int k = 0; k < 2 && ok; ++k) {
           if (fresh == (k == 1)) {
             if (!live) continue;
-            if ((fresh && !tree_wait<true>(sh.q_full, ip - 1, &sh.abort)) ||
-                !tree_wait<true>(sh.k_full[st], ph, &sh.abort)) {
+            if ((fresh && !tree_wait(sh.q_full, ip - 1, &sh.abort)) ||
+                !tree_wait(sh.k_full[st], ph, &sh.abort)) {
               ok = false;
               continue;
             }
@@ -886,8 +912,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
             }
           } else if (it > 0) {
             const uint32_t i = (it - 1) & 1u, pp = (it - 1) >> 1;
-            if (!tree_wait<true>(sh.p_full[i], pp, &sh.abort) ||
-                !tree_wait<true>(sh.v_full[i], pp, &sh.abort)) {
+            if (!tree_wait(sh.p_full[i], pp, &sh.abort) ||
+                !tree_wait(sh.v_full[i], pp, &sh.abort)) {
               ok = false;
               continue;
             }
@@ -935,7 +961,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         ok = tree_tile<D>(sh, tw, col0, 4 >> shift, it, t == pc.t, mrow, words, live ? node : -1,
                           t * kTreeN - pc.ctx, c2, st);
       }
-      ok = ok && tree_wait<true>(sh.pv_done[(it - 1) & 1u], (it - 1) >> 1, &sh.abort);
+      ok = ok && tree_wait(sh.pv_done[(it - 1) & 1u], (it - 1) >> 1, &sh.abort);
       sh.ml[warp][lane][0] = st.ref;
       sh.ml[warp][lane][1] = st.l;
       if (tree_any4(!ok)) break;                                 // no more pieces, or given up

@@ -232,7 +232,7 @@ def test_nan_codes_that_are_not_seen(Hq, Hkv, n):
     np.testing.assert_array_equal(got[~bad], same[~bad])
 
 
-# Small drafts over three or more kv heads: several heads share a row tile of the products.
+# Small drafts over three or more kv heads.
 SHARED = [(3, 3, 20), (4, 4, 64), (10, 5, 16), (32, 8, 16), (32, 8, 7), (12, 4, 21), (40, 5, 8),
           (7, 7, 1), (24, 3, 4)]
 

@@ -300,18 +300,9 @@ __device__ __forceinline__ void tree_arrive_copies(const uint64_t &barrier) {
                : "memory");
 }
 
-template <int N>
-__device__ __forceinline__ void tree_ld(uint32_t taddr, uint32_t (&r)[N]) {
-  if constexpr (N == 64) tmem_ld_32x32b_x64(taddr, r);
-  else if constexpr (N == 32) tmem_ld_32x32b_x32(taddr, r);
-  else tmem_ld_32x32b_x16(taddr, r);
+__device__ __forceinline__ void tree_ld(uint32_t taddr, uint32_t (&r)[16]) {
+  tmem_ld_32x32b_x16(taddr, r);
   tmem_ld_wait(r);
-}
-template <int N>
-__device__ __forceinline__ void tree_st(uint32_t taddr, const uint32_t (&r)[N]) {
-  if constexpr (N == 32) tmem_st_32x32b_x32(taddr, r);
-  else if constexpr (N == 16) tmem_st_32x32b_x16(taddr, r);
-  else tmem_st_32x32b_x8(taddr, r);
 }
 
 // What the CTA's roles share.
@@ -403,13 +394,13 @@ __device__ __forceinline__ bool tree_tile(TreeShared &sh, uint32_t tmem, uint32_
 #pragma unroll 1
     for (int c = 0; c < 16 * chunks; c += 16, seen >>= 16) {
       __syncwarp();                                              // whole warps at the TMEM loads
-      tree_ld<16>(buf + col0 + c, sr);
+      tree_ld(buf + col0 + c, sr);
       const uint32_t bits = static_cast<uint32_t>(seen);
 #pragma unroll
       for (int j = 0; j < 16; ++j)
         if (!((bits >> j) & 1)) sr[j] = 0xFF800000u;
       __syncwarp();
-      tree_st<16>(buf + col0 + c, sr);
+      tmem_st_32x32b_x16(buf + col0 + c, sr);
     }
     tmem_st_wait();
   }
@@ -418,7 +409,7 @@ __device__ __forceinline__ bool tree_tile(TreeShared &sh, uint32_t tmem, uint32_
 #pragma unroll 1
   do {
     --c;
-    tree_ld<16>(buf + col0 + 16 * c, sr);
+    tree_ld(buf + col0 + 16 * c, sr);
 #pragma unroll
     for (int j = 0; j < 16; ++j) mx[j & 1] = fmaxf(mx[j & 1], __uint_as_float(sr[j]));
   } while (c > 0);
@@ -435,10 +426,10 @@ __device__ __forceinline__ bool tree_tile(TreeShared &sh, uint32_t tmem, uint32_
 #pragma unroll 1
       for (int d = 0; d < D; d += 16) {
         uint32_t o[16];
-        tree_ld<16>(tmem + L::kColO + d, o);
+        tree_ld(tmem + L::kColO + d, o);
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-        tree_st<16>(tmem + L::kColO + d, o);
+        tmem_st_32x32b_x16(tmem + L::kColO + d, o);
       }
     }
   }
@@ -456,15 +447,15 @@ __device__ __forceinline__ bool tree_tile(TreeShared &sh, uint32_t tmem, uint32_
       sum = f2_add_rn(sum, w);
       pk[j / 2] = f32x2_to_f16x2(w.x, w.y);
     }
-    tree_st<8>(buf + col0 / 2 + 8 * c, pk);
+    tmem_st_32x32b_x8(buf + col0 / 2 + 8 * c, pk);
     if (++c >= chunks) break;
-    tree_ld<16>(buf + col0 + 16 * c, sr);
+    tree_ld(buf + col0 + 16 * c, sr);
   }
   // a repeat of a row has no weight at the other repeats' positions
 #pragma unroll 1
   for (int i = 8 * chunks; i < 32; i += 8) {
     const uint32_t z[8] = {};
-    tree_st<8>(buf + ((col0 / 2 + i) & 31u), z);
+    tmem_st_32x32b_x8(buf + ((col0 / 2 + i) & 31u), z);
   }
   st.l += sum.x + sum.y;
   tmem_st_wait();
@@ -1018,7 +1009,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       for (int c = 0; c < D; c += 16) {
         uint32_t o[16];
         __syncwarp();
-        tree_ld<16>(tw + L::kColO + c, o);
+        tree_ld(tw + L::kColO + c, o);
         float4 v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)

@@ -714,7 +714,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     }
     // after a wait that gave up: no copy in flight at exit
     for (uint32_t i = it < kTreeStages ? 0 : it - kTreeStages; i < it; ++i)
-      tree_wait(sh.k_full[i % kTreeStages], i / kTreeStages, &sh.abort);
+      wait_drain(smem_u32(&sh.k_full[i % kTreeStages]), i / kTreeStages & 1u);
   } else if (warp == 10) {
     // ---------------------------------------------------------------- queries
     constexpr int LPR = D / 16;                                  // 16-byte chunks per row

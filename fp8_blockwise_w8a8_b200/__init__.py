@@ -251,12 +251,16 @@ def _on_stream(device, stream, run):
 
 def paged_batch_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
                        free_blocks: torch.Tensor, free_count: torch.Tensor, block_size: int,
-                       max_tokens: int, out=None, stream=None):
+                       max_tokens: int, out=None, stream=None, held_blocks=None):
     """Block tables and slot maps from request lengths (fp8q_paged_batch_tables): int32 [B] cached
     and added positions, block_table int32 [B, max_blocks] (extended in place), the stack of free
     block ids int32 [num_free] and its height int32 [1] -> (cu_tokens int32 [B + 1], seq_lens
     int32 [B], slots int64 [max_tokens], positions int64 [max_tokens], free_left int32 [1]).
-    `out`: those five, to be written."""
+    `out`: those five, to be written.
+    held_blocks int32 [B] (fp8q_paged_batch_tables_held): the blocks each request holds, also behind
+    its context; a sixth result is their number afterwards, the next call's held_blocks.  Where tokens
+    can be rejected, pass it: without it the blocks of rejected tokens are popped anew, and lost unless
+    the caller puts them back on the stack."""
     dev, B = ctx_lens.device, ctx_lens.shape[0]
     i32, i64 = torch.int32, torch.int64
     _expect(dev, ctx_lens=(ctx_lens, i32, (B,)), new_lens=(new_lens, i32, (B,)),
@@ -266,19 +270,29 @@ def paged_batch_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_tab
         _expect(dev, cu_tokens=(out[0], i32, (B + 1,)), seq_lens=(out[1], i32, (B,)),
                 slots=(out[2], i64, (max_tokens,)), positions=(out[3], i64, (max_tokens,)),
                 free_left=(out[4], i32, (1,)))
+    if held_blocks is not None:
+        _expect(dev, held_blocks=(held_blocks, i32, (B,)))
+        if out is not None:
+            if len(out) < 6:
+                raise ValueError("out must have a sixth tensor for the held blocks")
+            _expect(dev, held_out=(out[5], i32, (B,)))
 
     def run(st):
-        cu, lens, slots, positions, left = out or (
+        cu, lens, slots, positions, left = out[:5] if out else (
             ctx_lens.new_empty(B + 1), ctx_lens.new_empty(B),
             torch.empty(max_tokens, dtype=i64, device=dev),
             torch.empty(max_tokens, dtype=i64, device=dev), ctx_lens.new_empty(1))
-        rc = _lib.lib().fp8q_paged_batch_tables(
+        held = ()
+        if held_blocks is not None:
+            held = (out[5] if out else ctx_lens.new_empty(B),)
+        rc = _lib.lib().fp8q_paged_batch_tables_held(
             ctx_lens.data_ptr(), new_lens.data_ptr(), B, int(block_size), block_table.data_ptr(),
             block_table.shape[1], free_blocks.data_ptr(), free_blocks.shape[0],
-            free_count.data_ptr(), left.data_ptr(), int(max_tokens), cu.data_ptr(),
+            free_count.data_ptr(), left.data_ptr(), _ptr(held_blocks),
+            held[0].data_ptr() if held else None, int(max_tokens), cu.data_ptr(),
             lens.data_ptr(), slots.data_ptr(), positions.data_ptr(), st)
         _lib.check(rc, "fp8q_paged_batch_tables")
-        return cu, lens, slots, positions, left
+        return cu, lens, slots, positions, left, *held
     return _on_stream(dev, stream, run)
 
 

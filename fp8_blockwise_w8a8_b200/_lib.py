@@ -65,6 +65,8 @@ SIGNATURES = {
     "fp8q_attention_decode_workspace_bytes": (_I, [_I64, _I64, _I64, _I64, _I64, _P]),
     "fp8q_paged_batch_tables": (_I, [_P, _P, _I64, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _P,
                                      _P, _P, _P, _P]),
+    "fp8q_paged_batch_tables_held": (_I, [_P, _P, _I64, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P,
+                                          _I64, _P, _P, _P, _P, _P]),
     "fp8q_tree_mask": (_I, [_P, _P, _P, _I64, _I64, _I64, _P, _I64, _P, _P]),
     "fp8q_attention_tree": (_I, [_P, _I64, _P, _P, _I64, _P, _P, _I64, _P, _P, _P, _I64, _I64,
                                  _I64, _I64, _I64, _I64, _I64, _I64, _I64, ctypes.c_float, _P,

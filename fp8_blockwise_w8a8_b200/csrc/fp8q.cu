@@ -446,7 +446,7 @@ int64_t attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t max_seq
 
 extern "C" {
 
-int fp8q_abi_version(void) { return (1 << 16) | 7; }
+int fp8q_abi_version(void) { return (1 << 16) | 8; }
 
 const char *fp8q_status_string(int status) {
   switch (status) {
@@ -1041,32 +1041,34 @@ int fp8q_attention_decode(const void *q_e4m3, int64_t ldq, const void *k_cache,
   return launch_status();
 }
 
-int fp8q_paged_batch_tables(const int32_t *ctx_lens, const int32_t *new_lens, int64_t B,
-                            int64_t block_size, int32_t *block_table, int64_t max_blocks,
-                            const int32_t *free_blocks, int64_t num_free,
-                            const int32_t *free_count, int32_t *free_left, int64_t max_tokens,
-                            int32_t *cu_tokens, int32_t *seq_lens, int64_t *slots,
-                            int64_t *positions, cudaStream_t stream) {
+int fp8q_paged_batch_tables_held(const int32_t *ctx_lens, const int32_t *new_lens, int64_t B,
+                                 int64_t block_size, int32_t *block_table, int64_t max_blocks,
+                                 const int32_t *free_blocks, int64_t num_free,
+                                 const int32_t *free_count, int32_t *free_left,
+                                 const int32_t *held_blocks, int32_t *held_out,
+                                 int64_t max_tokens, int32_t *cu_tokens, int32_t *seq_lens,
+                                 int64_t *slots, int64_t *positions, cudaStream_t stream) {
   if (B < 0 || B > fp8q::kTablesMaxB || block_size <= 0 || block_size > INT32_MAX ||
       max_blocks < 0 || max_blocks > INT32_MAX / block_size || num_free < 0 ||
       num_free > INT32_MAX || max_tokens < 0 || max_tokens > INT32_MAX)
     return FP8Q_ERR_SHAPE;
   if (!free_count || !free_left || !cu_tokens || (num_free > 0 && !free_blocks) ||
       (B > 0 && (!ctx_lens || !new_lens || !seq_lens || (max_blocks > 0 && !block_table))) ||
-      (max_tokens > 0 && (!slots || !positions)))
+      (max_tokens > 0 && (!slots || !positions)) || (B > 0 && !held_blocks != !held_out))
     return FP8Q_ERR_NULL;
   if (!aligned_to(ctx_lens, 4) || !aligned_to(new_lens, 4) || !aligned_to(block_table, 4) ||
       !aligned_to(free_blocks, 4) || !aligned_to(free_count, 4) || !aligned_to(free_left, 4) ||
       !aligned_to(cu_tokens, 4) || !aligned_to(seq_lens, 4) || !aligned_to(slots, 8) ||
-      !aligned_to(positions, 8))
+      !aligned_to(positions, 8) || !aligned_to(held_blocks, 4) || !aligned_to(held_out, 4))
     return FP8Q_ERR_ALIGN;
   // every CTA reads the inputs while the first one writes the results
-  const void *in[] = {ctx_lens, new_lens, free_count};
-  const int64_t in_bytes[] = {4 * B, 4 * B, 4};
-  const void *res[] = {free_left, cu_tokens, seq_lens};
-  const int64_t res_bytes[] = {4, 4 * (B + 1), 4 * B};
-  for (int i = 0; i < 3; ++i)
-    for (int j = 0; j < 3; ++j)
+  const int64_t held_bytes = held_blocks ? 4 * B : 0;
+  const void *in[] = {ctx_lens, new_lens, free_count, held_blocks};
+  const int64_t in_bytes[] = {4 * B, 4 * B, 4, held_bytes};
+  const void *res[] = {free_left, cu_tokens, seq_lens, held_out};
+  const int64_t res_bytes[] = {4, 4 * (B + 1), 4 * B, held_bytes};
+  for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < 4; ++j)
       if (overlap(in[i], in_bytes[i], res[j], res_bytes[j])) return FP8Q_ERR_ARG;
   DeviceState *st = nullptr;
   const int rc = device_state(&st);
@@ -1083,6 +1085,8 @@ int fp8q_paged_batch_tables(const int32_t *ctx_lens, const int32_t *new_lens, in
   a.num_free = num_free;
   a.free_count = free_count;
   a.free_left = free_left;
+  a.held = held_blocks;
+  a.held_out = held_out;
   a.max_tokens = max_tokens;
   a.cu = cu_tokens;
   a.seq_lens = seq_lens;
@@ -1098,6 +1102,17 @@ int fp8q_paged_batch_tables(const int32_t *ctx_lens, const int32_t *new_lens, in
   if (many) fp8q::k_paged_tables<4><<<grid, fp8q::kTablesThreads, 8 * (B + 1), stream>>>(a);
   else fp8q::k_paged_tables<1><<<grid, fp8q::kTablesThreads, 8 * (B + 1), stream>>>(a);
   return launch_status();
+}
+
+int fp8q_paged_batch_tables(const int32_t *ctx_lens, const int32_t *new_lens, int64_t B,
+                            int64_t block_size, int32_t *block_table, int64_t max_blocks,
+                            const int32_t *free_blocks, int64_t num_free,
+                            const int32_t *free_count, int32_t *free_left, int64_t max_tokens,
+                            int32_t *cu_tokens, int32_t *seq_lens, int64_t *slots,
+                            int64_t *positions, cudaStream_t stream) {
+  return fp8q_paged_batch_tables_held(ctx_lens, new_lens, B, block_size, block_table, max_blocks,
+                                      free_blocks, num_free, free_count, free_left, nullptr, nullptr,
+                                      max_tokens, cu_tokens, seq_lens, slots, positions, stream);
 }
 
 int fp8q_tree_mask(const int32_t *parents, const int32_t *cu_nodes, const int32_t *ctx_lens,

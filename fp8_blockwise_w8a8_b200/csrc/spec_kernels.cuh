@@ -28,6 +28,8 @@ struct TablesArgs {
   int64_t num_free;
   const int32_t *free_count;
   int32_t *free_left;
+  const int32_t *held;                 // [B] or null: blocks already held, beyond the context's too
+  int32_t *held_out;                   // [B] or null
   int64_t max_tokens;
   int32_t *cu, *seq_lens;              // [B + 1], [B]
   int64_t *slots, *positions;          // [max_tokens]
@@ -53,6 +55,16 @@ __device__ __forceinline__ int64_t cta_exclusive_scan(int64_t v, int64_t *s_warp
   }
   *total = all;
   return before + x - v;
+}
+
+// Blocks that request b holds: those of its c cached positions, and where the caller keeps count, those
+// left from drafts whose nodes were rejected.
+__device__ __forceinline__ uint32_t tables_have(const TablesArgs &a, int b, uint32_t c, bool *bad) {
+  const uint32_t have = c / a.block_size + (c % a.block_size != 0);
+  if (!a.held) return have;
+  const int32_t h = a.held[b], most = static_cast<int32_t>(a.max_blocks);  // at most INT32_MAX
+  *bad |= h < 0 || h > most;
+  return max(have, static_cast<uint32_t>(max(0, min(h, most))));
 }
 
 // Request b has c = ctx_lens[b] cached positions in ceil(c / bs) blocks and adds n = new_lens[b]
@@ -90,7 +102,8 @@ __global__ void __launch_bounds__(kTablesThreads) k_paged_tables(const TablesArg
     const int64_t lo = first < a.max_tokens ? first : a.max_tokens;
     const int64_t hi = first + n < a.max_tokens ? first + n : a.max_tokens;
     bad |= hi != first + n;
-    const int64_t have = (c + bs - 1) / bs, want = (c + (hi - lo) + bs - 1) / bs;
+    const int64_t have = b < a.B ? tables_have(a, b, static_cast<uint32_t>(c), &bad) : 0;
+    const int64_t want = max(have, (c + (hi - lo) + bs - 1) / bs);
     const int64_t nb = blocks + cta_exclusive_scan(want - have, s_warp, &sum);
     blocks += sum;
     if (b < a.B) {
@@ -114,6 +127,17 @@ __global__ void __launch_bounds__(kTablesThreads) k_paged_tables(const TablesArg
       a.cu[a.B] = total;
       *a.free_left = static_cast<int32_t>(avail > blocks ? avail - blocks : 0);
       bad |= blocks > avail;
+    }
+  }
+  if (lead && a.held_out) {
+    // where the stack runs short a request gets its lower entries, and the later requests none
+    if (tid == 0) s_nb[a.B] = static_cast<int32_t>(blocks);
+    __syncthreads();
+    for (int b = tid; b < a.B; b += kTablesThreads) {
+      const int64_t c0 = a.ctx_lens[b], need = s_nb[b + 1] - s_nb[b], left = avail - s_nb[b];
+      const uint32_t c = static_cast<uint32_t>(c0 < 0 ? 0 : (c0 > a.capacity ? a.capacity : c0));
+      const int64_t got = left < 0 ? 0 : (left < need ? left : need);
+      a.held_out[b] = static_cast<int32_t>(tables_have(a, b, c, &bad) + got);
     }
   }
   if (lead && bad) record_error(9 /* FP8Q_ERR_RANGE */);
@@ -148,7 +172,7 @@ __global__ void __launch_bounds__(kTablesThreads) k_paged_tables(const TablesArg
         pos = c + static_cast<uint32_t>(t - s_cu[lo]);
         blk = pos / bs;
         off = pos - blk * bs;
-        have = c / bs + (c % bs != 0);
+        have = tables_have(a, lo, c, &bad);
         fetch = true;
       } else {
         ++pos;

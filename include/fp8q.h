@@ -334,6 +334,8 @@ int fp8q_attention_decode_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, in
  *   fp8q_kv_cache_write      writes the nodes' K and V at those slots
  *   fp8q_attention_tree      attention of every node over the context and its ancestors
  *   fp8q_kv_cache_accept     moves the accepted nodes' rows up behind the context
+ * and the next step goes on from new_lens, free_left and, as nodes were rejected, held_out
+ * (fp8q_paged_batch_tables_held).
  * All lengths, offsets and tables are DEVICE memory, so that a step can be captured in a CUDA graph
  * and replayed with other lengths.  The pages define no such step; it is built on the cache of
  * FP8-RL abstract, item (ii).
@@ -362,6 +364,9 @@ int fp8q_attention_decode_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, in
  * B <= 16384, max_blocks * block_size and max_tokens <= 2^31 - 1 (FP8Q_ERR_SHAPE).  free_left,
  * cu_tokens and seq_lens must not overlap ctx_lens, new_lens or free_count (FP8Q_ERR_ARG), nor any
  * other array another (undefined results).  int32 arrays 4-byte, int64 arrays 8-byte aligned.
+ * A request holds ceil(ctx / block_size) blocks and no more: before a call whose contexts end ahead of
+ * the blocks of the call before (nodes were rejected), the caller puts the surplus back on the stack, or
+ * calls fp8q_paged_batch_tables_held.
  * One launch; B = 0 is a batch without requests (T = 0). */
 int fp8q_paged_batch_tables(const int32_t *ctx_lens, const int32_t *new_lens, int64_t B,
                             int64_t block_size, int32_t *block_table, int64_t max_blocks,
@@ -369,6 +374,23 @@ int fp8q_paged_batch_tables(const int32_t *ctx_lens, const int32_t *new_lens, in
                             const int32_t *free_count, int32_t *free_left, int64_t max_tokens,
                             int32_t *cu_tokens, int32_t *seq_lens, int64_t *slots,
                             int64_t *positions, cudaStream_t stream);
+
+/* The same where requests keep the blocks of rejected nodes for their next tokens: request b holds the
+ * entries 0 .. have - 1 of its row, have = max(held_blocks[b], ceil(ctx / block_size)), and entries are
+ * popped from there on.
+ *   held_blocks  [B] int32, read; held_out [B] int32, written: the entries held afterwards, the next
+ *                call's held_blocks (entries that the stack could not give are not among them, and are
+ *                popped by a later call).  A request that ends gives back that many entries of its row
+ * Recorded as FP8Q_ERR_RANGE besides: held_blocks outside [0, max_blocks] (clamped).  held_out must not
+ * overlap ctx_lens, new_lens or free_count, and none of the results held_blocks (FP8Q_ERR_ARG).  Both
+ * NULL: fp8q_paged_batch_tables. */
+int fp8q_paged_batch_tables_held(const int32_t *ctx_lens, const int32_t *new_lens, int64_t B,
+                                 int64_t block_size, int32_t *block_table, int64_t max_blocks,
+                                 const int32_t *free_blocks, int64_t num_free,
+                                 const int32_t *free_count, int32_t *free_left,
+                                 const int32_t *held_blocks, int32_t *held_out,
+                                 int64_t max_tokens, int32_t *cu_tokens, int32_t *seq_lens,
+                                 int64_t *slots, int64_t *positions, cudaStream_t stream);
 
 /* Ancestor masks of drafted trees.  The nodes of sequence b are rows cu_nodes[b] ..
  * cu_nodes[b + 1] - 1; node i's parent is parents[row] in [0, i), or -1 for a child of the context.

@@ -14,15 +14,19 @@ def e4m3_values() -> np.ndarray:
     return v
 
 
-def batch_tables(ctx, new, table, block_size, free_blocks, free_count, max_tokens):
+def batch_tables(ctx, new, table, block_size, free_blocks, free_count, max_tokens, held=None):
     """(table, cu, seq_lens, slots, positions, free_left) for lengths within the table and tokens
-    within max_tokens; blocks that the stack cannot give are -1."""
+    within max_tokens; blocks that the stack cannot give are -1.  `held`: the blocks that each request
+    holds already; their number afterwards is appended to the results."""
     table = np.array(table, np.int64)
     stack = list(free_blocks[:free_count])
-    slots, positions, cu = [], [], [0]
+    slots, positions, cu, after = [], [], [0], []
     for b, (c, n) in enumerate(zip(ctx, new)):
-        for k in range(-(-c // block_size), -(-(c + n) // block_size)):
+        have = max(-(-c // block_size), 0 if held is None else held[b])
+        for k in range(have, -(-(c + n) // block_size)):
+            have += bool(stack)
             table[b, k] = stack.pop() if stack else -1
+        after.append(have)
         for p in range(c, c + n):
             blk = table[b, p // block_size]
             slots.append(-1 if blk < 0 else blk * block_size + p % block_size)
@@ -31,7 +35,8 @@ def batch_tables(ctx, new, table, block_size, free_blocks, free_count, max_token
     behind = max_tokens - len(slots)
     return (table, np.array(cu), np.array(ctx, np.int64) + np.array(new, np.int64),
             np.array(slots + [-1] * behind, np.int64),
-            np.array(positions + [0] * behind, np.int64), len(stack))
+            np.array(positions + [0] * behind, np.int64), len(stack),
+            *([] if held is None else [np.array(after, np.int64)]))
 
 
 def tree_sees(parents) -> np.ndarray:

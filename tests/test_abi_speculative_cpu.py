@@ -159,3 +159,41 @@ def test_binding_refuses_other_types_shapes_and_devices():
         fq.kv_cache_accept(k, k, table, ctx, cu, z((2, 3), **i32), z(3, **i32), 16)
     with pytest.raises(ValueError, match="v_cache"):
         fq.kv_cache_accept(k, k.view(1, 64, 256), table, ctx, cu, z((2, 3), **i32), ctx, 16)
+
+
+def test_paged_batch_tables_held(L):
+    ok = dict(ctx=FAKE, new=FAKE + MB, B=8, bs=16, bt=FAKE + 2 * MB, maxb=4, fb=FAKE + 3 * MB, nf=9,
+              fc=FAKE + 4 * MB, fl=FAKE + 5 * MB, held=FAKE + 10 * MB, hout=FAKE + 11 * MB, mt=64,
+              cu=FAKE + 6 * MB, sl=FAKE + 7 * MB, slots=FAKE + 8 * MB, pos=FAKE + 9 * MB)
+
+    def call(**kw):
+        a = dict(ok, **kw)
+        return L.fp8q_paged_batch_tables_held(*(a[k] for k in ok), None)
+    for name in ("held", "hout"):                                 # one without the other
+        assert call(**{name: None}) == NULL, name
+        assert call(**{name: ok[name] + 2}) == ALIGN, name
+    for kw in (dict(hout=ok["held"]), dict(hout=ok["held"] + 28), dict(hout=ok["ctx"]),
+               dict(hout=ok["fc"] - 4), dict(sl=ok["held"] + 4), dict(fl=ok["held"]),
+               dict(cu=ok["held"] - 32)):
+        assert call(**kw) == ARG, kw
+    assert call(B=-1) == SHAPE
+    _no_device(call)
+    _no_device(lambda: call(held=None, hout=None))
+    _no_device(lambda: call(hout=ok["held"] + 32))
+    _no_device(lambda: call(B=0, held=None))
+
+
+def test_binding_of_held_blocks_refuses():
+    i32 = dict(dtype=torch.int32)
+    z = torch.zeros
+    args = (z(2, **i32), z(2, **i32), z((2, 4), **i32), z(9, **i32), z(1, **i32), 16, 8)
+    for held in (z(3, **i32), z(2), z(4, **i32)[::2]):
+        with pytest.raises(ValueError, match="held_blocks"):
+            fq.paged_batch_tables(*args, held_blocks=held)
+    five = (z(3, **i32), z(2, **i32), z(8, dtype=torch.int64), z(8, dtype=torch.int64), z(1, **i32))
+    with pytest.raises(ValueError, match="sixth"):
+        fq.paged_batch_tables(*args, held_blocks=z(2, **i32), out=five)
+    with pytest.raises(ValueError, match="held_out"):
+        fq.paged_batch_tables(*args, held_blocks=z(2, **i32), out=(*five, z(3, **i32)))
+    with pytest.raises(ValueError, match="CUDA"):
+        fq.paged_batch_tables(*args, held_blocks=z(2, **i32), out=(*five, z(2, **i32)))

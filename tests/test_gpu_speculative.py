@@ -136,6 +136,103 @@ def test_tables_step_after_step_in_a_graph():
     assert fq.check_device_error() == 0
 
 
+@pytest.mark.parametrize("bs,spare", [(16, 40), (5, 50), (1, 330)])
+def test_many_steps_with_rejections_keep_every_block(bs, spare):
+    """Speculative steps of tables and acceptance, each from the device results of the one before, with
+    most nodes rejected: after every step each block id is in exactly one held place or on the stack,
+    the requests hold no more than their longest reach so far, and requests that end give back what
+    they hold.  More steps than the stack could feed if the blocks of rejected nodes were popped anew."""
+    B, n_hi, steps, width = 9, 16, 60, 400
+    rng = np.random.default_rng(bs)
+    ctx = rng.integers(0, 40, B)
+    have = -(-ctx // bs)
+    perm = rng.permutation(int(have.sum()) + B * (-(-n_hi // bs) + 1) + spare).astype(np.int32)
+    table = np.full((B, width), -1, np.int32)
+    at = 0
+    for b in range(B):
+        table[b, :have[b]] = perm[at:at + have[b]]
+        at += have[b]
+    stack = np.zeros(len(perm), np.int32)
+    stack[:len(perm) - at] = perm[at:]
+    dctx, dbt, dfree = i32(ctx), i32(table), i32(stack)
+    count, held = i32([len(perm) - at]), i32(np.zeros(B))
+    cache = torch.zeros((len(perm) * bs, 16), dtype=torch.uint8, device="cuda")
+    reach, popped_anew = have.copy(), 0
+    for step in range(steps):
+        n = rng.integers(0, n_hi + 1, B)
+        accepted = np.minimum(n, rng.integers(0, 2, B))          # at most one
+        wtable, wcu, wlens, wslots, _, wleft, wheld = spec.batch_tables(
+            ctx, n, host(dbt), bs, host(dfree), int(host(count)[0]), B * n_hi, held=host(held))
+        cu, lens, slots, _, count, held = fq.paged_batch_tables(dctx, i32(n), dbt, dfree, count, bs,
+                                                                B * n_hi, held_blocks=held)
+        for got, ref in zip((dbt, cu, lens, slots, count, held),
+                            (wtable, wcu, wlens, wslots, [wleft], wheld)):
+            np.testing.assert_array_equal(host(got), ref)
+        assert (host(slots)[:n.sum()] >= 0).all()
+        path = np.array([[max(0, k - 1)] for k in n])            # the last node, where there is one
+        dctx = fq.kv_cache_accept(cache, cache.clone(), dbt, dctx, cu, i32(path), i32(accepted), bs)
+        popped_anew += (-(-(ctx + n) // bs) - -(-ctx // bs)).sum()
+        reach = np.maximum(reach, -(-(ctx + n) // bs))
+        np.testing.assert_array_equal(host(held), reach)
+        ctx = ctx + accepted
+        np.testing.assert_array_equal(host(dctx), ctx)
+        ids = np.concatenate([host(dbt)[b, :h] for b, h in enumerate(host(held))] +
+                             [host(dfree)[:host(count)[0]]])
+        np.testing.assert_array_equal(np.sort(ids), np.arange(len(perm)))
+        if step % 20 == 19:                                      # request 4 ends, another begins
+            h, c = int(host(held)[4]), int(host(count)[0])
+            dfree[c:c + h] = dbt[4, :h]
+            count += h
+            held[4], dctx[4], ctx[4], reach[4] = 0, 0, 0, 0
+    assert popped_anew > len(perm) - have.sum()
+    assert fq.check_device_error() == 0
+
+
+def test_tables_held_blocks_where_the_stack_runs_short():
+    """What the stack cannot give is not held, and is popped by the next call; counts out of range are
+    clamped and recorded; a context beyond the count holds its own blocks."""
+    table = [[3, 5, -1], [6, 7, 9], [0, -1, -1]]
+    bt = i32(table)
+    args = lambda ctx, new, free, count: (i32(ctx), i32(new), bt, i32(free), i32([count]), 4, 16)
+    out = fq.paged_batch_tables(*args([4, 1, 4], [6, 2, 8], [8, 2], 2), held_blocks=i32([2, 3, 0]))
+    assert fq.check_device_error() == RANGE
+    want = spec.batch_tables([4, 1, 4], [6, 2, 8], table, 4, [8, 2], 2, 16, held=[2, 3, 0])
+    for got, ref in zip((bt, *out), (*want[:5], [want[5]], want[6])):
+        np.testing.assert_array_equal(host(got), ref)
+    out = fq.paged_batch_tables(*args([4, 1, 4], [6, 2, 8], [1], 1), held_blocks=out[5])
+    assert fq.check_device_error() == 0
+    assert host(bt).tolist() == [[3, 5, 2], [6, 7, 9], [0, 8, 1]]
+    assert host(out[5]).tolist() == [3, 3, 3] and host(out[4]).tolist() == [0]
+    out = fq.paged_batch_tables(*args([4, 1, 4], [6, 2, 8], [1], 1), held_blocks=i32([-1, 3, 99]))
+    assert fq.check_device_error() == RANGE
+    assert host(out[5]).tolist() == [2, 3, 3] and host(out[4]).tolist() == [0]
+    assert host(bt).tolist() == [[3, 1, -1], [6, 7, 9], [0, 8, 1]]
+    assert host(out[2])[:6].tolist() == [4, 5, 6, 7, -1, -1]
+
+
+def test_tables_held_blocks_of_a_large_batch():
+    """More requests than a CTA has threads and more tokens than one thread's groups, with counts at
+    random between the context's blocks and the table's end."""
+    ctx, new, table, free = _tables_case(1500, 64, 500, 300, 21)
+    rng = np.random.default_rng(22)
+    have, want = -(-ctx // 64), -(-(ctx + new) // 64)
+    held = rng.integers(0, want + 2)
+    for b in range(1500):                                        # ids for the blocks held beyond
+        for k in range(have[b], held[b]):
+            table[b, k] = 10 ** 6 + 100 * b + k
+    total = int(new.sum()) + 5
+    assert total > 2 * 148 * 512
+    ref = spec.batch_tables(ctx, new, table, 64, free, len(free), total, held=held)
+    bt, out = i32(table), (i32(np.zeros(1501)), i32(np.zeros(1500)), torch.empty(
+        total, dtype=torch.int64, device="cuda"), torch.empty(total, dtype=torch.int64, device="cuda"),
+        i32([0]), i32(np.zeros(1500)))
+    got = fq.paged_batch_tables(i32(ctx), i32(new), bt, i32(free), i32([len(free)]), 64, total, out=out,
+                                held_blocks=i32(held))
+    for x, y in zip((bt, *got), (*ref[:5], [ref[5]], ref[6])):
+        np.testing.assert_array_equal(host(x), y)
+    assert got[5].data_ptr() == out[5].data_ptr() and fq.check_device_error() == 0
+
+
 # --- ancestor masks -------------------------------------------------------------------------------
 
 def _parents(n, rng, kind):

@@ -75,3 +75,14 @@ def test_accept_by_hand():
     want[11] = k[0]
     np.testing.assert_array_equal(got, want)
     assert lens.tolist() == [4]
+
+
+def test_batch_tables_with_blocks_held():
+    """By hand, blocks of 4: request 0 holds its context's block and one behind it (two of its tokens
+    need a third), request 1 holds more than it needs, request 2 meets the end of the stack and holds
+    only what it got."""
+    table = [[3, 5, -1], [6, 7, 9], [0, -1, -1]]
+    got = spec.batch_tables([4, 1, 4], [6, 2, 8], table, 4, [8, 2], 2, 16, held=[2, 3, 0])
+    assert got[0].tolist() == [[3, 5, 2], [6, 7, 9], [0, 8, -1]]
+    assert got[3].tolist() == [20, 21, 22, 23, 8, 9, 25, 26, 32, 33, 34, 35, -1, -1, -1, -1]
+    assert got[5] == 0 and got[6].tolist() == [3, 3, 2]

@@ -309,7 +309,8 @@ __device__ __forceinline__ void tree_ld(uint32_t taddr, uint32_t (&r)[16]) {
 constexpr int kTreePieces = 4;   // descriptors in the ring
 struct TreeTile {                // for the V warps
   int32_t slot[kTreeN];          // cache rows of the tile's positions, -1 where there is none
-  int32_t g, piece;              // kv head (-1: no more tiles), 1 + index of the piece
+  int32_t g;                     // kv head (-1: no more tiles)
+  int32_t piece;                 // 2 (1 + index of the piece), 1 more where the tile lies in the context
 };
 struct TreeShared {
   uint64_t k_full[kTreeStages], k_free[kTreeStages], t_full[kTreeStages], t_free[kTreeStages];
@@ -323,7 +324,7 @@ struct TreeShared {
   int64_t warp_sum[kTreeThreads / 32];
   uint32_t tmem;
   int abort;
-  int nan_piece;                 // 1 + index of the last piece with a NaN code in V
+  int nan_piece;                 // 1 + index of the last piece with a NaN code in V that was taken out
   float ml[4][32][2];
   float4 o[4][32][5];            // 16 columns, rows 80 bytes apart
 };
@@ -338,15 +339,17 @@ __device__ __forceinline__ bool tree_take(TreeShared &sh, uint32_t ip, TreePiece
   return pc.t_end > 0;
 }
 
-// The dims of kv head g that are NaN in a value row seen by row (node i) among the positions of
-// [t, t_end) whose column within its tile lies in [c0, c0 + nc).  Runs only where V holds NaN codes.
+// The dims of kv head g that are NaN in a value row seen by row (node i), among the positions behind the
+// tiles that lie in the context and within [t, t_end), whose column within its tile lies in
+// [c0, c0 + nc).  Runs only where a NaN code was taken out of V, over 17 tiles at most (1024 nodes): a
+// walk over the whole context once took 0.33 us a position, and the waits of other roles have limits.
 template <int D>
 __device__ __noinline__ uint4 tree_nan_dims(const TreeAttnArgs &a, TreePiece c, int i, int c0,
                                             int nc) {
   uint32_t dims[4] = {};
   const int words = (a.max_nodes + 63) / 64;
   const int64_t *mrow = a.mask ? a.mask + (c.first + i) * a.ldm : nullptr;
-  for (int tile = c.t; tile < c.t_end; ++tile) {
+  for (int tile = max(c.t, c.ctx / kTreeN); tile < c.t_end; ++tile) {
     const uint64_t bits = tree_bits(mrow, words, i, tile * kTreeN - c.ctx);
     for (int col = c0; col < c0 + nc; ++col) {
       const int pos = tile * kTreeN + col;
@@ -354,13 +357,18 @@ __device__ __noinline__ uint4 tree_nan_dims(const TreeAttnArgs &a, TreePiece c, 
       const int32_t blk = a.block_table[c.b * a.max_blocks + a.by_block(pos)];
       if (blk < 0 || blk >= a.num_blocks) continue;
       const int64_t slot = static_cast<int64_t>(blk) * a.block_size + pos % a.block_size;
-      const uint32_t *v = reinterpret_cast<const uint32_t *>(a.v_cache + (slot * a.Hkv + c.g) * D);
+      const uint4 *v = reinterpret_cast<const uint4 *>(a.v_cache + (slot * a.Hkv + c.g) * D);
       for (int w = 0; w < D / 32; ++w)
 #pragma unroll 1
-        for (int x = 0; x < 8; ++x) {
-          const uint32_t word = v[8 * w + x];
-          for (int y = 0; y < 4; ++y)
-            if (((word >> (8 * y)) & 0x7F) == 0x7F) dims[w] |= 1u << (4 * x + y);
+        for (int x = 0; x < 2; ++x) {
+          const uint4 q = v[2 * w + x];
+          const uint32_t word[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            // 0x80 where a byte is NaN; its four flags side by side
+            const uint32_t m = ((word[y] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+            dims[w] |= ((m >> 7) * 0x10204080u >> 28) << (16 * x + 4 * y);
+          }
         }
     }
   }
@@ -660,7 +668,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       if (lane == 0) {
         sh.valid[it & 7u] = there;
         sh.tile[st].g = pre.g;
-        sh.tile[st].piece = static_cast<int>(ip);
+        sh.tile[st].piece = static_cast<int>(2 * ip) + (pre.s.ctx >= (pre.t + 1) * kTreeN);
         if (by_row) mbar_arrive(bar);
         else mbar_arrive_expect_tx(bar, L::kTile);
       }
@@ -824,7 +832,10 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
 #pragma unroll
             for (int k = 0; k < d; ++k) m[k] = __hmax2_nan(m[k], m[k + d]);
           if (!__hisnan(__low2half(m[0])) && !__hisnan(__high2half(m[0]))) break;
-          // A NaN code becomes 0; it is put back into the results of the rows that see it.
+          // A NaN code of a tile in the context stays: every row sees it, and the products bring it to
+          // them.  Else, where some rows may not see it, it becomes 0 and is put back into the results
+          // of the rows that do.
+          if (piece & 1) break;
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             uint32_t *x[4] = {&v8[k].x, &v8[k].y, &v8[k].z, &v8[k].w};
@@ -832,7 +843,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
             for (int q = 0; q < 4; ++q)
               *x[q] &= ~(((((*x[q] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xFFu);
           }
-          atomicMax(&sh.nan_piece, piece);
+          atomicMax(&sh.nan_piece, piece >> 1);
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {

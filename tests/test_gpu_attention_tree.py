@@ -232,6 +232,80 @@ def test_nan_codes_that_are_not_seen(Hq, Hkv, n):
     np.testing.assert_array_equal(got[~bad], same[~bad])
 
 
+def _shared_contexts(B, Hkv, D, ctx, n, seed):
+    """B sequences whose contexts lie in the same cache blocks and whose n nodes each lie in blocks of
+    their own: long contexts over a small cache."""
+    bs, rng = 64, np.random.default_rng(seed)
+    assert ctx % bs == 0 and n <= bs
+    table = np.concatenate([np.tile(rng.permutation(ctx // bs), (B, 1)),
+                            ctx // bs + np.arange(B)[:, None]], axis=1)
+    slots = (ctx // bs + B) * bs
+    return dict(Hq=Hkv, Hkv=Hkv, D=D, bs=bs, ctx=np.full(B, ctx), nodes=[n] * B, table=table,
+                sees=[np.eye(n, dtype=bool)] * B, q=[_codes((n, Hkv * D), rng) for _ in range(B)],
+                k=_codes((slots, Hkv * D), rng), v=_codes((slots, Hkv * D), rng),
+                s3=np.array([0.011, 0.012, 0.007], np.float32), max_nodes=n, max_len=ctx + n)
+
+
+def test_nan_values_in_long_contexts():
+    """NaN in V of one cached position: exactly that dim of the rows of its kv head is NaN, whatever the
+    context's length, and the call takes about as long as without (some 340 position tiles in each
+    CTA's share)."""
+    B, Hkv, D, ctx, n = 40, 8, 64, 20032, 3
+    d = _shared_contexts(B, Hkv, D, ctx, n, 80)
+    a = _args(d)
+    clean = fq.attention_tree(*a)
+    two = dict(d, ctx=d["ctx"][:2], nodes=[n] * 2, table=d["table"][:2], sees=d["sees"][:2], q=d["q"][:2])
+    _check(clean[:2 * n], two)
+    dirty = list(a)
+    dirty[2] = a[2].clone()
+    dirty[2][int(d["table"][0, 3]) * 64 + 11, 5 * D + 17] = 0x7F          # position 203, kv head 5
+    dirty[2][int(d["table"][0, 311]) * 64 + 63, 2 * D + 40] = 0xFF        # position 19967, kv head 2
+    dirty[2][int(d["table"][7, -1]) * 64 + 1, 6 * D] = 0x7F               # node 1 of sequence 7, head 6
+    o = fq.attention_tree(*dirty)
+    bad = np.zeros((B * n, Hkv, D), bool)
+    bad[:, 5, 17] = bad[:, 2, 40] = bad[7 * n + 1, 6, 0] = True
+    got, same = (host_bf16_f64(x).reshape(B * n, Hkv, D) for x in (o, clean))
+    np.testing.assert_array_equal(np.isnan(got), bad)
+    np.testing.assert_array_equal(got[~bad], same[~bad])
+
+    def best(args):
+        times = []
+        for _ in range(5):
+            t = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+            t[0].record()
+            fq.attention_tree(*args)
+            t[1].record()
+            t[1].synchronize()
+            times.append(t[0].elapsed_time(t[1]))
+        return min(times)
+    slow, fast = best(dirty), best(a)
+    assert slow < 3 * fast, f"{slow} ms with NaN, {fast} ms without"
+    assert fq.check_device_error() == 0
+
+
+@pytest.mark.parametrize("Hq,Hkv,n,D", [(4, 2, 9, 128), (8, 1, 8, 64), (16, 1, 40, 128), (4, 4, 200, 64)])
+def test_nan_values_of_context_and_nodes_in_split_items(Hq, Hkv, n, D):
+    """One long sequence split over many CTAs: NaN values of cached positions reach every row of their
+    kv head, those of a node the rows that see it; repeats of a row and whole row tiles."""
+    d = _case(Hq, Hkv, D, [n, 2], [9001, 30], 7, seed=81 + n)
+    clean = fq.attention_tree(*_args(d))
+    _check(clean, d)
+    slot = lambda p: d["table"][0, p // 7] * 7 + p % 7
+    G, bad = Hq // Hkv, np.zeros((n + 2, Hq, D), bool)
+    for p, g, dim in ((0, 0, 3), (4999, Hkv - 1, D - 1), (9000, 0, 31)):
+        d["v"][slot(p), g * D + dim] = 0x7F
+        bad[:n, g * G:(g + 1) * G, dim] = True
+    for j in {0, n // 2, n - 1}:
+        d["v"][slot(9001 + j), (Hkv - 1) * D + 16 + j % 16] = 0xFF
+        for i in range(j, n):
+            if d["sees"][0][i, j]:
+                bad[i, (Hkv - 1) * G:, 16 + j % 16] = True
+    got, same = (host_bf16_f64(x).reshape(n + 2, Hq, D) for x in (fq.attention_tree(*_args(d)), clean))
+    np.testing.assert_array_equal(np.isnan(got), bad)
+    np.testing.assert_array_equal(got[~bad], same[~bad])
+    assert fq.check_device_error() == 0
+
+
 # Small drafts over three or more kv heads.
 SHARED = [(3, 3, 20), (4, 4, 64), (10, 5, 16), (32, 8, 16), (32, 8, 7), (12, 4, 21), (40, 5, 8),
           (7, 7, 1), (24, 3, 4)]

@@ -306,6 +306,99 @@ def test_nan_values_of_context_and_nodes_in_split_items(Hq, Hkv, n, D):
     assert fq.check_device_error() == 0
 
 
+def _rising_case(B, Hq, Hkv, n, D, ctx, shape, seed):
+    """_shared_contexts with keys whose level u (a multiple of 2 up to 478, in two dims) follows the
+    positions up a ramp, or up and down again, and single large keys in a third dim; query rows that
+    take the ramp once, twice, half, negated, not at all, or the large keys.  Three products a score:
+    exact in 32 bits."""
+    d = _shared_contexts(B, Hkv, D, ctx, n, seed)
+    rng = np.random.default_rng(seed + 1)
+    G, L = Hq // Hkv, ctx + n
+    enc = lambda x: (torch.from_numpy(np.asarray(x, np.float32)).to(torch.float8_e4m3fn)
+                     .view(torch.uint8).numpy())
+    at = np.linspace(0, 1, L)
+    if shape == "tent":
+        at = 1 - np.abs(2 * at - 1)
+    for g in range(Hkv):
+        u = np.clip(np.round((at[:ctx] * 470 + rng.normal(0, 4, ctx)) / 2) * 2, 0, 478).astype(int)
+        own = np.clip(np.round((at[ctx:] * 470 + rng.normal(0, 4, (B, n))) / 2) * 2, 0, 478).astype(int)
+        big = rng.random(ctx) < 3 / ctx
+        big[rng.integers(0, ctx)] = True
+        slots = (d["table"][0, :-1][:, None] * 64 + np.arange(64)).reshape(-1)
+        d["k"][slots, g * D + 3] = enc(u // 32 * 32)
+        d["k"][slots, g * D + 40] = enc(u % 32)
+        d["k"][slots, g * D + 63] = enc(np.where(big, 448, 0))
+        for b in range(B):
+            rows = d["table"][b, -1] * 64 + np.arange(n)
+            d["k"][rows, g * D + 3] = enc(own[b] // 32 * 32)
+            d["k"][rows, g * D + 40] = enc(own[b] % 32)
+            d["k"][rows, g * D + 63] = 0
+    d["Hq"] = Hq
+    kinds = np.array([[1, 1, 0], [2, 2, 0], [.5, .5, 0], [-1, -1, 0], [0, 0, 0], [1, 1, 1], [1, 1, 0]])
+    d["q"] = []
+    for b in range(B):
+        q = np.zeros((n, Hq, D), np.float32)
+        q[:, :, [3, 40, 63]] = kinds[rng.integers(0, len(kinds), (n, Hq))]
+        d["q"].append(enc(q).reshape(n, Hq * D))
+    d["s3"] = np.array([0.1, 0.1, 0.007], np.float32)
+    d["sees"] = [spec.tree_sees([rng.integers(max(-1, i - 5), i) for i in range(n)]) for _ in range(B)]
+    return d
+
+
+def _rescales(d, sm_scale, tiles):
+    """How often the accumulators of sequence 0's rows are rescaled over its first `tiles` position tiles
+    if a CTA takes them all: the reference moves when a score is more than 8 (in log2 units) above it.
+    [rows, repeats] of each kv head, by repeats of the row as the kernel lays them out."""
+    val, (D, G) = spec.e4m3_values(), (d["D"], d["Hq"] // d["Hkv"])
+    n = d["nodes"][0]
+    c2 = sm_scale * float(d["s3"][0]) * float(d["s3"][1]) * np.log2(np.e)
+    slots = (d["table"][0][:tiles, None] * 64 + np.arange(64)).reshape(-1)
+    rows = min(128, n * G)
+    rep = 4 if rows <= 32 else 2 if rows <= 64 else 1
+    counts = []
+    for h in range(d["Hq"]):
+        cols = slice(h // G * D, (h // G + 1) * D)
+        z = val[d["q"][0][:, h * D:(h + 1) * D]] @ val[d["k"][slots, cols]].T * c2
+        top = z.reshape(n, tiles, rep, 64 // rep).max(axis=3)
+        ref, moved = top[:, 0].copy(), np.zeros((n, rep), int)
+        for t in range(1, tiles):
+            up = top[:, t] > ref + 8
+            ref[up] = top[:, t][up]
+            moved += up
+        counts.append(moved)
+    return np.array(counts)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("shape", ["ramp", "tent"])
+@pytest.mark.parametrize("Hq,Hkv,n,B", [(8, 4, 3, 30), (16, 4, 10, 30), (8, 2, 30, 60), (8, 2, 50, 30)])
+def test_accumulators_rescaled_in_many_tiles(Hq, Hkv, n, B, shape, D):
+    """Running maxima that rise by about 10 log2 units a tile (5, 20, or at once by hundreds, in other
+    rows), over shares of ten tiles and more: four, two and one repeats of a row, and two row tiles."""
+    ctx, sm = 1920, 44.0
+    d = _rising_case(B, Hq, Hkv, n, D, ctx, shape, 90 + n)
+    moved = _rescales(d, sm, 10)
+    assert (moved >= 5).mean() > 0.15 and (moved == 0).mean() > 0.1
+    a = _args(d)
+    o = fq.attention_tree(*a, sm_scale=sm)
+    assert fq.check_device_error() == 0
+    two = dict(d, ctx=d["ctx"][:2], nodes=[n] * 2, table=d["table"][:2], sees=d["sees"][:2], q=d["q"][:2])
+    _check(o[:2 * n], two, sm)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("shape", ["ramp", "tent"])
+@pytest.mark.parametrize("Hq,Hkv,n", [(4, 2, 5), (8, 2, 12), (4, 1, 30)])
+def test_parts_whose_maxima_lie_far_apart(Hq, Hkv, n, shape, D):
+    """One sequence split over many CTAs: their parts' references are tens of log2 units apart."""
+    ctx, sm = 6400, 44.0
+    d = _rising_case(1, Hq, Hkv, n, D, ctx, shape, 95 + n)
+    for scale in (sm, 4.0, 0.3):                        # one part counts, several, all
+        o = fq.attention_tree(*_args(d), sm_scale=scale)
+        assert fq.check_device_error() == 0
+        _check(o, d, scale)
+
+
 # Small drafts over three or more kv heads.
 SHARED = [(3, 3, 20), (4, 4, 64), (10, 5, 16), (32, 8, 16), (32, 8, 7), (12, 4, 21), (40, 5, 8),
           (7, 7, 1), (24, 3, 4)]

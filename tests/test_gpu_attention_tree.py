@@ -118,6 +118,30 @@ def test_block_sizes(bs):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bs", [1, 2, 3, 4, 6, 8, 12, 20, 24, 48, 64, 96, 100, 128, 640])
+def test_block_sizes_on_both_sides_of_the_row_copies(bs, D):
+    """K goes by rows where a copy has less than 512 bytes: blocks whose runs of 1, 2, 4, 8, 16, 32 and
+    64 rows lie on either side for both head sizes, several tiles per sequence, ends inside a tile and
+    inside a block."""
+    d = _case(8, 2, D, [5, 1, 12, 70, 3], [330, 77, 3, 190, 64 * 3 - 3], bs, seed=300 + bs + D)
+    o = fq.attention_tree(*_args(d))
+    assert fq.check_device_error() == 0
+    _check(o, d)
+
+
+@pytest.mark.parametrize("D,bs", [(64, 4), (64, 6), (128, 2), (128, 4), (128, 12)])
+def test_bad_block_ids_in_blocks_of_few_rows(D, bs):
+    """Ids out of range among small blocks: their positions are not seen, their neighbours in the same
+    tile are."""
+    d = _case(8, 2, D, [5, 9], [330, 77], bs, seed=310 + bs + D)
+    for b, k in ((0, 0), (0, 17), (0, (330 + 4) // bs), (1, 5)):
+        d["table"][b, k] = 10 ** 6 if k % 2 else -1
+    o = fq.attention_tree(*_args(d))
+    assert fq.check_device_error() == RANGE
+    _check(o, d)
+
+
+@pytest.mark.parametrize("D", [64, 128])
 def test_arbitrary_masks_and_rows_that_see_nothing(D):
     d = _case(8, 4, D, [70, 1, 9, 20], [0, 0, 0, 5], 16, seed=50, kind="random")
     d["sees"][0][3] = False

@@ -393,6 +393,8 @@ def kv_cache_accept(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: t
     if k_cache.dim() not in (2, 3):
         raise ValueError("k_cache must be [slots, Hkv*D] or [layers, slots, Hkv*D]")
     layers = k_cache.shape[0] if k_cache.dim() == 3 else 1
+    if layers == 0:                       # the call would do nothing, new lengths included
+        raise ValueError("k_cache must have a layer")
     slots, row = k_cache.shape[-2:]
     shape = tuple(k_cache.shape)
     _expect(dev, k_cache=(k_cache, torch.uint8, shape), v_cache=(v_cache, torch.uint8, shape),

@@ -402,7 +402,8 @@ int fp8q_paged_batch_tables_held(const int32_t *ctx_lens, const int32_t *new_len
  * Recorded as FP8Q_ERR_RANGE: a parent outside [-1, i) (taken as -1); offsets that leave [0, total]
  * (clamped); a sequence of more than max_nodes nodes (the rest of its rows are not written); offsets
  * that decrease, cu_nodes[b + 1] < cu_nodes[b] (the batch ends before sequence b).  Rows behind the
- * last sequence are left as they were.  B <= 65535, total <= 2^31 - 1. */
+ * last sequence are left as they were.  B <= 65535, total <= 2^31 - 1.  Where B, total or max_nodes is 0
+ * nothing is launched: nothing is read, written or recorded, whatever cu_nodes holds. */
 int fp8q_tree_mask(const int32_t *parents, const int32_t *cu_nodes, const int32_t *ctx_lens,
                    int64_t B, int64_t total, int64_t max_nodes, int64_t *mask, int64_t ldm,
                    int64_t *positions, cudaStream_t stream);
@@ -433,7 +434,8 @@ int fp8q_tree_mask(const int32_t *parents, const int32_t *cu_nodes, const int32_
  * Results do not depend on timing.  Recorded as FP8Q_ERR_RANGE: offsets as in fp8q_tree_mask; a context
  * that is negative or makes ctx + nodes exceed max_seq_len (clamped; a sequence with more nodes than
  * max_seq_len has no rows); a block id outside [0, num_slots / block_size) (its positions are not
- * seen).  Two launches; bounds (max_nodes, max_seq_len) that fit the batch are faster. */
+ * seen).  Two launches; bounds (max_nodes, max_seq_len) that fit the batch are faster.  Where B, total or
+ * max_nodes is 0 nothing is launched: nothing is read, written or recorded, whatever cu_nodes holds. */
 int fp8q_attention_tree(const void *q_e4m3, int64_t ldq, const void *k_cache, const void *v_cache,
                         int64_t num_slots, const float *scale3, const int32_t *block_table,
                         int64_t max_blocks, const int32_t *ctx_lens, const int32_t *cu_nodes,
@@ -459,7 +461,8 @@ int fp8q_attention_tree_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int6
  * A sequence whose path is not strictly ascending within its nodes, is longer than its nodes or
  * max_path, leaves the table (max_blocks * block_size positions) or meets a block id outside
  * [0, num_slots / block_size) records FP8Q_ERR_RANGE: none of its rows moves and its new length is
- * ctx_lens[b].  Slots of different (sequence, position) pairs that are moved must differ.  new_lens
+ * ctx_lens[b].  Where B or layers is 0 nothing is launched: new_lens is not written either, and the
+ * binding refuses caches without a layer.  Slots of different (sequence, position) pairs that are moved must differ.  new_lens
  * must not overlap the other int32 arrays (FP8Q_ERR_ARG). */
 int fp8q_kv_cache_accept(void *k_cache, void *v_cache, int64_t num_slots, int64_t layers,
                          int64_t layer_stride, int64_t row_bytes, const int32_t *block_table,

@@ -197,3 +197,14 @@ def test_binding_of_held_blocks_refuses():
         fq.paged_batch_tables(*args, held_blocks=z(2, **i32), out=(*five, z(3, **i32)))
     with pytest.raises(ValueError, match="CUDA"):
         fq.paged_batch_tables(*args, held_blocks=z(2, **i32), out=(*five, z(2, **i32)))
+
+
+def test_accept_without_a_layer_is_refused_by_the_binding():
+    """The C call does nothing then, and the binding would return lengths that nothing has written."""
+    i32 = dict(dtype=torch.int32)
+    z = torch.zeros
+    ctx, cu, table = z(2, **i32), z(3, **i32), z((2, 4), **i32)
+    k = z((0, 64, 256), dtype=torch.uint8)
+    for out in (None, z(2, **i32)):
+        with pytest.raises(ValueError, match="layer"):
+            fq.kv_cache_accept(k, k, table, ctx, cu, z((2, 3), **i32), ctx, 16, out_lens=out)

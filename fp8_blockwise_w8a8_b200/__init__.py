@@ -35,9 +35,9 @@ __all__ = ["quant_weight_block", "rmsnorm_quant_token", "add_rmsnorm_quant", "ge
            "quant_rowwise", "gemm_w8a8_rowwise", "silu_mul_quant", "inverse_rope_quant",
            "gemm_w8a8_block_diag", "gemm_w8a8_mx", "qkv_scales", "kv_cache_write", "WeightBatch",
            "paged_batch_tables", "tree_mask", "attention_tree", "attention_tree_workspace_bytes",
-           "kv_cache_accept", "selftest_timeout", "attention_decode", "attention_decode_workspace_bytes",
-           "grouped_gemm_w8a8_block", "check_device_error", "Fp8qError", "FP8Q_SCALE_F32",
-           "FP8Q_SCALE_E8M0", "scale_format"]
+           "kv_cache_accept", "selftest_timeout", "selftest_attention_tree", "attention_decode",
+           "attention_decode_workspace_bytes", "grouped_gemm_w8a8_block", "check_device_error",
+           "Fp8qError", "FP8Q_SCALE_F32", "FP8Q_SCALE_E8M0", "scale_format"]
 
 
 def scale_format(fmt) -> int:
@@ -344,6 +344,13 @@ def attention_tree(q_codes: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     [total, Hq*D], caches uint8 [slots, Hkv*D], scale3 fp32 [3], block_table int32 [B, max blocks],
     ctx_lens int32 [B], cu_nodes int32 [B + 1], mask int64 [total, words] (from tree_mask; None: each
     node sees all nodes before it) -> bf16 [total, Hq*D].  sm_scale defaults to 1/sqrt(D)."""
+    return _attention_tree(None, q_codes, k_cache, v_cache, scale3, block_table, ctx_lens, cu_nodes,
+                           mask, Hq, Hkv, block_size, max_nodes, max_seq_len, sm_scale, workspace,
+                           out, stream)
+
+
+def _attention_tree(polls, q_codes, k_cache, v_cache, scale3, block_table, ctx_lens, cu_nodes, mask, Hq,
+                    Hkv, block_size, max_nodes, max_seq_len, sm_scale, workspace, out, stream):
     dev, total, B = q_codes.device, q_codes.shape[0], ctx_lens.shape[0]
     D = k_cache.shape[-1] // Hkv
     slots = k_cache.shape[0]
@@ -371,13 +378,14 @@ def attention_tree(q_codes: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
             n = attention_tree_workspace_bytes(B, Hq, Hkv, D, max_nodes, max_seq_len)
             ws = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
         o = torch.empty((total, Hq * D), dtype=torch.bfloat16, device=dev) if out is None else out
-        rc = _lib.lib().fp8q_attention_tree(
-            q_codes.data_ptr(), _ld(q_codes), k_cache.data_ptr(), v_cache.data_ptr(), slots,
-            scale3.data_ptr(), block_table.data_ptr(), block_table.shape[1], ctx_lens.data_ptr(),
-            cu_nodes.data_ptr(), _ptr(mask), 0 if mask is None else _ld(mask), B, total, Hq, Hkv, D,
-            int(block_size), int(max_nodes), int(max_seq_len), float(sm_scale), o.data_ptr(), _ld(o),
-            ws.data_ptr(), ws.numel() * ws.element_size(), st)
-        _lib.check(rc, "fp8q_attention_tree")
+        name = "fp8q_attention_tree" if polls is None else "fp8q_selftest_attention_tree"
+        rc = getattr(_lib.lib(), name)(
+            *(() if polls is None else (int(polls),)), q_codes.data_ptr(), _ld(q_codes),
+            k_cache.data_ptr(), v_cache.data_ptr(), slots, scale3.data_ptr(), block_table.data_ptr(),
+            block_table.shape[1], ctx_lens.data_ptr(), cu_nodes.data_ptr(), _ptr(mask),
+            0 if mask is None else _ld(mask), B, total, Hq, Hkv, D, int(block_size),
+            int(max_nodes), int(max_seq_len), float(sm_scale), o.data_ptr(), _ld(o), ws.data_ptr(), ws.numel() * ws.element_size(), st)
+        _lib.check(rc, name)
         return o
     return _on_stream(dev, stream, run)
 
@@ -619,6 +627,11 @@ def gemm_w8a8_rowwise(aq: torch.Tensor, sa: torch.Tensor, wq: torch.Tensor, sw: 
                                            _ptr(sw), M, N, K, _ptr(o), _ld(o), _stream(stream))
     _lib.check(st, "fp8q_gemm_w8a8_rowwise")
     return o
+
+
+def selftest_attention_tree(polls: int, *args, sm_scale=None, workspace=None, out=None, stream=None):
+    """attention_tree with bounded waits of `polls` polls (fp8q_selftest_attention_tree; tests)."""
+    return _attention_tree(polls, *args, sm_scale, workspace, out, stream)
 
 
 def selftest_timeout(limit_ns: int = 1_000_000, stream=None):

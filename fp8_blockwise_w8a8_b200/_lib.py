@@ -71,6 +71,9 @@ SIGNATURES = {
     "fp8q_attention_tree": (_I, [_P, _I64, _P, _P, _I64, _P, _P, _I64, _P, _P, _P, _I64, _I64,
                                  _I64, _I64, _I64, _I64, _I64, _I64, _I64, ctypes.c_float, _P,
                                  _I64, _P, _I64, _P]),
+    "fp8q_selftest_attention_tree": (_I, [_I64, _P, _I64, _P, _P, _I64, _P, _P, _I64, _P, _P, _P,
+                                          _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64,
+                                          ctypes.c_float, _P, _I64, _P, _I64, _P]),
     "fp8q_attention_tree_workspace_bytes": (_I, [_I64, _I64, _I64, _I64, _I64, _I64, _P]),
     "fp8q_kv_cache_accept": (_I, [_P, _P, _I64, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _P,
                                   _I64, _P, _I64, _P, _P]),

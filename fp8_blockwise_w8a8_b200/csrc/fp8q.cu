@@ -424,6 +424,101 @@ int64_t tree_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
          (4 * fp8q::kTreeMetaInts + 8 * tree_attn_row_cap(Hq, Hkv, max_nodes) * (D + 2));
 }
 
+// fp8q_attention_tree with the limit of its bounded waits, in polls.
+int attention_tree(uint32_t polls, const void *q_e4m3, int64_t ldq, const void *k_cache,
+                   const void *v_cache, int64_t num_slots, const float *scale3,
+                   const int32_t *block_table, int64_t max_blocks, const int32_t *ctx_lens,
+                   const int32_t *cu_nodes, const int64_t *tree_mask, int64_t ldm, int64_t B,
+                   int64_t total, int64_t Hq, int64_t Hkv, int64_t D, int64_t block_size,
+                   int64_t max_nodes, int64_t max_seq_len, float sm_scale, void *out_bf16,
+                   int64_t ldo, void *workspace, int64_t workspace_bytes, cudaStream_t stream) {
+  int rc = tree_attn_shape_status(B, Hq, Hkv, D, block_size, max_nodes, max_seq_len);
+  if (rc != FP8Q_OK) return rc;
+  if (num_slots < 0 || num_slots > INT32_MAX || max_blocks < 0 || max_blocks > INT32_MAX ||
+      max_blocks * block_size < max_seq_len || total < 0 || total > INT32_MAX ||
+      ldq < Hq * D || ldo < Hq * D || (tree_mask && ldm < (max_nodes + 63) / 64))
+    return FP8Q_ERR_SHAPE;
+  if (B == 0 || total == 0 || max_nodes == 0) return FP8Q_OK;
+  if (!q_e4m3 || !k_cache || !v_cache || !scale3 || !block_table || !ctx_lens || !cu_nodes ||
+      !out_bf16 || !workspace)
+    return FP8Q_ERR_NULL;
+  if (!aligned16(q_e4m3) || ldq % 16 || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned16(workspace) || !aligned16(out_bf16) || ldo % 8 || !aligned_to(scale3, 4) ||
+      !aligned_to(block_table, 4) || !aligned_to(ctx_lens, 4) || !aligned_to(cu_nodes, 4) ||
+      !aligned_to(tree_mask, 8))
+    return FP8Q_ERR_ALIGN;
+  if (workspace_bytes < tree_attn_workspace_bytes(B, Hq, Hkv, D, max_nodes, max_seq_len))
+    return FP8Q_ERR_SHAPE;
+  DeviceState *st = nullptr;
+  if ((rc = device_state(&st)) != FP8Q_OK) return rc;
+  fp8q::TreeAttnArgs a;
+  a.q = static_cast<const uint8_t *>(q_e4m3);
+  a.ldq = ldq;
+  a.k_cache = static_cast<const uint8_t *>(k_cache);
+  a.v_cache = static_cast<const uint8_t *>(v_cache);
+  a.num_blocks = num_slots / block_size;
+  a.scale3 = scale3;
+  a.block_table = block_table;
+  a.max_blocks = max_blocks;
+  a.ctx_lens = ctx_lens;
+  a.cu = cu_nodes;
+  a.mask = tree_mask;
+  a.ldm = ldm;
+  a.total = total;
+  a.B = static_cast<int>(B);
+  a.Hq = static_cast<int>(Hq);
+  a.Hkv = static_cast<int>(Hkv);
+  a.block_size = static_cast<int>(block_size);
+  a.max_nodes = static_cast<int>(max_nodes);
+  a.max_seq_len = static_cast<int>(max_seq_len);
+  a.sm_scale = sm_scale;
+  a.polls = polls;
+  a.out = static_cast<uint16_t *>(out_bf16);
+  a.ldo = ldo;
+  const int64_t ctas = tree_attn_ctas(B, Hq, Hkv, max_nodes, max_seq_len);
+  a.row_cap = static_cast<int>(tree_attn_row_cap(Hq, Hkv, max_nodes));
+  a.meta = static_cast<int32_t *>(workspace);
+  a.part = reinterpret_cast<float *>(a.meta + ctas * fp8q::kTreeMetaInts);
+  const unsigned grid = static_cast<unsigned>(ctas < 2 * st->sms ? ctas : 2 * st->sms);
+  a.grid_recip = ~uint64_t{0} / grid;
+  // rows per TMA copy
+  const int64_t pow2 = block_size & -block_size;
+  a.box = static_cast<int>(pow2 > 64 ? 64 : pow2);
+  a.by_block = tree_div(block_size);
+  a.by_group = tree_div(Hq / Hkv);
+  // a cache without slots: every position is out of range and loads row 0, here of q
+  CUtensorMap tm_k;
+  if ((rc = get_encoder()) != FP8Q_OK ||
+      (rc = make_u8_row_map(&tm_k, num_slots > 0 ? k_cache : q_e4m3, num_slots > 0 ? num_slots : 1,
+                            Hkv * D, static_cast<uint32_t>(a.box), static_cast<uint32_t>(D),
+                            D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B)) !=
+          FP8Q_OK)
+    return rc;
+  if (D == 128)
+    fp8q::k_tree_attn<128><<<grid, fp8q::kTreeThreads, fp8q::TreeLayout<128>::kSmem, stream>>>(tm_k,
+                                                                                               a);
+  else
+    fp8q::k_tree_attn<64><<<grid, fp8q::kTreeThreads, fp8q::TreeLayout<64>::kSmem, stream>>>(tm_k, a);
+  if ((rc = launch_status()) != FP8Q_OK) return rc;
+  // the merge as a programmatic dependent launch: scheduled while the first kernel drains
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, static_cast<unsigned>((a.row_cap + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t err = D == 128
+                              ? cudaLaunchKernelEx(&cfg, fp8q::k_tree_attn_combine<128>, a)
+                              : cudaLaunchKernelEx(&cfg, fp8q::k_tree_attn_combine<64>, a);
+  if (err != cudaSuccess) {
+    cudaGetLastError();
+    return FP8Q_ERR_LAUNCH;
+  }
+  return launch_status();
+}
 
 int attn_shape_status(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t block_size,
                       int64_t max_seq_len) {
@@ -1167,91 +1262,26 @@ int fp8q_attention_tree(const void *q_e4m3, int64_t ldq, const void *k_cache, co
                         int64_t max_nodes, int64_t max_seq_len, float sm_scale, void *out_bf16,
                         int64_t ldo, void *workspace, int64_t workspace_bytes,
                         cudaStream_t stream) {
-  int rc = tree_attn_shape_status(B, Hq, Hkv, D, block_size, max_nodes, max_seq_len);
-  if (rc != FP8Q_OK) return rc;
-  if (num_slots < 0 || num_slots > INT32_MAX || max_blocks < 0 || max_blocks > INT32_MAX ||
-      max_blocks * block_size < max_seq_len || total < 0 || total > INT32_MAX ||
-      ldq < Hq * D || ldo < Hq * D || (tree_mask && ldm < (max_nodes + 63) / 64))
-    return FP8Q_ERR_SHAPE;
-  if (B == 0 || total == 0 || max_nodes == 0) return FP8Q_OK;
-  if (!q_e4m3 || !k_cache || !v_cache || !scale3 || !block_table || !ctx_lens || !cu_nodes ||
-      !out_bf16 || !workspace)
-    return FP8Q_ERR_NULL;
-  if (!aligned16(q_e4m3) || ldq % 16 || !aligned16(k_cache) || !aligned16(v_cache) ||
-      !aligned16(workspace) || !aligned16(out_bf16) || ldo % 8 || !aligned_to(scale3, 4) ||
-      !aligned_to(block_table, 4) || !aligned_to(ctx_lens, 4) || !aligned_to(cu_nodes, 4) ||
-      !aligned_to(tree_mask, 8))
-    return FP8Q_ERR_ALIGN;
-  if (workspace_bytes < tree_attn_workspace_bytes(B, Hq, Hkv, D, max_nodes, max_seq_len))
-    return FP8Q_ERR_SHAPE;
-  DeviceState *st = nullptr;
-  if ((rc = device_state(&st)) != FP8Q_OK) return rc;
-  fp8q::TreeAttnArgs a;
-  a.q = static_cast<const uint8_t *>(q_e4m3);
-  a.ldq = ldq;
-  a.k_cache = static_cast<const uint8_t *>(k_cache);
-  a.v_cache = static_cast<const uint8_t *>(v_cache);
-  a.num_blocks = num_slots / block_size;
-  a.scale3 = scale3;
-  a.block_table = block_table;
-  a.max_blocks = max_blocks;
-  a.ctx_lens = ctx_lens;
-  a.cu = cu_nodes;
-  a.mask = tree_mask;
-  a.ldm = ldm;
-  a.total = total;
-  a.B = static_cast<int>(B);
-  a.Hq = static_cast<int>(Hq);
-  a.Hkv = static_cast<int>(Hkv);
-  a.block_size = static_cast<int>(block_size);
-  a.max_nodes = static_cast<int>(max_nodes);
-  a.max_seq_len = static_cast<int>(max_seq_len);
-  a.sm_scale = sm_scale;
-  a.out = static_cast<uint16_t *>(out_bf16);
-  a.ldo = ldo;
-  const int64_t ctas = tree_attn_ctas(B, Hq, Hkv, max_nodes, max_seq_len);
-  a.row_cap = static_cast<int>(tree_attn_row_cap(Hq, Hkv, max_nodes));
-  a.meta = static_cast<int32_t *>(workspace);
-  a.part = reinterpret_cast<float *>(a.meta + ctas * fp8q::kTreeMetaInts);
-  const unsigned grid = static_cast<unsigned>(ctas < 2 * st->sms ? ctas : 2 * st->sms);
-  a.grid_recip = ~uint64_t{0} / grid;
-  // rows per TMA copy
-  const int64_t pow2 = block_size & -block_size;
-  a.box = static_cast<int>(pow2 > 64 ? 64 : pow2);
-  a.by_block = tree_div(block_size);
-  a.by_group = tree_div(Hq / Hkv);
-  // a cache without slots: every position is out of range and loads row 0, here of q
-  CUtensorMap tm_k;
-  if ((rc = get_encoder()) != FP8Q_OK ||
-      (rc = make_u8_row_map(&tm_k, num_slots > 0 ? k_cache : q_e4m3, num_slots > 0 ? num_slots : 1,
-                            Hkv * D, static_cast<uint32_t>(a.box), static_cast<uint32_t>(D),
-                            D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B)) !=
-          FP8Q_OK)
-    return rc;
-  if (D == 128)
-    fp8q::k_tree_attn<128><<<grid, fp8q::kTreeThreads, fp8q::TreeLayout<128>::kSmem, stream>>>(tm_k,
-                                                                                               a);
-  else
-    fp8q::k_tree_attn<64><<<grid, fp8q::kTreeThreads, fp8q::TreeLayout<64>::kSmem, stream>>>(tm_k, a);
-  if ((rc = launch_status()) != FP8Q_OK) return rc;
-  // the merge as a programmatic dependent launch: scheduled while the first kernel drains
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, static_cast<unsigned>((a.row_cap + 7) / 8));
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  const cudaError_t err = D == 128
-                              ? cudaLaunchKernelEx(&cfg, fp8q::k_tree_attn_combine<128>, a)
-                              : cudaLaunchKernelEx(&cfg, fp8q::k_tree_attn_combine<64>, a);
-  if (err != cudaSuccess) {
-    cudaGetLastError();
-    return FP8Q_ERR_LAUNCH;
-  }
-  return launch_status();
+  return attention_tree(fp8q::kTreePolls, q_e4m3, ldq, k_cache, v_cache, num_slots, scale3,
+                        block_table, max_blocks, ctx_lens, cu_nodes, tree_mask, ldm, B, total, Hq,
+                        Hkv, D, block_size, max_nodes, max_seq_len, sm_scale, out_bf16, ldo,
+                        workspace, workspace_bytes, stream);
+}
+
+int fp8q_selftest_attention_tree(int64_t polls, const void *q_e4m3, int64_t ldq,
+                                 const void *k_cache, const void *v_cache, int64_t num_slots,
+                                 const float *scale3, const int32_t *block_table,
+                                 int64_t max_blocks, const int32_t *ctx_lens,
+                                 const int32_t *cu_nodes, const int64_t *tree_mask, int64_t ldm,
+                                 int64_t B, int64_t total, int64_t Hq, int64_t Hkv, int64_t D,
+                                 int64_t block_size, int64_t max_nodes, int64_t max_seq_len,
+                                 float sm_scale, void *out_bf16, int64_t ldo, void *workspace,
+                                 int64_t workspace_bytes, cudaStream_t stream) {
+  if (polls < 1 || polls > fp8q::kTreePolls) return FP8Q_ERR_ARG;
+  return attention_tree(static_cast<uint32_t>(polls), q_e4m3, ldq, k_cache, v_cache, num_slots,
+                        scale3, block_table, max_blocks, ctx_lens, cu_nodes, tree_mask, ldm, B,
+                        total, Hq, Hkv, D, block_size, max_nodes, max_seq_len, sm_scale, out_bf16,
+                        ldo, workspace, workspace_bytes, stream);
 }
 
 int fp8q_kv_cache_accept(void *k_cache, void *v_cache, int64_t num_slots, int64_t layers,

@@ -75,6 +75,7 @@ struct TreeAttnArgs {
   int row_cap;                 // rows of a partial slot: min(128, max_nodes * Hq / Hkv)
   int32_t *meta;               // [CTAs][kTreeMetaInts]
   float *part;                 // [CTAs][2][row_cap][D + 2]: o, then m, l
+  uint32_t polls;              // of a bounded wait
 };
 
 struct TreeSeq {
@@ -261,31 +262,32 @@ __device__ __forceinline__ uint64_t tree_sdesc_k(uint32_t saddr) {
          (static_cast<uint64_t>(B == 128 ? 2 : 4) << 61);
 }
 
-// Bounded wait of a warp, short in code: about 2^20 polls of a microsecond at most, then the timeout is
-// recorded and the CTA's roles give up.  The lanes leave it together.
+// Bounded wait of a warp, short in code: after `*polls` polls in vain the timeout is recorded, *polls
+// becomes 0 and the CTA's roles give up.  A poll in vain takes 4.0 us on a B200, whatever time it is
+// given, so 2^18 of them are a second.  The lanes leave it together.
 __device__ __forceinline__ bool tree_poll(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(1000u)
+      : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
 }
-constexpr uint32_t kTreePolls = 1u << 20;
+constexpr uint32_t kTreePolls = 1u << 18;
 __device__ __forceinline__ bool tree_wait(const uint64_t &barrier, uint32_t parity,
-                                          volatile int *abort_flag) {
+                                          volatile uint32_t *polls) {
   const uint32_t bar = smem_u32(&barrier);
 #pragma unroll 1
-  for (uint32_t n = 0;; ++n) {
+  for (uint32_t n = 1;; ++n) {
     const bool ok = tree_poll(bar, parity & 1u);
     if (__all_sync(0xffffffffu, ok)) return true;
-    const bool stop = *abort_flag != 0 || n >= kTreePolls;
+    const bool stop = n >= *polls;
     if (__any_sync(0xffffffffu, stop)) break;
   }
-  if (atomicExch(const_cast<int *>(abort_flag), 1) == 0) record_error(6 /* FP8Q_ERR_TIMEOUT */);
+  if (atomicExch(const_cast<uint32_t *>(polls), 0u) != 0) record_error(6 /* FP8Q_ERR_TIMEOUT */);
   return false;
 }
 // The calling warp's share of an arrival.
@@ -323,7 +325,7 @@ struct TreeShared {
   int64_t start_off;
   int64_t warp_sum[kTreeThreads / 32];
   uint32_t tmem;
-  int abort;
+  uint32_t polls;                // of a wait at most; 0 once one has given up
   int nan_piece;                 // 1 + index of the last piece with a NaN code in V that was taken out
   float ml[4][32][2];
   float4 o[4][32][5];            // 16 columns, rows 80 bytes apart
@@ -333,7 +335,7 @@ struct TreeShared {
 __device__ __forceinline__ bool tree_take(TreeShared &sh, uint32_t ip, TreePiece &pc) {
   const uint32_t i = ip % kTreePieces;
   pc.t = pc.t_end = 0;
-  if (!tree_wait(sh.piece_full[i], ip / kTreePieces, &sh.abort)) return false;
+  if (!tree_wait(sh.piece_full[i], ip / kTreePieces, &sh.polls)) return false;
   pc = sh.piece[i];
   tree_arrive(sh.piece_free[i]);
   return pc.t_end > 0;
@@ -390,7 +392,7 @@ __device__ __forceinline__ bool tree_tile(TreeShared &sh, uint32_t tmem, uint32_
                                           uint32_t it, bool first, const int64_t *mrow, int words,
                                           int node, int j0, float c2, TreeRow &st) {
   using L = TreeLayout<D>;
-  if (!tree_wait(sh.s_full[it & 1u], it >> 1, &sh.abort)) return false;
+  if (!tree_wait(sh.s_full[it & 1u], it >> 1, &sh.polls)) return false;
   tc_fence_after();
   const uint32_t buf = tmem + L::kColS + 64 * (it & 1u);
   uint32_t sr[16];
@@ -429,7 +431,7 @@ __device__ __forceinline__ bool tree_tile(TreeShared &sh, uint32_t tmem, uint32_
     st.ref = up ? top : st.ref;
     st.l *= f;
     if (!first && __any_sync(0xffffffffu, held)) {
-      if (!tree_wait(sh.pv_done[(it - 1) & 1u], (it - 1) >> 1, &sh.abort)) return false;
+      if (!tree_wait(sh.pv_done[(it - 1) & 1u], (it - 1) >> 1, &sh.polls)) return false;
       tc_fence_after();
 #pragma unroll 1
       for (int d = 0; d < D; d += 16) {
@@ -524,7 +526,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       mbar_init(smem_u32(&sh.s_full[i]), 1);
     }
     mbar_init(smem_u32(&sh.drain), 1);
-    sh.abort = 0;
+    sh.polls = a.polls;
     sh.nan_piece = 0;
     fence_barrier_init();
   }
@@ -627,7 +629,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     uint32_t ip = 0;
     auto publish = [&]() {                                       // the piece, or the end
       const uint32_t i = ip % kTreePieces;
-      if (!tree_wait(sh.piece_free[i], (ip / kTreePieces) ^ 1u, &sh.abort)) return false;
+      if (!tree_wait(sh.piece_free[i], (ip / kTreePieces) ^ 1u, &sh.polls)) return false;
       if (lane == 0)
         sh.piece[i] = TreePiece{pre.s.first, pre.b, pre.s.n, pre.s.ctx, pre.g, pre.rt * kTreeM,
                                 min(kTreeM, pre.s.n * G - pre.rt * kTreeM), pre.t,
@@ -643,8 +645,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       if (fresh && !publish()) break;
       if (!pre.live) break;
       // the stage first: the block ids are on their way meanwhile
-      if (!tree_wait(sh.k_free[st], ph, &sh.abort) ||
-          !tree_wait(sh.t_free[st], ph, &sh.abort))
+      if (!tree_wait(sh.k_free[st], ph, &sh.polls) ||
+          !tree_wait(sh.t_free[st], ph, &sh.polls))
         break;
       bool ok;
       int32_t slot[2] = {slot_of(0, &ok), 0};
@@ -712,7 +714,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     }
     // the end, for both pairs of V warps
     for (int i = 0; i < 2; ++i) {
-      if (!tree_wait(sh.t_free[st], ph, &sh.abort)) break;
+      if (!tree_wait(sh.t_free[st], ph, &sh.polls)) break;
       if (lane == 0) sh.tile[st].g = -1;
       tree_arrive(sh.t_full[st]);
       if (++st == kTreeStages) {
@@ -747,7 +749,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         if (r < min(pc.rows, step))
           v[k] = *reinterpret_cast<const uint4 *>(source(r) + i % LPR * 16);
       }
-      if (!(ok = tree_wait(sh.q_free, ip ^ 1u, &sh.abort))) break;
+      if (!(ok = tree_wait(sh.q_free, ip ^ 1u, &sh.polls))) break;
 #pragma unroll 1
       for (int i = 256 + lane; i < step * LPR; i += 32) {
         const int r = i / LPR, x = (i % LPR ^ (r & 7)) << 4;
@@ -791,7 +793,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     const uint32_t stage = sbase + L::kV8 + pair * L::kTile + gt * 16;
     for (uint32_t it = pair;; it += 2) {
       const uint32_t st = it % kTreeStages;
-      if (!tree_wait(sh.t_full[st], it / kTreeStages, &sh.abort)) break;
+      if (!tree_wait(sh.t_full[st], it / kTreeStages, &sh.polls)) break;
       const TreeTile &tile = sh.tile[st];
       const int32_t g = tile.g, piece = tile.piece;
       if (g < 0) break;
@@ -805,7 +807,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
       tree_arrive(sh.t_free[st]);
-      if (it >= 2 && !tree_wait(sh.pv_done[pair], (it - 2) >> 1, &sh.abort)) break;
+      if (it >= 2 && !tree_wait(sh.pv_done[pair], (it - 2) >> 1, &sh.polls)) break;
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       uint8_t *dst = smem + L::kV16 + pair * L::kV16Bytes + (ch >> 2) * 8192 + r0 * 128;
       const int at0 = ((ch & 3) * 2 ^ (r0 & 7)) << 4;            // RPS is a multiple of 8
@@ -871,7 +873,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         fresh = left == 0;
         if (fresh) {
           const uint32_t i = ip % kTreePieces;
-          if (!tree_wait(sh.piece_full[i], ip / kTreePieces, &sh.abort)) return false;
+          if (!tree_wait(sh.piece_full[i], ip / kTreePieces, &sh.polls)) return false;
           left = sh.piece[i].t_end - (sh.piece[i].t_end > 0 ? sh.piece[i].t : 0);
           tree_arrive(sh.piece_free[i]);
           ++ip;
@@ -890,8 +892,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         for (int k = 0; k < 2 && ok; ++k) {
           if (fresh == (k == 1)) {
             if (!live) continue;
-            if ((fresh && !tree_wait(sh.q_full, ip - 1, &sh.abort)) ||
-                !tree_wait(sh.k_full[st], ph, &sh.abort)) {
+            if ((fresh && !tree_wait(sh.q_full, ip - 1, &sh.polls)) ||
+                !tree_wait(sh.k_full[st], ph, &sh.polls)) {
               ok = false;
               continue;
             }
@@ -914,8 +916,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
             }
           } else if (it > 0) {
             const uint32_t i = (it - 1) & 1u, pp = (it - 1) >> 1;
-            if (!tree_wait(sh.p_full[i], pp, &sh.abort) ||
-                !tree_wait(sh.v_full[i], pp, &sh.abort)) {
+            if (!tree_wait(sh.p_full[i], pp, &sh.polls) ||
+                !tree_wait(sh.v_full[i], pp, &sh.polls)) {
               ok = false;
               continue;
             }
@@ -963,7 +965,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         ok = tree_tile<D>(sh, tw, col0, 4 >> shift, it, t == pc.t, mrow, words, live ? node : -1,
                           t * kTreeN - pc.ctx, c2, st);
       }
-      ok = ok && tree_wait(sh.pv_done[(it - 1) & 1u], (it - 1) >> 1, &sh.abort);
+      ok = ok && tree_wait(sh.pv_done[(it - 1) & 1u], (it - 1) >> 1, &sh.polls);
       sh.ml[warp][lane][0] = st.ref;
       sh.ml[warp][lane][1] = st.l;
       if (tree_any4(!ok)) break;                                 // no more pieces, or given up

@@ -585,6 +585,21 @@ int fp8q_gemm_w8a8_rowwise(const void *aq, int64_t lda, const float *sa, const v
  * returns FP8Q_ERR_TIMEOUT; the context stays usable.  For tests. */
 int fp8q_selftest_timeout(int64_t limit_ns, cudaStream_t stream);
 
+/* fp8q_attention_tree with another limit of its bounded waits: 1 <= polls <= 2^18 (FP8Q_ERR_ARG), the
+ * limit of the ordinary call, where a poll in vain takes 4 us.  With few polls waits of a sound call can
+ * run out: the CTAs concerned give up as on a real timeout (copies and products in flight are waited
+ * for, TMEM is released), FP8Q_ERR_TIMEOUT is recorded and rows of out_bf16 may be left as they were or
+ * hold partial results.  For tests. */
+int fp8q_selftest_attention_tree(int64_t polls, const void *q_e4m3, int64_t ldq,
+                                 const void *k_cache, const void *v_cache, int64_t num_slots,
+                                 const float *scale3, const int32_t *block_table,
+                                 int64_t max_blocks, const int32_t *ctx_lens,
+                                 const int32_t *cu_nodes, const int64_t *tree_mask, int64_t ldm,
+                                 int64_t B, int64_t total, int64_t Hq, int64_t Hkv, int64_t D,
+                                 int64_t block_size, int64_t max_nodes, int64_t max_seq_len,
+                                 float sm_scale, void *out_bf16, int64_t ldo, void *workspace,
+                                 int64_t workspace_bytes, cudaStream_t stream);
+
 /* Synchronize `stream`, then read and clear the device error word of the current device.
  * Returns FP8Q_OK, FP8Q_ERR_TIMEOUT (a kernel gave up on a bounded wait since the last call;
  * its outputs are incomplete) or FP8Q_ERR_LAUNCH (the synchronize failed). */

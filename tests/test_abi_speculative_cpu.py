@@ -208,3 +208,16 @@ def test_accept_without_a_layer_is_refused_by_the_binding():
     for out in (None, z(2, **i32)):
         with pytest.raises(ValueError, match="layer"):
             fq.kv_cache_accept(k, k, table, ctx, cu, z((2, 3), **i32), ctx, 16, out_lens=out)
+
+
+def test_selftest_attention_tree(L):
+    """The limit's range, then the ordinary call's checks."""
+    def call(polls, B=2, D=128, ws=FAKE):
+        return L.fp8q_selftest_attention_tree(polls, FAKE, 1024, FAKE, FAKE, 64, FAKE, FAKE, 4, FAKE,
+                                              FAKE, None, 0, B, 8, 8, 2, D, 16, 16, 64, 0.088, FAKE,
+                                              1024, ws, 1 << 40, None)
+    for polls in (0, -1, (1 << 18) + 1):
+        assert call(polls) == ARG
+    assert call(1, D=96) == SHAPE and call(1, ws=None) == NULL and call(1, B=0) == OK
+    _no_device(lambda: call(1))
+    _no_device(lambda: call(1 << 18))

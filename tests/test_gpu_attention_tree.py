@@ -571,6 +571,28 @@ def test_cache_beyond_two_gigabytes():
     _check(o, small)
 
 
+def test_cache_beyond_two_gigabytes_by_rows():
+    """The same where K is copied row by row: blocks of 6 at both ends of 2.5 GiB caches."""
+    Hkv, D, bs = 16, 64, 6
+    slots = (5 << 30) // (2 * Hkv * D)
+    blocks = slots // bs
+    nodes, ctx = [3, 2], [200, 100]
+    small = _case(16, Hkv, D, nodes, ctx, bs, seed=84)
+    table = np.where(small["table"] % 2, small["table"], blocks - 1 - small["table"])
+    k = torch.zeros((slots, Hkv * D), dtype=torch.uint8, device="cuda")
+    v = torch.zeros_like(k)
+    for b in range(2):
+        for i in range(-(-(ctx[b] + nodes[b]) // bs)):
+            at, to = small["table"][b, i] * bs, int(table[b, i]) * bs
+            k[to:to + bs] = dev(small["k"][at:at + bs])
+            v[to:to + bs] = dev(small["v"][at:at + bs])
+    a = _args(small)
+    a[1], a[2], a[4] = k, v, i32(table)
+    o = fq.attention_tree(*a)
+    assert fq.check_device_error() == 0
+    _check(o, small)
+
+
 def test_inputs_out_of_range():
     """A bad block id hides its positions, a context beyond the bound and too many nodes are clamped,
     offsets outside the rows too: recorded, the other sequences as ever."""
@@ -660,6 +682,23 @@ def test_on_another_stream():
         assert torch.equal(x, o)
 
 
+def test_two_calls_at_once():
+    """Calls on two streams, each with the workspace it allocates, that run side by side."""
+    d1 = _case(8, 2, 128, [4, 9, 30], [500, 30, 2000], 16, seed=86)
+    d2 = _case(6, 3, 64, [7, 1], [900, 64], 7, seed=87)
+    a1, a2 = _args(d1), _args(d2)
+    want = fq.attention_tree(*a1), fq.attention_tree(*a2)
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    outs = [[fq.attention_tree(*a, stream=s) for a, s in zip((a1, a2), streams)] for _ in range(100)]
+    for s in streams:
+        torch.cuda.current_stream().wait_stream(s)
+    for pair in outs:
+        assert torch.equal(pair[0], want[0]) and torch.equal(pair[1], want[1])
+    assert fq.check_device_error() == 0
+
+
 def test_speculative_step_end_to_end():
     """Tables, positions, cache write, tree attention, acceptance, and the next step's decode over the
     moved rows, each from the device results of the one before, against the oracle."""
@@ -719,3 +758,78 @@ def test_speculative_step_end_to_end():
     np.testing.assert_allclose(host_bf16_f64(step),
                                host_bf16_f64(o)[[wcu[b] + paths[b][-1] for b in range(B)]],
                                rtol=2.0 ** -6, atol=2.0 ** -8)
+
+
+def test_speculative_loop_in_a_graph():
+    """Steps of a whole loop, captured once and replayed: tables over the blocks held, masks, cache write,
+    attention, acceptance, and the lengths, stack height and held blocks handed on by the graph itself.
+    Every result of every step against the oracle; no block is lost although most nodes are rejected."""
+    Hq, Hkv, D, bs, B, most, cap, width = 8, 2, 64, 4, 3, 8, 24, 24
+    rng = np.random.default_rng(85)
+    ctx, s3 = np.array([13, 0, 30]), np.array([0.02, 0.03, 0.01], np.float32)
+    table, ids = np.full((B, width), -1, np.int32), rng.permutation(30).astype(np.int32)
+    have, at = -(-ctx // bs), 0
+    for b in range(B):
+        table[b, :have[b]] = ids[at:at + have[b]]
+        at += have[b]
+    free = np.concatenate([ids[at:], np.zeros(at, np.int32)])
+    k, v = _codes((30 * bs, Hkv * D), rng), _codes((30 * bs, Hkv * D), rng)
+    dk, dv, dbt, dctx, ds3, dfree = dev(k), dev(v), i32(table), i32(ctx), dev(s3), i32(free)
+    count, held = i32([30 - at]), i32(np.zeros(B))
+    new, parents = i32(np.zeros(B)), i32(np.full(cap, -1))
+    path, plen = i32(np.zeros((B, most))), i32(np.zeros(B))
+    qkv = torch.zeros((cap, (Hq + 2 * Hkv) * D), dtype=torch.bfloat16, device="cuda")
+
+    def step():
+        cu, lens, slots, _, left, now = fq.paged_batch_tables(dctx, new, dbt, dfree, count, bs, cap,
+                                                              held_blocks=held)
+        mask, pos = fq.tree_mask(parents, cu, most, ctx_lens=dctx)
+        q = fq.kv_cache_write(qkv, Hq, Hkv, D, slots, ds3, dk, dv)
+        o = fq.attention_tree(q, dk, dv, ds3, dbt, dctx, cu, mask, Hq, Hkv, bs, most, width * bs)
+        lens = fq.kv_cache_accept(dk, dv, dbt, dctx, cu, path, plen, bs)
+        for old, x in ((count, left), (held, now), (dctx, lens)):
+            old.copy_(x)
+        return slots, pos, q, o
+    step()                                               # no nodes: everything stays as it is
+    assert held.cpu().numpy().tolist() == have.tolist() and dctx.cpu().numpy().tolist() == ctx.tolist()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        slots, pos, q, o = step()
+    wfree, wcount, wheld, wtable = free, 30 - at, have, table
+    for _ in range(12):
+        nodes = rng.integers(0, most + 1, B)
+        trees = [[int(rng.integers(max(-1, i - 4), i)) for i in range(n)] for n in nodes]
+        paths = []
+        for t in trees:                                  # from the root to some node, cut short
+            p, i = [], len(t) - 1
+            while i >= 0:
+                p.append(i)
+                i = t[i]
+            paths.append(p[::-1][:rng.integers(0, 3)])
+        total = int(nodes.sum())
+        new.copy_(i32(nodes))
+        parents[:total] = i32(np.concatenate([np.array(t, int) for t in trees]))
+        for b, p in enumerate(paths):
+            path[b, :len(p)] = i32(p)
+        plen.copy_(i32([len(p) for p in paths]))
+        qkv.copy_(torch.from_numpy(rng.standard_normal(tuple(qkv.shape), dtype=np.float32)))
+        g.replay()
+        assert fq.check_device_error() == 0
+        wtable, wcu, _, wslots, _, wcount, wheld = spec.batch_tables(ctx, nodes, wtable, bs, wfree, wcount,
+                                                                     cap, held=wheld)
+        np.testing.assert_array_equal(slots.cpu().numpy(), wslots)
+        np.testing.assert_array_equal(dbt.cpu().numpy(), wtable)
+        bits = qkv.cpu().view(torch.int16).numpy().view(np.uint16)
+        wq = oracle.kv_cache_write(bits, Hq, Hkv, D, wslots, s3, k, v)
+        np.testing.assert_array_equal(q.cpu().numpy()[:total], wq[:total])
+        sees = [spec.tree_sees(t) for t in trees]
+        np.testing.assert_array_equal(
+            pos.cpu().numpy()[:total], np.concatenate([s.sum(1) - 1 + c for s, c in zip(sees, ctx)]))
+        d = dict(Hq=Hq, Hkv=Hkv, D=D, bs=bs, ctx=ctx, nodes=nodes, table=wtable, sees=sees, k=k, v=v,
+                 s3=s3, q=[wq[wcu[b]:wcu[b + 1]] for b in range(B)])
+        _check(o[:total], d)
+        (k, v), ctx = spec.accept([k, v], wtable, ctx, paths, [len(p) for p in paths], bs)
+        for got, ref in ((dk, k), (dv, v), (dctx, ctx), (held, wheld), (count, [wcount])):
+            np.testing.assert_array_equal(got.cpu().numpy(), ref)
+        kept = np.concatenate([wtable[b, :wheld[b]] for b in range(B)] + [wfree[:wcount]])
+        np.testing.assert_array_equal(np.sort(kept), np.arange(30))

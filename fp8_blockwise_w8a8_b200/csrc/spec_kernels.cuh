@@ -74,8 +74,9 @@ __device__ __forceinline__ uint32_t tables_have(const TablesArgs &a, int b, uint
 // either in the table (a block the request had) or in the stack; the first position of a new
 // block is always a new token, so that token writes the table entry and no thread reads an entry
 // that this launch writes.  Every CTA makes the prefix sums itself (2 B words from L2): one launch,
-// no exchange between CTAs.  A decode step's 64 tokens take 8 us of device time, bound by the chain of
-// dependent loads; a million tokens of 256 prompts 15 us, 1.1 TB/s, of it 2.6 us for the bytes.
+// no exchange between CTAs.  A decode step's 64 tokens take 4 us of device time (6 with nothing in L2),
+// bound by the chain of dependent loads; a million tokens of 256 prompts 12 us (15), of it 2.6 for the
+// bytes.
 template <int R>
 __global__ void __launch_bounds__(kTablesThreads) k_paged_tables(const TablesArgs a) {
   extern __shared__ int32_t s_tab[];          // [B + 1] token offsets, [B + 1] new-block offsets
@@ -248,8 +249,9 @@ __device__ __forceinline__ int tree_rows(const int32_t *cu, int b, int64_t total
 // round ORs in the row of anc[i] and jumps to anc[anc[i]], so a tree of depth d takes ceil(log2 d)
 // rounds instead of d steps.  Word w needs no ancestor below its first node 64 w: anc is cut there.
 // The first word's CTA counts the depths along the way.  Each round reads into registers, then
-// writes, so no row is read while it changes.  16 trees of up to 1000 nodes take 10 us (one CTA per
-// tree over all words took 80), 64 of up to 16 nodes 5 us: the rounds' latency.
+// writes, so no row is read while it changes.  16 trees of up to 1000 nodes take 8 us (one CTA per
+// tree over all words took 80), 64 of up to 16 nodes 3 us: the rounds' latency.  The look through the
+// offsets is quadratic in the batch: 15 us for 8000 sequences, 0.56 ms for 65535, and 10 ms with 16 words.
 template <int T, int ITEMS>
 __global__ void __launch_bounds__(T) k_tree_mask(const TreeMaskArgs a) {
   __shared__ uint64_t s_bits[T * ITEMS];
@@ -332,8 +334,9 @@ struct AcceptArgs {
 // ascending.  path is strictly ascending, so path[k] >= k: a row is only overwritten by a move
 // whose index is not below its own, and a thread that keeps its 16-byte columns to itself, and
 // loads a batch of rows before storing it, reads every row before it is overwritten.  36 layers of 64
-// sequences with up to 8 moved rows of 1 KB (75 MB read and written) take 15 us, 5 TB/s of the copy
-// rate's 6.5; one layer 6 us, the latency of the launch and of three dependent loads.
+// sequences with up to 8 moved rows of 1 KB (75 MB read and written) take 16 us with nothing in L2,
+// 4.6 TB/s of the copy rate's 6.5, and 11 where it holds them; one layer 3 to 5 us, the latency of the
+// launch and of three dependent loads.
 __global__ void __launch_bounds__(kAcceptThreads) k_kv_accept(const AcceptArgs a) {
   extern __shared__ int64_t s_slot[];                          // [max_path] source, then target
   const int b = blockIdx.x, tid = threadIdx.x;

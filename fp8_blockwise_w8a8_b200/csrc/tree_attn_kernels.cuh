@@ -26,12 +26,13 @@
 // 8 MMAs, 9 K (by TMA a copy per run of positions in a block, or row by row), 10 queries.  Every wait is
 // bounded, and a warp's lanes leave it together.
 //
-// Measured (calls back to back, new inputs every time): 64 sequences of 512 to 4096 positions with up to
-// 16 nodes, 32/8 heads of 128: 107 us, 3.0 TB/s of cache and 46 % of the copy rate; one sequence of
-// 131501 positions with 61 nodes 192 us, 685 TFLOP/s; 8 of up to 512 nodes over up to 6000 positions
-// 336 us, 704 TFLOP/s; 40 sequences, 16 heads of 64, blocks of 7: 64 us.  What bounds it is the issue of
-// the roles' instructions and the hand-offs between them (0.46 to 0.53 instructions per cycle and
-// scheduler), with the tensor pipe at 27 %.  The MMA warp runs converged, one lane issuing, so that its
+// Measured (calls back to back, new inputs every time, several boxes): 64 sequences of 512 to 4096
+// positions with up to 16 nodes, 32/8 heads of 128: 107 to 113 us, 2.8 to 3.0 TB/s of cache and 43 to 46 %
+// of the copy rate; one sequence of 131501 positions with 61 nodes 192 to 205 us, 640 to 685 TFLOP/s; 8 of
+// up to 512 nodes over up to 6000 positions 332 to 341 us, 690 to 712 TFLOP/s; 40 sequences, 16 heads of
+// 64, blocks of 7: 64 us.  What bounds it is the issue of the roles' instructions and the hand-offs
+// between them (0.46 to 0.53 instructions per cycle and scheduler), with the tensor pipe at 29 %.  80
+// registers a thread, of which heads of 128 spill 12 bytes.  The MMA warp runs converged, one lane issuing, so that its
 // operands stay in uniform registers: 128 -> 107 us on the first case.  The roles' code has to stay
 // small: at 170 KB instruction fetch was the largest stall and everything took twice as long.
 #pragma once

@@ -28,7 +28,7 @@
 //
 // Measured (calls back to back, new inputs every time, several boxes): 64 sequences of 512 to 4096
 // positions with up to 16 nodes, 32/8 heads of 128: 107 to 113 us, 2.8 to 3.0 TB/s of cache and 43 to 46 %
-// of the copy rate; one sequence of 131501 positions with 61 nodes 192 to 205 us, 640 to 685 TFLOP/s; 8 of
+// of the copy rate; one sequence of 131501 positions with 61 nodes 191 to 205 us, 640 to 685 TFLOP/s; 8 of
 // up to 512 nodes over up to 6000 positions 332 to 341 us, 690 to 712 TFLOP/s; 40 sequences, 16 heads of
 // 64, blocks of 7: 64 us.  What bounds it is the issue of the roles' instructions and the hand-offs
 // between them (0.46 to 0.53 instructions per cycle and scheduler), with the tensor pipe at 29 %.  80

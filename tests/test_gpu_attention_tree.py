@@ -593,6 +593,26 @@ def test_cache_beyond_two_gigabytes_by_rows():
     _check(o, small)
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,nodes,ctx,bs", [
+    (1, 1, 64, 65535, None, 4), (4096, 4096, 64, [2, 1], [5, 70], 3), (128, 1, 128, [7, 0, 20], [300, 3, 65], 16),
+    (256, 2, 64, [3, 1], [130, 64], 16), (4, 2, 64, [5, 9], [300, 90], 1 << 14)])
+def test_declared_limits(Hq, Hkv, D, nodes, ctx, bs):
+    """The largest batch, thousands of kv heads, 128 query heads per kv head, and blocks and length bounds
+    far above the lengths."""
+    rng = np.random.default_rng(88)
+    if ctx is None:
+        nodes, ctx = rng.integers(0, 3, nodes).tolist(), rng.integers(0, 20, nodes).tolist()
+    d = _case(Hq, Hkv, D, nodes, ctx, bs, seed=88)
+    a = _args(d)
+    if bs == 1 << 14:
+        wide = np.full((2, (1 << 31) // bs), -1, np.int32)
+        wide[:, :d["table"].shape[1]] = d["table"]
+        a[4], a[12] = i32(wide), 2 ** 31 - 129
+    o = fq.attention_tree(*a)
+    assert fq.check_device_error() == 0
+    _check(o, d)
+
+
 def test_inputs_out_of_range():
     """A bad block id hides its positions, a context beyond the bound and too many nodes are clamped,
     offsets outside the rows too: recorded, the other sequences as ever."""

@@ -32,7 +32,7 @@
 // up to 512 nodes over up to 6000 positions 332 to 341 us, 690 to 712 TFLOP/s; 40 sequences, 16 heads of
 // 64, blocks of 7: 64 us.  What bounds it is the issue of the roles' instructions and the hand-offs
 // between them (0.46 to 0.53 instructions per cycle and scheduler), with the tensor pipe at 29 %.  80
-// registers a thread, of which heads of 128 spill 12 bytes.  The MMA warp runs converged, one lane issuing, so that its
+// registers a thread, of which heads of 128 spill 8 bytes.  The MMA warp runs converged, one lane issuing, so that its
 // operands stay in uniform registers: 128 -> 107 us on the first case.  The roles' code has to stay
 // small: at 170 KB instruction fetch was the largest stall and everything took twice as long.
 #pragma once
@@ -265,7 +265,8 @@ __device__ __forceinline__ uint64_t tree_sdesc_k(uint32_t saddr) {
 
 // Bounded wait of a warp, short in code: after `*polls` polls in vain the timeout is recorded, *polls
 // becomes 0 and the CTA's roles give up.  A poll in vain takes 4.0 us on a B200, whatever time it is
-// given, so 2^18 of them are a second.  The lanes leave it together.
+// given, so 2^18 of them are a second.  Every wait but one is for the next position tile or less; that one
+// has `rounds` times the limit.  The lanes leave it together.
 __device__ __forceinline__ bool tree_poll(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -279,13 +280,13 @@ __device__ __forceinline__ bool tree_poll(uint32_t bar, uint32_t parity) {
 }
 constexpr uint32_t kTreePolls = 1u << 18;
 __device__ __forceinline__ bool tree_wait(const uint64_t &barrier, uint32_t parity,
-                                          volatile uint32_t *polls) {
+                                          volatile uint32_t *polls, uint32_t rounds = 1) {
   const uint32_t bar = smem_u32(&barrier);
 #pragma unroll 1
   for (uint32_t n = 1;; ++n) {
     const bool ok = tree_poll(bar, parity & 1u);
     if (__all_sync(0xffffffffu, ok)) return true;
-    const bool stop = n >= *polls;
+    const bool stop = n >= *polls * rounds;
     if (__any_sync(0xffffffffu, stop)) break;
   }
   if (atomicExch(const_cast<uint32_t *>(polls), 0u) != 0) record_error(6 /* FP8Q_ERR_TIMEOUT */);
@@ -333,10 +334,11 @@ struct TreeShared {
 };
 
 // The next piece of the ring for the calling warp; false where there is none.
-__device__ __forceinline__ bool tree_take(TreeShared &sh, uint32_t ip, TreePiece &pc) {
+__device__ __forceinline__ bool tree_take(TreeShared &sh, uint32_t ip, TreePiece &pc,
+                                          uint32_t rounds = 1) {
   const uint32_t i = ip % kTreePieces;
   pc.t = pc.t_end = 0;
-  if (!tree_wait(sh.piece_full[i], ip / kTreePieces, &sh.polls)) return false;
+  if (!tree_wait(sh.piece_full[i], ip / kTreePieces, &sh.polls, rounds)) return false;
   pc = sh.piece[i];
   tree_arrive(sh.piece_free[i]);
   return pc.t_end > 0;
@@ -731,9 +733,14 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     constexpr int LPR = D / 16;                                  // 16-byte chunks per row
     const float c = a.sm_scale * a.scale3[0] * a.scale3[1];
     const uint32_t qflip = c < 0.0f ? 0x80808080u : 0u;          // a negative scale negates Q
+    // The next piece is not published before the load warp has come through this one: a wait of as many
+    // tiles (at most 2^32 polls).  Without it pieces that took longer than the limit, 40 million
+    // positions and more, were given up.
     TreePiece pc;
     bool ok = true;
-    for (uint32_t ip = 0; ok && tree_take(sh, ip, pc); ++ip) {
+    uint32_t rounds = 1;
+    for (uint32_t ip = 0; ok && tree_take(sh, ip, pc, rounds); ++ip) {
+      rounds = min(pc.t_end - pc.t + 1, (1 << 14) - 1);
       // Row r is head g G + r % G of node r / G; up to 32 (64) rows are repeated 4 (2) times down the
       // tile.  The first 256 chunks are on their way while the scores of the piece before complete,
       // the others all at once behind them.

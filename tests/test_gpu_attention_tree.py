@@ -307,6 +307,19 @@ def test_nan_values_in_long_contexts():
     assert fq.check_device_error() == 0
 
 
+def test_shares_that_outlast_the_wait_limit():
+    """Some 3000 position tiles in each CTA's share of work, a few milliseconds, under waits of 0.25 ms:
+    a role that has nothing to do until the next item must not take that for a stall."""
+    d = _shared_contexts(40, 8, 64, 64 * 3000, 2, 89)
+    a = _args(d)
+    o = fq.attention_tree(*a)
+    assert fq.check_device_error() == 0
+    for _ in range(3):
+        got = fq.selftest_attention_tree(64, *a)
+        assert fq.check_device_error() == 0
+        assert torch.equal(got, o)
+
+
 @pytest.mark.parametrize("Hq,Hkv,n,D", [(4, 2, 9, 128), (8, 1, 8, 64), (16, 1, 40, 128), (4, 4, 200, 64)])
 def test_nan_values_of_context_and_nodes_in_split_items(Hq, Hkv, n, D):
     """One long sequence split over many CTAs: NaN values of cached positions reach every row of their

@@ -409,6 +409,8 @@ def kv_cache_accept(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: t
             block_table=(block_table, i32, (B, *block_table.shape[-1:])),
             ctx_lens=(ctx_lens, i32, (B,)), cu_nodes=(cu_nodes, i32, (B + 1,)),
             path=(path, i32, (B, *path.shape[-1:])), path_lens=(path_lens, i32, (B,)))
+    if abs(k_cache.data_ptr() - v_cache.data_ptr()) < k_cache.numel():   # moved side by side
+        raise ValueError("k_cache and v_cache must not overlap")
     if out_lens is not None:
         _expect(dev, out_lens=(out_lens, i32, (B,)))
 

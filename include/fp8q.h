@@ -455,7 +455,9 @@ int fp8q_attention_tree_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int6
  * ctx + path[b][k] are copied to position ctx + k, in K and V of every layer, as if in the order of
  * k; new_lens[b] = ctx_lens[b] + path_lens[b] is the committed context of the next step.
  *   k_cache, v_cache  [layers] caches of [num_slots][row_bytes] uint8, layer_stride BYTES apart, read
- *                     and written (row_bytes = Hkv * D, a multiple of 16); 16-byte aligned
+ *                     and written (row_bytes = Hkv * D, a multiple of 16); 16-byte aligned.  The two
+ *                     must not overlap: their rows move at the same time (undefined results; the
+ *                     binding refuses it)
  *   path              [B][max_path] int32, max_path <= 1024; entries from path_lens[b] on are not read
  *   cu_nodes          [B + 1] int32: sequence b has cu_nodes[b + 1] - cu_nodes[b] nodes
  * A sequence whose path is not strictly ascending within its nodes, is longer than its nodes or

@@ -221,3 +221,16 @@ def test_selftest_attention_tree(L):
     assert call(1, D=96) == SHAPE and call(1, ws=None) == NULL and call(1, B=0) == OK
     _no_device(lambda: call(1))
     _no_device(lambda: call(1 << 18))
+
+
+def test_accept_of_overlapping_caches_is_refused_by_the_binding():
+    """Rows of K and V move at the same time: one of them would read what the other has moved."""
+    i32 = dict(dtype=torch.int32)
+    z = torch.zeros
+    ctx, cu, table = z(2, **i32), z(3, **i32), z((2, 4), **i32)
+    both = z((100, 256), dtype=torch.uint8)
+    for k, v in ((both, both), (both[:64], both[36:]), (both[36:], both[:64])):
+        with pytest.raises(ValueError, match="overlap"):
+            fq.kv_cache_accept(k, v, table, ctx, cu, z((2, 3), **i32), ctx, 16)
+    with pytest.raises(ValueError, match="CUDA"):                 # adjacent is not overlapping
+        fq.kv_cache_accept(both[:50], both[50:], table, ctx, cu, z((2, 3), **i32), ctx, 16)
